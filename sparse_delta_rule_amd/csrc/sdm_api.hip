@@ -17,6 +17,7 @@
 #include <vector>
 
 #include "../../include/sdm.h"
+#include "sdm_host.h"
 #include "sdm_kernels.h"
 
 namespace {
@@ -24,6 +25,10 @@ namespace {
 constexpr int kMaxDevices = 64;  // devices whose compute-unit count is cached
 
 thread_local std::string g_last_error;
+
+}  // namespace
+
+namespace sdm {
 
 int fail(int code, const char* fmt, ...) {
     char buf[512];
@@ -60,7 +65,7 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
 }
 
 // a * b * c fits in int64 (all non-negative).
-bool mul_fits(int64_t a, int64_t b, int64_t c = 1) {
+bool mul_fits(int64_t a, int64_t b, int64_t c) {
     const int64_t lim = INT64_MAX;
     if (a == 0 || b == 0 || c == 0) return true;
     if (a > lim / b) return false;
@@ -73,39 +78,6 @@ bool debug_validate() {
         return (e != nullptr && e[0] != '\0' && std::strcmp(e, "0") != 0) ? 1 : 0;
     }();
     return on != 0;
-}
-
-// Compute units of the current device, queried once per device.
-int device_cus(int* cus) {
-    static std::atomic<int> cache[kMaxDevices];  // 0: not queried yet
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess) return fail(SDM_E_HIP, "hipGetDevice failed: %s", hipGetErrorString(e));
-    int v = dev >= 0 && dev < kMaxDevices ? cache[dev].load(std::memory_order_relaxed) : 0;
-    if (v <= 0) {
-        e = hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev);
-        if (e != hipSuccess || v <= 0)
-            return fail(SDM_E_HIP, "cannot query the compute units of device %d: %s", dev, hipGetErrorString(e));
-        if (dev >= 0 && dev < kMaxDevices) cache[dev].store(v, std::memory_order_relaxed);
-    }
-    *cus = v;
-    return SDM_OK;
-}
-
-// SDM_STEPS_LOOP=compact|wide pins the multi-step loop; read on every call.
-int forced_loop(int* loop) {
-    const char* e = std::getenv("SDM_STEPS_LOOP");
-    *loop = -1;
-    if (e == nullptr || e[0] == '\0') return SDM_OK;
-    if (std::strcmp(e, "compact") == 0) {
-        *loop = sdm::kLoopCompact;
-        return SDM_OK;
-    }
-    if (std::strcmp(e, "wide") == 0) {
-        *loop = sdm::kLoopWide;
-        return SDM_OK;
-    }
-    return fail(SDM_E_RANGE, "SDM_STEPS_LOOP is '%s'; expected 'compact' or 'wide'", e);
 }
 
 int check_device_ptr(const void* p, const char* name) {
@@ -140,45 +112,20 @@ int fetch_slots(const void* dev, int dtype, int64_t n, std::vector<int64_t>& out
     return SDM_OK;
 }
 
-// The slot preconditions of a decode call, over all of its tokens: every slot in
-// [0, num_slots), a stream's W write slots of a token distinct, and every slot
-// touched (written or read) by one stream only, across all tokens, since the
-// tokens of different streams run in no fixed order relative to one another.
-int validate_decode_slots(int64_t num_slots, int64_t steps, int64_t streams, int W, int R, const void* k_idx,
-                          int kd, const void* q_idx, int qd, hipStream_t stream) {
-    std::vector<int64_t> k, q;
-    int rc = fetch_slots(k_idx, kd, steps * streams * W, k, stream, "k_idx");
-    if (rc != SDM_OK) return rc;
-    rc = fetch_slots(q_idx, qd, steps * streams * R, q, stream, "q_idx");
-    if (rc != SDM_OK) return rc;
-    std::unordered_map<int64_t, int64_t> owner;
-    owner.reserve(size_t(streams) * size_t(W + R));
-    for (int64_t t = 0; t < steps; ++t) {
-        for (int64_t s = 0; s < streams; ++s) {
-            const int64_t* ks = k.data() + (t * streams + s) * W;
-            const int64_t* qs = q.data() + (t * streams + s) * R;
-            for (int w = 0; w < W; ++w) {
-                if (ks[w] < 0 || ks[w] >= num_slots)
-                    return fail(SDM_E_RANGE, "token %lld: k_idx[%lld, %d] = %lld outside [0, %lld)", (long long)t,
-                                (long long)s, w, (long long)ks[w], (long long)num_slots);
-                for (int u = 0; u < w; ++u)
-                    if (ks[u] == ks[w])
-                        return fail(SDM_E_RANGE, "token %lld: stream %lld writes slot %lld twice", (long long)t,
-                                    (long long)s, (long long)ks[w]);
-            }
-            for (int r = 0; r < R; ++r)
-                if (qs[r] < 0 || qs[r] >= num_slots)
-                    return fail(SDM_E_RANGE, "token %lld: q_idx[%lld, %d] = %lld outside [0, %lld)", (long long)t,
-                                (long long)s, r, (long long)qs[r], (long long)num_slots);
-            for (int i = 0; i < W + R; ++i) {
-                const int64_t x = i < W ? ks[i] : qs[i - W];
-                auto it = owner.emplace(x, s);
-                if (!it.second && it.first->second != s)
-                    return fail(SDM_E_RANGE, "token %lld: slot %lld is used by streams %lld and %lld", (long long)t,
-                                (long long)x, (long long)it.first->second, (long long)s);
-            }
-        }
+// Compute units of the current device, queried once per device.
+int device_cus(int* cus) {
+    static std::atomic<int> cache[kMaxDevices];  // 0: not queried yet
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return fail(SDM_E_HIP, "hipGetDevice failed: %s", hipGetErrorString(e));
+    int v = dev >= 0 && dev < kMaxDevices ? cache[dev].load(std::memory_order_relaxed) : 0;
+    if (v <= 0) {
+        e = hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev);
+        if (e != hipSuccess || v <= 0)
+            return fail(SDM_E_HIP, "cannot query the compute units of device %d: %s", dev, hipGetErrorString(e));
+        if (dev >= 0 && dev < kMaxDevices) cache[dev].store(v, std::memory_order_relaxed);
     }
+    *cus = v;
     return SDM_OK;
 }
 
@@ -218,6 +165,70 @@ int validate_gather_slots(int64_t num_slots, int64_t rows, int64_t chunk, int64_
                 if (x < 0 || x >= num_slots)
                     return fail(SDM_E_RANGE, "%s[%lld, %d] = %lld outside [0, %lld)", op.name, (long long)i, n,
                                 (long long)x, (long long)num_slots);
+            }
+        }
+    }
+    return SDM_OK;
+}
+
+}  // namespace sdm
+
+namespace {
+
+using namespace sdm;
+
+// SDM_STEPS_LOOP=compact|wide pins the multi-step loop; read on every call.
+int forced_loop(int* loop) {
+    const char* e = std::getenv("SDM_STEPS_LOOP");
+    *loop = -1;
+    if (e == nullptr || e[0] == '\0') return SDM_OK;
+    if (std::strcmp(e, "compact") == 0) {
+        *loop = sdm::kLoopCompact;
+        return SDM_OK;
+    }
+    if (std::strcmp(e, "wide") == 0) {
+        *loop = sdm::kLoopWide;
+        return SDM_OK;
+    }
+    return fail(SDM_E_RANGE, "SDM_STEPS_LOOP is '%s'; expected 'compact' or 'wide'", e);
+}
+
+// The slot preconditions of a decode call, over all of its tokens: every slot in
+// [0, num_slots), a stream's W write slots of a token distinct, and every slot
+// touched (written or read) by one stream only, across all tokens, since the
+// tokens of different streams run in no fixed order relative to one another.
+int validate_decode_slots(int64_t num_slots, int64_t steps, int64_t streams, int W, int R, const void* k_idx,
+                          int kd, const void* q_idx, int qd, hipStream_t stream) {
+    std::vector<int64_t> k, q;
+    int rc = fetch_slots(k_idx, kd, steps * streams * W, k, stream, "k_idx");
+    if (rc != SDM_OK) return rc;
+    rc = fetch_slots(q_idx, qd, steps * streams * R, q, stream, "q_idx");
+    if (rc != SDM_OK) return rc;
+    std::unordered_map<int64_t, int64_t> owner;
+    owner.reserve(size_t(streams) * size_t(W + R));
+    for (int64_t t = 0; t < steps; ++t) {
+        for (int64_t s = 0; s < streams; ++s) {
+            const int64_t* ks = k.data() + (t * streams + s) * W;
+            const int64_t* qs = q.data() + (t * streams + s) * R;
+            for (int w = 0; w < W; ++w) {
+                if (ks[w] < 0 || ks[w] >= num_slots)
+                    return fail(SDM_E_RANGE, "token %lld: k_idx[%lld, %d] = %lld outside [0, %lld)", (long long)t,
+                                (long long)s, w, (long long)ks[w], (long long)num_slots);
+                for (int u = 0; u < w; ++u)
+                    if (ks[u] == ks[w])
+                        return fail(SDM_E_RANGE, "token %lld: stream %lld writes slot %lld twice", (long long)t,
+                                    (long long)s, (long long)ks[w]);
+            }
+            for (int r = 0; r < R; ++r)
+                if (qs[r] < 0 || qs[r] >= num_slots)
+                    return fail(SDM_E_RANGE, "token %lld: q_idx[%lld, %d] = %lld outside [0, %lld)", (long long)t,
+                                (long long)s, r, (long long)qs[r], (long long)num_slots);
+            for (int i = 0; i < W + R; ++i) {
+                const int64_t x = i < W ? ks[i] : qs[i - W];
+                auto it = owner.emplace(x, s);
+                if (!it.second && it.first->second != s)
+                    return fail(SDM_E_RANGE, "token %lld: slot %lld is used by streams %lld and %lld", (long long)t,
+                                (long long)x, (long long)it.first->second, (long long)s);
             }
         }
     }
