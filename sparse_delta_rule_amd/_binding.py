@@ -73,6 +73,20 @@ def library() -> ctypes.CDLL:
     lib.sdm_abi_version.restype = ctypes.c_int
     lib.sdm_round_bf16.argtypes = [P, P, i64, P]
     lib.sdm_round_bf16.restype = ctypes.c_int
+    f32 = ctypes.c_float
+    lib.sdm_route.argtypes = [P, i32, i64, i64, i32, i32, P, i32, i32, i32, i32, f32, i64, i64, P, i32, P, i32, P]
+    lib.sdm_route.restype = ctypes.c_int
+    lib.sdm_route_backward.argtypes = [P, i32, i64, i64, i32, i32, P, i32, f32, i64, i64, P, i32, P, i32, P, P]
+    lib.sdm_route_backward.restype = ctypes.c_int
+    lib.sdm_bank_pack.argtypes = [P, P, i32, i64, i64, P, i32, i64, i64, P, P, i32, P]
+    lib.sdm_bank_pack.restype = ctypes.c_int
+    lib.sdm_gather_packed.argtypes = [P, P, i32, i64, i64, i64, i64, i64, P, i32, i32, P, P, i32, P, P, P, i32, P, P]
+    lib.sdm_gather_packed.restype = ctypes.c_int
+    lib.sdm_gather_weight_grad.argtypes = lib.sdm_gather_packed.argtypes
+    lib.sdm_gather_weight_grad.restype = ctypes.c_int
+    for fn in (lib.sdm_packed_row_bytes, lib.sdm_packed_scale_bytes):
+        fn.argtypes = [i32, i64]
+        fn.restype = i64
     _lib = lib
     return lib
 

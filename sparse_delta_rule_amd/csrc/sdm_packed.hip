@@ -1,0 +1,385 @@
+// Packed banks (include/sdm_memory.h): sdm_bank_pack, sdm_gather_packed and
+// sdm_gather_weight_grad.
+
+#include "../../include/sdm_memory.h"
+#include "sdm_kernels.h"
+#include "sdm_memory.h"
+
+namespace sdm {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// Lane i's value of the lane that `ctrl` names within its row of 16 lanes.
+template <int ctrl> __device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), ctrl, 0xf, 0xf, true));
+}
+template <int ctrl> __device__ __forceinline__ float dpp(float v) { return __uint_as_float(dpp<ctrl>(__float_as_uint(v))); }
+constexpr int kXor1 = 0xb1, kXor2 = 0x4e;               // quad_perm [1,0,3,2] and [2,3,0,1]
+constexpr int kHalfMirror = 0x141, kMirror = 0x140;     // lane i of 8, of 16 <- lane 7 - i, 15 - i
+
+// ------------------------------------------------------------------ pack
+
+// Eight consecutive columns of a row as float32, VB bytes a load; columns at or
+// past `left` are 0.
+template <typename E, int VB> __device__ __forceinline__ void load_octet(const E* p, int left, float (&x)[8]) {
+    constexpr int VEC = VB / int(sizeof(E));
+    if (left >= 8) {
+        typename RawVec<VB>::T raw[8 / VEC];
+#pragma unroll
+        for (int i = 0; i < 8 / VEC; ++i) raw[i] = reinterpret_cast<const typename RawVec<VB>::T*>(p)[i];
+        E e[8];
+        __builtin_memcpy(e, raw, sizeof e);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = widen(e[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = i < left ? widen(p[i]) : 0.0f;
+    }
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+constexpr uint32_t kInfBits = 0x7f800000u;
+
+// The largest |x| (as bits) of four lanes' octets: of a block.
+__device__ __forceinline__ uint32_t block_max(uint32_t m) {
+    m = max(m, dpp<kXor1>(m));
+    return max(m, dpp<kXor2>(m));
+}
+
+// A thread takes eight columns of a row, four neighbouring lanes a block of 32;
+// a row's threads are neighbours.
+template <typename E, int VB, bool MX4>
+__global__ __launch_bounds__(kThreads) void pack_kernel(PackParams p) {
+    const int blocks = (p.hd + SDM_PACK_BLOCK - 1) / SDM_PACK_BLOCK;
+    const int per_row = min(4 * blocks, kThreads);  // threads of a row
+    const int rows = kThreads / per_row;            // rows of a workgroup
+    const int r = int(threadIdx.x) / per_row, o0 = int(threadIdx.x) % per_row;
+    if (r >= rows) return;
+    const int64_t stride = int64_t(gridDim.x) * rows;
+    for (int64_t i = int64_t(blockIdx.x) * rows + r; i < p.n; i += stride) {
+        const int64_t src = p.row_idx != nullptr ? slot_at(p.row_idx, i, p.idx64 ? 8 : 4) : i;
+        const int64_t dst = p.slots != nullptr ? slot_at(p.slots, i, p.idx64 ? 8 : 4) : i;
+        if (src < 0 || src >= p.num_rows || dst < 0 || dst >= p.num_slots) continue;
+        const E* row = static_cast<const E*>(p.rows) + src * p.hd;
+        uint8_t* codes = p.codes + dst * p.row_bytes;
+        uint8_t* scales = p.scales + dst * p.scale_bytes;
+        for (int o = o0; o < 4 * blocks; o += per_row) {
+            float x[8];
+            load_octet<E, VB>(row + 8 * o, p.hd - 8 * o, x);
+            uint32_t m = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m = max(m, abs_bits(x[j]));
+            m = block_max(m);
+            uint32_t bad = 0;  // bit j: element j is not finite
+            if (m >= kInfBits) {
+                m = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (abs_bits(x[j]) >= kInfBits) {
+                        bad |= 1u << j;
+                        x[j] = 0;
+                    }
+                    m = max(m, abs_bits(x[j]));
+                }
+                m = block_max(m);
+            }
+            // The least e with m <= 448 2^e (6 2^e), as e + 127, from m's own exponent.
+            uint32_t scale = MX4 ? (m >> 23) + ((m & 0x7fffffu) > 0x400000u) : (m >> 23) + ((m & 0x7fffffu) > 0x600000u);
+            constexpr uint32_t kTop = MX4 ? 2 : 8;
+            scale = scale > kTop ? scale - kTop : 0;
+            const float s = __uint_as_float(scale << 23);  // the conversions read the exponent field alone
+            if constexpr (MX4) {
+                uint32_t any = bad;
+                any |= dpp<kXor1>(any);
+                any |= dpp<kXor2>(any);
+                uint32_t c = 0;
+                c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[0], x[1], s, 0);
+                c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[2], x[3], s, 1);
+                c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[4], x[5], s, 2);
+                c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, x[6], x[7], s, 3);
+                if (any != 0) {
+                    c = 0;
+                    scale = 255;
+                }
+                if (4 * o < p.row_bytes) *reinterpret_cast<uint32_t*>(codes + 4 * o) = c;
+            } else {
+                typedef short Short2 __attribute__((ext_vector_type(2)));
+                uint32_t c[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    Short2 v = {0, 0};
+                    v = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(v, x[4 * h], x[4 * h + 1], s, false);
+                    v = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(v, x[4 * h + 2], x[4 * h + 3], s, true);
+                    __builtin_memcpy(&c[h], &v, 4);
+                }
+                if (bad != 0) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (bad >> j & 1) c[j / 4] |= 0x7fu << (8 * (j % 4));
+                }
+                if (8 * o < p.row_bytes) *reinterpret_cast<uint2*>(codes + 8 * o) = make_uint2(c[0], c[1]);
+            }
+            if (o % 4 == 0) {
+                scales[o / 4] = uint8_t(scale);
+                if (o / 4 == blocks - 1)
+                    for (int b = blocks; b < p.scale_bytes; ++b) scales[b] = 0;
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ gather
+
+// 16 columns of a packed row: their codes, and their values as float32.
+template <bool MX4> struct Codes16;
+template <> struct Codes16<false> {
+    using Raw = uint4;
+    static constexpr int kBytes = 16;
+    static __device__ __forceinline__ void values(const Raw& v, float s, float (&x)[16]) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const F32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[i], s, false);
+            const F32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[i], s, true);
+            x[4 * i] = a.x, x[4 * i + 1] = a.y, x[4 * i + 2] = b.x, x[4 * i + 3] = b.y;
+        }
+    }
+};
+template <> struct Codes16<true> {
+    using Raw = uint2;
+    static constexpr int kBytes = 8;
+    static __device__ __forceinline__ void values(const Raw& v, float s, float (&x)[16]) {
+        const uint32_t w[2] = {v.x, v.y};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const F32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], s, 0);
+            const F32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], s, 1);
+            const F32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], s, 2);
+            const F32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], s, 3);
+            float* y = x + 8 * i;
+            y[0] = a.x, y[1] = a.y, y[2] = b.x, y[3] = b.y, y[4] = c.x, y[5] = c.y, y[6] = d.x, y[7] = d.y;
+        }
+    }
+};
+
+__device__ __forceinline__ bool is_live(const MemoryGatherParams& p, int64_t t) {
+    const int64_t c = t / p.chunk;
+    const int64_t limit = p.chunk_valid != nullptr ? int64_t(p.chunk_valid[c]) : p.valid;
+    return t - c * p.chunk < limit;
+}
+
+constexpr int kFlight = 8;  // rows of a pair whose loads are in flight together
+
+// A pair (token, operand) takes `lanes` neighbouring lanes, 16 columns each.
+template <bool MX4>
+__global__ __launch_bounds__(kThreads) void gather_packed_kernel(MemoryGatherParams p, int lanes) {
+    using C = Codes16<MX4>;
+    const int per = kThreads / lanes;
+    const int64_t q = int64_t(blockIdx.x) * per + int(threadIdx.x) / lanes;
+    const int64_t t = q / p.operands;
+    const int op = int(q - t * p.operands);
+    if (t >= p.tokens) return;
+    const int c0 = 16 * (int(blockIdx.y) * lanes + int(threadIdx.x) % lanes);
+    if (c0 >= p.hd) return;
+    float acc[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+    if (is_live(p, t)) {
+        const int width = p.width[op];
+        const int idx_bytes = p.idx64 ? 8 : 4, w_bytes = p.w_bf16 ? 2 : 4;
+        const uint8_t* codes = static_cast<const uint8_t*>(p.bank) + c0 / 16 * C::kBytes;
+        const uint8_t* scales = p.scales + c0 / SDM_PACK_BLOCK;
+        for (int n0 = 0; n0 < width; n0 += kFlight) {
+            typename C::Raw raw[kFlight];
+            float s[kFlight], w[kFlight];
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u) {
+                const int64_t n = t * width + min(n0 + u, width - 1);
+                const int64_t slot = slot_at(p.idx[op], n, idx_bytes);
+                w[u] = value_at(p.w[op], n, w_bytes);
+                raw[u] = *reinterpret_cast<const typename C::Raw*>(codes + slot * p.row_bytes);
+                s[u] = __uint_as_float(uint32_t(scales[slot * p.scale_bytes]) << 23);
+            }
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u) {
+                if (n0 + u < width) {
+                    float x[16];
+                    C::values(raw[u], s[u], x);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[i] = fmaf(w[u], x[i], acc[i]);
+                }
+            }
+        }
+    }
+    float* out = p.out[op] + t * p.hd + c0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (c0 + i < p.hd) out[i] = acc[i];
+}
+
+// ------------------------------------------------------------------ weight gradient
+
+// A row's vector of a bank: of kN columns, read by one lane.
+template <int KIND, int VB> struct BankVec;
+template <int VB> struct BankVec<SDM_F32, VB> {
+    using Raw = typename RawVec<VB>::T;
+    static constexpr int kN = VB / 4;
+    static constexpr bool kPacked = false;
+    static __device__ __forceinline__ void values(const Raw& v, float, float (&x)[kN]) { __builtin_memcpy(x, &v, VB); }
+};
+template <int VB> struct BankVec<SDM_BF16, VB> {
+    using Raw = typename RawVec<VB>::T;
+    static constexpr int kN = VB / 2;
+    static constexpr bool kPacked = false;
+    static __device__ __forceinline__ void values(const Raw& v, float, float (&x)[kN]) {
+        uint16_t e[kN];
+        __builtin_memcpy(e, &v, VB);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) x[i] = widen(e[i]);
+    }
+};
+template <> struct BankVec<SDM_MX8, 16> : Codes16<false> {
+    static constexpr int kN = 16;
+    static constexpr bool kPacked = true;
+};
+template <> struct BankVec<SDM_MX4, 8> : Codes16<true> {
+    static constexpr int kN = 16;
+    static constexpr bool kPacked = true;
+};
+
+// Sum over the `lanes` (a power of two) neighbouring lanes of a pair.
+__device__ __forceinline__ float lane_sum(float v, int lanes) {
+    if (lanes > 1) v += dpp<kXor1>(v);
+    if (lanes > 2) v += dpp<kXor2>(v);
+    if (lanes > 4) v += dpp<kHalfMirror>(v);
+    if (lanes > 8) v += dpp<kMirror>(v);
+    if (lanes > 16) v += __shfl_xor(v, 16);
+    if (lanes > 32) v += __shfl_xor(v, 32);
+    return v;
+}
+
+template <int KIND, int VB>
+__global__ __launch_bounds__(kThreads) void weight_grad_kernel(MemoryGatherParams p, int lanes) {
+    using V = BankVec<KIND, VB>;
+    const int per = kThreads / lanes;
+    const int lane = int(threadIdx.x) % lanes;
+    const int64_t q = int64_t(blockIdx.x) * per + int(threadIdx.x) / lanes;
+    const int64_t t = q / p.operands;
+    const int op = int(q - t * p.operands);
+    if (t >= p.tokens) return;
+    const int width = p.width[op];
+    const int idx_bytes = p.idx64 ? 8 : 4;
+    const bool live = is_live(p, t);
+    const int vecs = (p.hd + V::kN - 1) / V::kN;
+    for (int n0 = 0; n0 < width; n0 += kFlight) {
+        float sum[kFlight];
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) sum[u] = 0.0f;
+        if (live) {
+            int64_t slot[kFlight];
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u) slot[u] = slot_at(p.idx[op], t * width + min(n0 + u, width - 1), idx_bytes);
+            for (int v = lane; v < vecs; v += lanes) {
+                const int c0 = v * V::kN;
+                float g[V::kN];
+#pragma unroll
+                for (int i = 0; i < V::kN; ++i) g[i] = c0 + i < p.hd ? p.dout[op][t * p.hd + c0 + i] : 0.0f;
+                typename V::Raw raw[kFlight];
+                float s[kFlight];
+#pragma unroll
+                for (int u = 0; u < kFlight; ++u) {
+                    raw[u] = *reinterpret_cast<const typename V::Raw*>(static_cast<const char*>(p.bank) +
+                                                                       slot[u] * p.row_bytes + int64_t(v) * VB);
+                    if (V::kPacked)
+                        s[u] = __uint_as_float(uint32_t(p.scales[slot[u] * p.scale_bytes + c0 / SDM_PACK_BLOCK]) << 23);
+                }
+#pragma unroll
+                for (int u = 0; u < kFlight; ++u) {
+                    float x[V::kN];
+                    V::values(raw[u], s[u], x);
+#pragma unroll
+                    for (int i = 0; i < V::kN; ++i)
+                        if (!V::kPacked || c0 + i < p.hd) sum[u] = fmaf(g[i], x[i], sum[u]);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+            const float total = lane_sum(sum[u], lanes);
+            if (lane == u % lanes && n0 + u < width) {
+                const int64_t n = t * width + n0 + u;
+                if (p.w_bf16) static_cast<uint16_t*>(p.dw[op])[n] = to_bf16_rne(total);
+                else static_cast<float*>(p.dw[op])[n] = total;
+            }
+        }
+    }
+}
+
+int pow2_lanes(int64_t vecs) {
+    int lanes = 1;
+    while (lanes < vecs && lanes < 64) lanes *= 2;
+    return lanes;
+}
+
+template <int KIND, int VB> void run_weight_grad(const MemoryGatherParams& p, hipStream_t stream) {
+    using V = BankVec<KIND, VB>;
+    const int lanes = pow2_lanes((p.hd + V::kN - 1) / V::kN);
+    const int64_t per = kThreads / lanes, blocks = (p.tokens * p.operands + per - 1) / per;
+    hipLaunchKernelGGL((weight_grad_kernel<KIND, VB>), dim3(unsigned(blocks)), dim3(kThreads), 0, stream, p, lanes);
+}
+
+template <typename E, int VB> void run_pack(const PackParams& p, bool mx4, hipStream_t stream) {
+    const int blocks = (p.hd + SDM_PACK_BLOCK - 1) / SDM_PACK_BLOCK;
+    const int rows = kThreads / (4 * blocks < kThreads ? 4 * blocks : kThreads);
+    int64_t grid = (p.n + rows - 1) / rows;
+    if (grid > (1 << 20)) grid = 1 << 20;
+    if (mx4) hipLaunchKernelGGL((pack_kernel<E, VB, true>), dim3(unsigned(grid)), dim3(kThreads), 0, stream, p);
+    else hipLaunchKernelGGL((pack_kernel<E, VB, false>), dim3(unsigned(grid)), dim3(kThreads), 0, stream, p);
+}
+
+}  // namespace
+
+hipError_t launch_pack(const PackParams& p, bool bf16, bool mx4, hipStream_t stream) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p.rows) | uintptr_t(p.hd) * (bf16 ? 2 : 4);
+    const int vb = at % 16 == 0 ? 16 : at % 8 == 0 ? 8 : at % 4 == 0 ? 4 : 2;
+    if (bf16) {
+        if (vb == 16) run_pack<uint16_t, 16>(p, mx4, stream);
+        else if (vb == 8) run_pack<uint16_t, 8>(p, mx4, stream);
+        else if (vb == 4) run_pack<uint16_t, 4>(p, mx4, stream);
+        else run_pack<uint16_t, 2>(p, mx4, stream);
+    } else {
+        if (vb == 16) run_pack<float, 16>(p, mx4, stream);
+        else if (vb == 8) run_pack<float, 8>(p, mx4, stream);
+        else run_pack<float, 4>(p, mx4, stream);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_gather_packed(const MemoryGatherParams& p, bool mx4, hipStream_t stream) {
+    const int lanes = pow2_lanes((p.hd + 15) / 16);
+    const int64_t per = kThreads / lanes, blocks = (p.tokens * p.operands + per - 1) / per;
+    const int slices = (p.hd + 16 * lanes - 1) / (16 * lanes);
+    const dim3 grid{unsigned(blocks), unsigned(slices)}, block{unsigned(kThreads)};
+    if (mx4) hipLaunchKernelGGL(gather_packed_kernel<true>, grid, block, 0, stream, p, lanes);
+    else hipLaunchKernelGGL(gather_packed_kernel<false>, grid, block, 0, stream, p, lanes);
+    return hipGetLastError();
+}
+
+hipError_t launch_weight_grad(const MemoryGatherParams& p, int bank_dtype, hipStream_t stream) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p.bank) | uintptr_t(p.row_bytes);
+    const int vb = at % 16 == 0 ? 16 : at % 8 == 0 ? 8 : at % 4 == 0 ? 4 : 2;
+    if (bank_dtype == SDM_MX8) run_weight_grad<SDM_MX8, 16>(p, stream);
+    else if (bank_dtype == SDM_MX4) run_weight_grad<SDM_MX4, 8>(p, stream);
+    else if (bank_dtype == SDM_F32 && vb == 16) run_weight_grad<SDM_F32, 16>(p, stream);
+    else if (bank_dtype == SDM_F32 && vb == 8) run_weight_grad<SDM_F32, 8>(p, stream);
+    else if (bank_dtype == SDM_F32) run_weight_grad<SDM_F32, 4>(p, stream);
+    else if (vb == 16) run_weight_grad<SDM_BF16, 16>(p, stream);
+    else if (vb == 8) run_weight_grad<SDM_BF16, 8>(p, stream);
+    else if (vb == 4) run_weight_grad<SDM_BF16, 4>(p, stream);
+    else run_weight_grad<SDM_BF16, 2>(p, stream);
+    return hipGetLastError();
+}
+
+}  // namespace sdm
