@@ -27,6 +27,7 @@ extern "C" {
 #endif
 
 #define SDM_MAX_KEYS 65536  /* most keys of a route */
+#define SDM_MAX_ROUTE_TOKENS (1LL << 25) /* most tokens of a route */
 #define SDM_MAX_GROUPS 256  /* most groups of a route */
 #define SDM_PACK_BLOCK 32   /* columns of a packed row that share a scale */
 
@@ -82,7 +83,7 @@ int64_t sdm_packed_scale_bytes(int packed_dtype, int64_t head_dim);
  *
  * Arguments:
  *   logits      [tokens, keys] of logit_dtype (SDM_F32 or SDM_BF16).
- *   tokens      >= 0; 0 enqueues nothing. keys in 1..SDM_MAX_KEYS.
+ *   tokens      0..SDM_MAX_ROUTE_TOKENS; 0 enqueues nothing. keys 1..SDM_MAX_KEYS.
  *   k           1..SDM_MAX_WIDTH, at most kept_groups * keys / groups.
  *   score       SDM_SOFTMAX or SDM_SIGMOID.
  *   bias        NULL, or [keys] float32.

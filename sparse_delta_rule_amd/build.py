@@ -14,6 +14,7 @@ import glob
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -63,16 +64,29 @@ def build_example(verbose: bool = False) -> str:
     return EXAMPLE
 
 
-def _hipcc(out: str, srcs: list, verbose: bool) -> str:
-    hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-    tmp = out + ".tmp"
-    cmd = [hipcc, *FLAGS, "-I", os.path.join(ROOT, "include"), "-o", tmp, *srcs]
+def _run_hipcc(args: list, out: str, verbose: bool) -> None:
+    cmd = [os.environ.get("HIPCC", "/opt/rocm/bin/hipcc"), *args]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError(f"hipcc failed ({r.returncode}) building {out}")
+
+
+def _hipcc(out: str, srcs: list, verbose: bool) -> str:
+    """Each source to an object, several at a time, then the objects to the library."""
+    objects = [os.path.splitext(s)[0] + ".o" for s in srcs]
+    compile_flags = [f for f in FLAGS if f != "-shared"]
+    with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as pool:
+        done = [pool.submit(_run_hipcc, [*compile_flags, "-I", os.path.join(ROOT, "include"), "-c", "-o", o, s], o, verbose)
+                for s, o in zip(srcs, objects)]
+        for d in done:
+            d.result()
+    tmp = out + ".tmp"
+    _run_hipcc([f"--offload-arch={ARCH}", "-fPIC", "-shared", "-o", tmp, *objects], out, verbose)
+    for o in objects:
+        os.remove(o)
     os.replace(tmp, out)
     return out
 

@@ -67,6 +67,8 @@ int check_route(const char* fn, int logit_dtype, int64_t tokens, int64_t keys, i
     if (!is_value(w_dtype))
         return fail(SDM_E_DTYPE, "%s: weights must be float32 or bfloat16 (dtype %d)", fn, w_dtype);
     if (tokens < 0) return fail(SDM_E_SHAPE, "%s: tokens = %lld < 0", fn, (i64)tokens);
+    if (tokens > SDM_MAX_ROUTE_TOKENS)
+        return fail(SDM_E_SHAPE, "%s: at most 2^25 tokens per call, got %lld", fn, (i64)tokens);
     if (keys < 1 || keys > SDM_MAX_KEYS)
         return fail(SDM_E_RANGE, "%s: keys must be in 1..%d, got %lld", fn, SDM_MAX_KEYS, (i64)keys);
     if (k < 1 || k > SDM_MAX_WIDTH || k > choice)
@@ -78,7 +80,7 @@ int check_route(const char* fn, int logit_dtype, int64_t tokens, int64_t keys, i
     if (streams < 1 || stream_slots < 0)
         return fail(SDM_E_SHAPE, "%s: streams = %lld, stream_slots = %lld: at least 1 and 0 are needed", fn,
                     (i64)streams, (i64)stream_slots);
-    if (!mul_fits(tokens, SDM_MAX_KEYS, 8) || !mul_fits(streams, stream_slots))
+    if (!mul_fits(streams, stream_slots))
         return fail(SDM_E_SHAPE, "%s: sizes overflow 64-bit byte counts", fn);
     const int64_t used = tokens < streams ? (tokens > 0 ? tokens : 1) : streams;  // streams that occur
     const int64_t last = (used - 1) * stream_slots;

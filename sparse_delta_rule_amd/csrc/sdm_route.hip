@@ -15,13 +15,41 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int64_t kMaxBlocks = 1 << 20;  // a grid's workgroups; more tokens are looped over
 
+// The larger and the smaller of two that are not NaN, without the moves that a NaN would need.
+__device__ __forceinline__ float max32(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, INFINITY); }
+__device__ __forceinline__ float min32(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, -INFINITY); }
 // A logit as the definition reads it: NaN counts as -inf, +inf as the largest float32.
-__device__ __forceinline__ float clean(float x) { return x != x ? -INFINITY : fminf(x, FLT_MAX); }
+__device__ __forceinline__ float clean(float x) { return min32(x != x ? -INFINITY : x, FLT_MAX); }
 template <typename E> __device__ __forceinline__ float logit_at(const E* row, int64_t i) { return clean(widen(row[i])); }
 
 __device__ __forceinline__ bool bias_excludes(float b) { return !(b > -INFINITY); }
 
 __device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
+// Within 2^-22 of its value: the hardware's base-2 exponential and reciprocal.
+__device__ __forceinline__ float exp32(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+__device__ __forceinline__ float sigmoid32(float x) { return __builtin_amdgcn_rcpf(1.0f + exp32(-x)); }
+
+// float32 as an unsigned integer of the same order (-0 as +0), and back.
+__device__ __forceinline__ uint32_t ordered(float x) {
+    const uint32_t u = __float_as_uint(x + 0.0f);
+    return u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_ordered(uint32_t u) {
+    return __uint_as_float(u ^ (~uint32_t(int32_t(u) >> 31) | 0x80000000u));
+}
+constexpr uint32_t kOut = 0x007fffffu;  // ordered(-inf): a key that is not eligible
+constexpr uint32_t kAbsent = 0;         // a key that cannot be chosen at all
+
+__device__ __forceinline__ void store_choice(const RouteParams& p, int64_t t, int j, int key, double u) {
+    const int64_t o = t * p.k + j, slot = (t % p.streams) * p.stream_slots + key;
+    if (p.idx64) static_cast<int64_t*>(p.idx)[o] = slot;
+    else static_cast<int32_t*>(p.idx)[o] = int32_t(slot);
+    const float w = float(p.scale * u);
+    if (p.w_bf16) static_cast<uint16_t*>(p.w)[o] = to_bf16_rne(w);
+    else static_cast<float*>(p.w)[o] = w;
+}
+
+// ------------------------------------------------------------------ any row, exactly
 
 // A key's rank among the keys of its row: the larger value first, then the lower key.
 struct Ranked {
@@ -32,102 +60,376 @@ __device__ __forceinline__ bool before(const Ranked& a, const Ranked& b) {
     return a.c > b.c || (a.c == b.c && a.key < b.key);
 }
 
-template <typename T, typename F> __device__ __forceinline__ T block_reduce(T v, T* lds, F f) {
+template <int THREADS, typename T, typename F> __device__ __forceinline__ T block_reduce(T v, T* lds, F f) {
     __syncthreads();
     lds[threadIdx.x] = v;
     __syncthreads();
-    for (int n = kThreads / 2; n > 0; n /= 2) {
+    for (int n = THREADS / 2; n > 0; n /= 2) {
         if (int(threadIdx.x) < n) lds[threadIdx.x] = f(lds[threadIdx.x], lds[threadIdx.x + n]);
         __syncthreads();
     }
     return lds[0];
 }
 
-// One workgroup per token; every value in float64, k rounds of a reduction over
-// the keys that come after the last one chosen.
-template <typename E>
-__global__ __launch_bounds__(kThreads) void route_kernel(RouteParams p) {
-    __shared__ Ranked red[kThreads];
-    __shared__ double redd[kThreads];
-    __shared__ double worth[SDM_MAX_GROUPS];
-    __shared__ uint8_t kept[SDM_MAX_GROUPS];
-    __shared__ int chosen[SDM_MAX_WIDTH];
-    const int tid = threadIdx.x;
-    for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
-        const E* row = static_cast<const E*>(p.logits) + t * p.keys;
+template <int THREADS> struct ExactLds {
+    union {
+        Ranked ranked[THREADS];
+        double value[THREADS];
+    };
+    double worth[SDM_MAX_GROUPS];
+    uint8_t kept[SDM_MAX_GROUPS];
+    int chosen[SDM_MAX_WIDTH];
+};
 
-        double m = 0, z = 1;
-        if (p.score == SDM_SOFTMAX) {
-            double v = -INFINITY;
-            for (int i = tid; i < p.keys; i += kThreads) v = fmax(v, double(logit_at(row, i)));
-            m = fmax(block_reduce(v, redd, [](double a, double b) { return fmax(a, b); }), -double(FLT_MAX));
-            v = 0;
-            for (int i = tid; i < p.keys; i += kThreads) v += exp(double(logit_at(row, i)) - m);
-            z = block_reduce(v, redd, [](double a, double b) { return a + b; });
-        }
-        auto eligible = [&](int i) {
-            return logit_at(row, i) > -INFINITY && !(p.bias != nullptr && bias_excludes(p.bias[i]));
-        };
-        auto score = [&](int i) {
-            const double x = logit_at(row, i);
-            return p.score == SDM_SOFTMAX ? (z > 0 ? exp(x - m) / z : 0.0) : sigmoid64(x);
-        };
-        const int size = p.keys / p.groups;
-        if (p.groups > 1) {
-            for (int g = tid; g < p.groups; g += kThreads) {
-                double a = -INFINITY, b = -INFINITY;  // the two largest
-                for (int i = g * size; i < (g + 1) * size; ++i) {
-                    if (!eligible(i)) continue;
-                    const double c = score(i) + (p.bias != nullptr ? double(p.bias[i]) : 0.0);
-                    b = fmax(b, fmin(a, c));
-                    a = fmax(a, c);
-                }
-                worth[g] = p.top == 2 && b > -INFINITY ? a + b : a;
+// One row by one workgroup, every value in float64: k rounds of a reduction over
+// the keys that come after the last one chosen. The kernels below use it for the
+// rows whose order float32 cannot tell.
+template <typename E, int THREADS>
+__device__ __noinline__ void exact_row(RouteParams p, int64_t t, ExactLds<THREADS>& lds) {
+    const int tid = threadIdx.x;
+    const E* row = static_cast<const E*>(p.logits) + t * p.keys;
+    const auto larger = [](double a, double b) { return fmax(a, b); };
+    const auto plus = [](double a, double b) { return a + b; };
+
+    double m = 0, z = 1;
+    if (p.score == SDM_SOFTMAX) {
+        double v = -INFINITY;
+        for (int i = tid; i < p.keys; i += THREADS) v = fmax(v, double(logit_at(row, i)));
+        m = fmax(block_reduce<THREADS>(v, lds.value, larger), -double(FLT_MAX));
+        v = 0;
+        for (int i = tid; i < p.keys; i += THREADS) v += exp(double(logit_at(row, i)) - m);
+        z = block_reduce<THREADS>(v, lds.value, plus);
+    }
+    auto eligible = [&](int i) {
+        return logit_at(row, i) > -INFINITY && !(p.bias != nullptr && bias_excludes(p.bias[i]));
+    };
+    auto score = [&](int i) {
+        const double x = logit_at(row, i);
+        return p.score == SDM_SOFTMAX ? (z > 0 ? exp(x - m) / z : 0.0) : sigmoid64(x);
+    };
+    const int size = p.keys / p.groups;
+    if (p.groups > 1) {
+        for (int g = tid; g < p.groups; g += THREADS) {
+            double a = -INFINITY, b = -INFINITY;  // the two largest
+            for (int i = g * size; i < (g + 1) * size; ++i) {
+                if (!eligible(i)) continue;
+                const double c = score(i) + (p.bias != nullptr ? double(p.bias[i]) : 0.0);
+                b = fmax(b, fmin(a, c));
+                a = fmax(a, c);
             }
-            __syncthreads();
-            for (int g = tid; g < p.groups; g += kThreads) {
-                int rank = 0;
-                for (int h = 0; h < p.groups; ++h) rank += worth[h] > worth[g] || (worth[h] == worth[g] && h < g);
-                kept[g] = rank < p.kept;
-            }
-            __syncthreads();
-        }
-        Ranked last = {INFINITY, -1};
-        for (int j = 0; j < p.k; ++j) {
-            Ranked best = {-INFINITY, 0x7fffffff};
-            for (int i = tid; i < p.keys; i += kThreads) {
-                if (p.groups > 1 && !kept[i / size]) continue;
-                Ranked r = {-INFINITY, i};
-                if (eligible(i)) r.c = p.bias != nullptr ? score(i) + double(p.bias[i]) : double(logit_at(row, i));
-                if (before(last, r) && before(r, best)) best = r;
-            }
-            last = block_reduce(best, red, [](Ranked a, Ranked b) { return before(b, a) ? b : a; });
-            if (tid == 0) chosen[j] = last.key;
+            lds.worth[g] = p.top == 2 && b > -INFINITY ? a + b : a;
         }
         __syncthreads();
-        const int key = tid < p.k ? chosen[tid] : 0;
-        const bool mine = tid < p.k && eligible(key);
-        double u = 0;
-        if (p.normalise && p.score == SDM_SOFTMAX) {
-            const double x = mine ? double(logit_at(row, key)) : -INFINITY;
-            const double top = fmax(block_reduce(x, redd, [](double a, double b) { return fmax(a, b); }), -double(FLT_MAX));
-            u = exp(x - top);
-        } else if (mine) {
-            u = score(key);
+        for (int g = tid; g < p.groups; g += THREADS) {
+            int rank = 0;
+            for (int h = 0; h < p.groups; ++h)
+                rank += lds.worth[h] > lds.worth[g] || (lds.worth[h] == lds.worth[g] && h < g);
+            lds.kept[g] = rank < p.kept;
         }
-        if (p.normalise) {
-            const double total = block_reduce(u, redd, [](double a, double b) { return a + b; });
-            u = total > 0 ? u / total : 0.0;
+        __syncthreads();
+    }
+    Ranked last = {INFINITY, -1};
+    for (int j = 0; j < p.k; ++j) {
+        Ranked best = {-INFINITY, 0x7fffffff};
+        for (int i = tid; i < p.keys; i += THREADS) {
+            if (p.groups > 1 && !lds.kept[i / size]) continue;
+            Ranked r = {-INFINITY, i};
+            if (eligible(i)) r.c = p.bias != nullptr ? score(i) + double(p.bias[i]) : double(logit_at(row, i));
+            if (before(last, r) && before(r, best)) best = r;
         }
-        if (tid < p.k) {
-            const int64_t o = t * p.k + tid, slot = (t % p.streams) * p.stream_slots + key;
-            if (p.idx64) static_cast<int64_t*>(p.idx)[o] = slot;
-            else static_cast<int32_t*>(p.idx)[o] = int32_t(slot);
-            const float w = float(p.scale * u);
-            if (p.w_bf16) static_cast<uint16_t*>(p.w)[o] = to_bf16_rne(w);
-            else static_cast<float*>(p.w)[o] = w;
+        last = block_reduce<THREADS>(best, lds.ranked, [](Ranked a, Ranked b) { return before(b, a) ? b : a; });
+        if (tid == 0) lds.chosen[j] = last.key;
+    }
+    __syncthreads();
+    double top = -INFINITY, total = 0;
+    const bool relative = p.normalise && p.score == SDM_SOFTMAX;
+    if (relative) {
+        for (int j = tid; j < p.k; j += THREADS)
+            if (eligible(lds.chosen[j])) top = fmax(top, double(logit_at(row, lds.chosen[j])));
+        top = fmax(block_reduce<THREADS>(top, lds.value, larger), -double(FLT_MAX));
+    }
+    auto part = [&](int key) {
+        if (!eligible(key)) return 0.0;
+        return relative ? exp(double(logit_at(row, key)) - top) : score(key);
+    };
+    if (p.normalise) {
+        for (int j = tid; j < p.k; j += THREADS) total += part(lds.chosen[j]);
+        total = block_reduce<THREADS>(total, lds.value, plus);
+    }
+    for (int j = tid; j < p.k; j += THREADS) {
+        const double u = part(lds.chosen[j]);
+        store_choice(p, t, j, lds.chosen[j], !p.normalise ? u : total > 0 ? u / total : 0.0);
+    }
+    __syncthreads();
+}
+
+// ------------------------------------------------------------------ few keys: several rows of a wavefront
+
+// Lane i's value of the lane that `ctrl` names within its row of 16 lanes.
+template <int ctrl> __device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), ctrl, 0xf, 0xf, true));
+}
+template <int ctrl> __device__ __forceinline__ float dpp(float v) { return __uint_as_float(dpp<ctrl>(__float_as_uint(v))); }
+constexpr int kXor1 = 0xb1, kXor2 = 0x4e;            // quad_perm [1,0,3,2] and [2,3,0,1]
+constexpr int kHalfMirror = 0x141, kMirror = 0x140;  // lane i of 8, of 16 <- lane 7 - i, 15 - i
+
+// f over the LANES (16, 32 or 64) neighbouring lanes of a row, of 32-bit values.
+template <int LANES, typename T, typename F> __device__ __forceinline__ T lanes_reduce(T v, F f) {
+    auto with = [&](uint32_t other) {
+        T o;
+        __builtin_memcpy(&o, &other, 4);
+        v = f(v, o);
+    };
+    auto bits = [&] {
+        uint32_t u;
+        __builtin_memcpy(&u, &v, 4);
+        return u;
+    };
+    with(dpp<kXor1>(bits()));
+    with(dpp<kXor2>(bits()));
+    with(dpp<kHalfMirror>(bits()));
+    with(dpp<kMirror>(bits()));
+    if constexpr (LANES >= 32) with(uint32_t(__shfl_xor(int(bits()), 16)));
+    if constexpr (LANES >= 64) with(uint32_t(__shfl_xor(int(bits()), 32)));
+    return v;
+}
+
+constexpr int kSpare = 4;  // candidates beyond k
+
+// How far a float32 score + bias near c may be from its value: the scores, at most
+// 1, are within 2^-16 (a softmax's sum of 1024 terms included), the sum is rounded.
+__device__ __forceinline__ float value_slack(float c) { return 0x1p-16f + 0x1p-22f * fabsf(c); }
+
+template <int LANES> struct SmallLds {
+    double value[64], score[64];
+    int key[64];
+    float worth[64];
+    ExactLds<64> exact;
+};
+
+// One wavefront a workgroup, 64 / LANES rows of it, VPT consecutive keys a lane.
+// The keys are put in order by an integer that holds the value's leading bits and
+// the key below them, so that one maximum gives both and a round of the selection
+// is a subtraction and a maximum for each key held. kSpare candidates more than k
+// are taken that way, and put in exact order by their float64 values. Where the
+// leading bits cannot show that the candidates hold the k best, or the groups'
+// order is in doubt, the row goes to exact_row.
+template <typename E, int VPT, int LANES, bool VEC>
+__global__ __launch_bounds__(64, 5) void route_small_kernel(RouteParams p) {
+    __shared__ SmallLds<LANES> lds;
+    constexpr int kRows = 64 / LANES;
+    constexpr int kKeys = VPT * LANES;
+    constexpr int kBits = kKeys <= 64 ? 6 : kKeys <= 128 ? 7 : kKeys <= 256 ? 8 : kKeys <= 512 ? 9 : 10;
+    constexpr uint32_t kMask = (1u << kBits) - 1;
+    const int tid = threadIdx.x, l = tid % LANES, first = tid - l;
+    const bool biased = p.bias != nullptr, softmax = p.score == SDM_SOFTMAX;
+    const int size = p.keys / p.groups;
+    const int available = p.kept * size;
+    const bool exact_keys = !biased && sizeof(E) == 2;  // the leading bits are all there are
+    const int rounds = min(p.k + (exact_keys ? 0 : kSpare), available);
+    const int64_t t0 = int64_t(blockIdx.x) * kRows;
+    const int64_t t = t0 + tid / LANES;
+    const bool row_there = t < p.tokens;
+    const E* row = static_cast<const E*>(p.logits) + (row_there ? t : t0) * p.keys;
+    // Keys past the row's end repeat its last ones here and are left out below.
+    float x[VPT], b[VPT];
+    if constexpr (VEC) {
+        constexpr int kN = 16 / int(sizeof(E));
+        uint4 raw[VPT / kN];
+#pragma unroll
+        for (int i = 0; i < VPT / kN; ++i)
+            raw[i] = *reinterpret_cast<const uint4*>(row + min(l * VPT + i * kN, p.keys - kN));
+#pragma unroll
+        for (int i = 0; i < VPT / kN; ++i) {
+            E e[kN];
+            __builtin_memcpy(e, &raw[i], 16);
+#pragma unroll
+            for (int j = 0; j < kN; ++j) x[i * kN + j] = widen(e[j]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) x[i] = widen(row[min(l * VPT + i, p.keys - 1)]);
+    }
+    if (biased) {
+        if (VEC && reinterpret_cast<uintptr_t>(p.bias) % 16 == 0) {
+#pragma unroll
+            for (int i = 0; i < VPT / 4; ++i) {
+                const float4 v = *reinterpret_cast<const float4*>(p.bias + min(l * VPT + i * 4, p.keys - 4));
+                b[4 * i] = v.x, b[4 * i + 1] = v.y, b[4 * i + 2] = v.z, b[4 * i + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) b[i] = p.bias[min(l * VPT + i, p.keys - 1)];
         }
     }
+    const int held = p.keys - l * VPT;  // of this lane's keys, those that there are
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) x[i] = i < held ? clean(x[i]) : -INFINITY;
+    float m = 0, z = 1;
+    if (softmax && (biased || !p.normalise)) {
+        float v = -FLT_MAX;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) v = max32(v, x[i]);
+        m = lanes_reduce<LANES>(v, [](float a, float c) { return max32(a, c); });
+        v = 0;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) v += exp32(x[i] - m);
+        z = lanes_reduce<LANES>(v, [](float a, float c) { return a + c; });
+    }
+    // What the keys are chosen by: the value, or what has its order.
+    float c[VPT];
+    if (biased) {
+        const float inv = 1.0f / max32(z, FLT_MIN);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) c[i] = (softmax ? exp32(x[i] - m) * inv : sigmoid32(x[i])) + b[i];
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) c[i] = (x[i] > -INFINITY) & (b[i] > -INFINITY) ? c[i] : -INFINITY;
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) c[i] = x[i];
+    }
+    bool doubt = false;
+    bool mine_kept = true;
+    if (p.groups > 1) {
+        const int of_group = size / VPT;  // lanes of a group: a power of two
+        float hi = -INFINITY, lo = -INFINITY;  // the two largest
+        auto add = [&](float v) {
+            lo = __builtin_amdgcn_fmed3f(hi, lo, v);
+            hi = max32(hi, v);
+        };
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) add(c[i]);
+        auto merge = [&](float h, float w) {
+            add(h);
+            lo = max32(lo, w);  // w <= h: above hi only if h was
+        };
+        if (of_group > 1) merge(dpp<kXor1>(hi), dpp<kXor1>(lo));
+        if (of_group > 2) merge(dpp<kXor2>(hi), dpp<kXor2>(lo));
+        if (of_group > 4) merge(dpp<kHalfMirror>(hi), dpp<kHalfMirror>(lo));
+        if (of_group > 8) merge(dpp<kMirror>(hi), dpp<kMirror>(lo));
+        if (of_group > 16) merge(__shfl_xor(hi, 16), __shfl_xor(lo, 16));
+        // Without a bias and with one value a group, the order of the logits is exact.
+        const bool exact_worth = !biased && p.top == 1;
+        float worth = hi;
+        if (!exact_worth) {
+            if (!biased) {
+                float top = 0;
+                if (softmax) top = lanes_reduce<LANES>(max32(hi, -FLT_MAX), [](float a, float d) { return max32(a, d); });
+                hi = hi > -INFINITY ? (softmax ? exp32(hi - top) : sigmoid32(hi)) : hi;
+                lo = lo > -INFINITY ? (softmax ? exp32(lo - top) : sigmoid32(lo)) : lo;
+            }
+            worth = p.top == 2 && lo > -INFINITY ? hi + lo : hi;
+        }
+        const int g = l / of_group;
+        __syncthreads();
+        if (l % of_group == 0 && g < p.groups) lds.worth[first + g] = worth;
+        __syncthreads();
+        int above = 0, not_below = 0;  // groups that surely, that perhaps go before this one
+        for (int h = 0; h < p.groups; ++h) {
+            const float other = lds.worth[first + h];
+            if (h == g) continue;
+            if (exact_worth || !(fmaxf(other, worth) > -INFINITY)) {
+                const bool ahead = other > worth || (other == worth && h < g);
+                above += ahead;
+                not_below += ahead;
+            } else {
+                // Scores alone are within 2^-16 of their values relatively, above underflow.
+                const float far = biased ? 4 * value_slack(fmaxf(fabsf(other), fabsf(worth)) < INFINITY
+                                                               ? fabsf(other) + fabsf(worth) : 0.0f)
+                                         : 0x1p-15f * (other + worth) + 0x1p-120f;
+                above += other > worth + far;
+                not_below += !(other < worth - far);
+            }
+        }
+        mine_kept = not_below < p.kept;
+        if (g < p.groups) doubt = not_below >= p.kept && above < p.kept;
+    }
+    uint32_t key[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const uint32_t k = (ordered(c[i]) >> 1 & ~kMask) | (kMask - uint32_t(l * VPT + i));
+        key[i] = (i < held) & mine_kept ? k : kAbsent;
+    }
+    uint32_t last = 0x80000000u, mine = 0, at_k = 0;
+    for (int r = 0; r < rounds; ++r) {
+        uint32_t best = 0;  // of key - last: those after the last one are past 2^31
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) best = max(best, key[i] - last);
+        best = lanes_reduce<LANES>(best, [](uint32_t a, uint32_t d) { return max(a, d); });
+        last += best;
+        if (l == r) mine = last;
+        if (r == p.k - 1) at_k = last;
+    }
+    // Every key outside the candidates has leading bits of at most `last`'s.
+    if (!exact_keys && rounds < available) {
+        const uint32_t qk = at_k & ~kMask, ql = last & ~kMask;
+        if (ql != (kOut >> 1 & ~kMask)) {  // else: what is eligible is all in, the rest goes by the key
+            if (!biased) {
+                doubt |= qk == ql;
+            } else {
+                const float low_k = from_ordered(qk << 1), high_last = from_ordered((ql | kMask) << 1 | 1);
+                doubt |= !(low_k - high_last > 4 * (value_slack(low_k) + value_slack(high_last)));
+            }
+        }
+    }
+    const int n = min(int(kMask - (mine & kMask)), p.keys - 1);
+    float xn = -INFINITY, bn = 0;
+    if (l < rounds) {
+        xn = logit_at(row, n);
+        if (biased) bn = p.bias[n];
+    }
+    const bool ok = xn > -INFINITY && bn > -INFINITY;
+    double s = 0;  // the score, where something needs it
+    if (biased || !p.normalise || !softmax) {
+        if (ok) s = softmax ? exp(double(xn) - double(m)) / double(z) : sigmoid64(xn);
+    }
+    int rank = l;
+    if (!exact_keys) {
+        const double v = !ok ? -INFINITY : biased ? s + double(bn) : double(xn);
+        __syncthreads();
+        lds.value[tid] = v;
+        lds.score[tid] = s;
+        lds.key[tid] = n;
+        __syncthreads();
+        rank = 0;
+        for (int r = 0; r < rounds; ++r) {
+            const double o = lds.value[first + r];
+            rank += (o > v) | ((o == v) & (lds.key[first + r] < n));
+            // The scores of a softmax are off by 2^-16, its float32 sum, of themselves, all by the same.
+            if (softmax && biased && l < rounds && ok && o > -INFINITY) {
+                const double apart = fabs(s - lds.score[first + r]);
+                doubt |= apart > 0 && fabs(o - v) <= 0x1p-15 * apart;
+            }
+        }
+    }
+    double u = s;
+    const bool chosen = l < rounds && rank < p.k;
+    if (p.normalise) {
+        if (softmax) {
+            float top = chosen && ok ? xn : -FLT_MAX;
+            top = lanes_reduce<LANES>(top, [](float a, float d) { return fmaxf(a, d); });
+            u = ok ? exp(double(xn) - double(top)) : 0.0;
+        }
+        __syncthreads();
+        lds.value[tid] = chosen ? u : 0.0;
+        __syncthreads();
+        double total = 0;
+        for (int r = 0; r < rounds; ++r) total += lds.value[first + r];
+        u = total > 0 ? u / total : 0.0;
+    }
+    constexpr uint64_t kRow = LANES == 64 ? ~0ull : (1ull << (LANES % 64)) - 1;
+    const uint64_t in_doubt = __ballot(doubt && row_there);
+    if (chosen && row_there && !(in_doubt >> first & kRow)) store_choice(p, t, rank, n, u);
+    for (int r = 0; r < kRows; ++r)
+        if (in_doubt >> (r * LANES) & kRow) exact_row<E, 64>(p, t0 + r, lds.exact);
+}
+
+// ------------------------------------------------------------------ any row, simply
+
+template <typename E>
+__global__ __launch_bounds__(kThreads) void route_exact_kernel(RouteParams p) {
+    __shared__ ExactLds<kThreads> lds;
+    for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) exact_row<E, kThreads>(p, t, lds);
 }
 
 constexpr int kTile = 4096;  // gradients assembled in LDS at a time
@@ -149,10 +451,10 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(RouteBackwardP
         if (whole) {
             float v = -INFINITY;
             for (int i = tid; i < p.keys; i += kThreads) v = fmaxf(v, logit_at(row, i));
-            m = fmaxf(block_reduce(v, redf, [](float a, float b) { return fmaxf(a, b); }), -FLT_MAX);
+            m = fmaxf(block_reduce<kThreads>(v, redf, [](float a, float b) { return fmaxf(a, b); }), -FLT_MAX);
             v = 0;
             for (int i = tid; i < p.keys; i += kThreads) v += expf(logit_at(row, i) - m);
-            z = block_reduce(v, redf, [](float a, float b) { return a + b; });
+            z = block_reduce<kThreads>(v, redf, [](float a, float b) { return a + b; });
         }
         int64_t key = -1;
         double x = -INFINITY, dw = 0;
@@ -170,19 +472,19 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(RouteBackwardP
         if (p.score == SDM_SIGMOID) {
             if (mine) u = sigmoid64(x);
         } else if (p.normalise) {
-            const double top = fmax(block_reduce(x, redd, [](double a, double b) { return fmax(a, b); }), -double(FLT_MAX));
+            const double top = fmax(block_reduce<kThreads>(x, redd, [](double a, double b) { return fmax(a, b); }), -double(FLT_MAX));
             u = exp(x - top);
         } else if (mine) {
             u = exp(x - double(m)) / double(z);
         }
         double d = p.scale * dw;
         if (p.normalise) {
-            const double total = block_reduce(u, redd, [](double a, double b) { return a + b; });
+            const double total = block_reduce<kThreads>(u, redd, [](double a, double b) { return a + b; });
             u = total > 0 ? u / total : 0.0;
         }
         float sum = 0;
         if (p.normalise || whole) {
-            const double dot = block_reduce(d * u, redd, [](double a, double b) { return a + b; });
+            const double dot = block_reduce<kThreads>(d * u, redd, [](double a, double b) { return a + b; });
             if (whole) sum = float(dot);
             else d -= dot;
         }
@@ -210,10 +512,50 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(RouteBackwardP
 
 }  // namespace
 
-hipError_t launch_route(const RouteParams& p, bool bf16, hipStream_t stream) {
+namespace {
+
+template <typename E, int VPT, int LANES> void run_small(const RouteParams& p, bool vec, hipStream_t stream) {
+    const dim3 grid{unsigned((p.tokens + 64 / LANES - 1) / (64 / LANES))}, block{64};
+    if constexpr (VPT * sizeof(E) % 16 == 0) {
+        if (vec) {
+            hipLaunchKernelGGL((route_small_kernel<E, VPT, LANES, true>), grid, block, 0, stream, p);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((route_small_kernel<E, VPT, LANES, false>), grid, block, 0, stream, p);
+}
+
+template <typename E, int LANES> void run_small(const RouteParams& p, int vpt, bool vec, hipStream_t stream) {
+    if (vpt == 4) run_small<E, 4, LANES>(p, vec, stream);
+    else if (vpt == 8) run_small<E, 8, LANES>(p, vec, stream);
+    else run_small<E, 16, LANES>(p, vec, stream);
+}
+
+template <typename E> void run_route(const RouteParams& p, hipStream_t stream) {
+    // 16 keys a lane at most, and a lane for each candidate.
+    int lanes = 16;
+    while (lanes < 64 && (lanes * 16 < p.keys || lanes < p.k + kSpare)) lanes *= 2;
+    int vpt = 4;
+    while (vpt < 16 && lanes * vpt < p.keys) vpt *= 2;
+    const int size = p.keys / p.groups;
+    // A group is whole lanes, a power of two of them.
+    const bool groups_fit = p.groups == 1 || (size % vpt == 0 && (size / vpt & (size / vpt - 1)) == 0 && p.groups <= lanes);
+    if (lanes * vpt >= p.keys && lanes >= p.k + kSpare && groups_fit) {
+        const bool vec = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && p.keys * sizeof(E) % 16 == 0;
+        if (lanes == 16) run_small<E, 16>(p, vpt, vec, stream);
+        else if (lanes == 32) run_small<E, 32>(p, vpt, vec, stream);
+        else run_small<E, 64>(p, vpt, vec, stream);
+        return;
+    }
     const dim3 grid{unsigned(p.tokens < kMaxBlocks ? p.tokens : kMaxBlocks)}, block{unsigned(kThreads)};
-    if (bf16) hipLaunchKernelGGL(route_kernel<uint16_t>, grid, block, 0, stream, p);
-    else hipLaunchKernelGGL(route_kernel<float>, grid, block, 0, stream, p);
+    hipLaunchKernelGGL(route_exact_kernel<E>, grid, block, 0, stream, p);
+}
+
+}  // namespace
+
+hipError_t launch_route(const RouteParams& p, bool bf16, hipStream_t stream) {
+    if (bf16) run_route<uint16_t>(p, stream);
+    else run_route<float>(p, stream);
     return hipGetLastError();
 }
 

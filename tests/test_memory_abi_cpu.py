@@ -91,7 +91,7 @@ ROUTE = dict(logits=A, logit_dtype=F32, tokens=16, keys=256, k=8, score=0, bias=
     (dict(streams=0), E_SHAPE, "streams = 0"),
     (dict(stream_slots=-1), E_SHAPE, "stream_slots = -1"),
     (dict(streams=1 << 40, stream_slots=1 << 40), E_SHAPE, "overflow"),
-    (dict(tokens=1 << 60), E_SHAPE, "overflow"),
+    (dict(tokens=(1 << 25) + 1), E_SHAPE, "at most 2^25 tokens"),
     (dict(stream_slots=1 << 28, idx_dtype=I32), E_RANGE, "does not fit"),
     (dict(logits=None), E_NULL, "required"),
     (dict(idx=None), E_NULL, "required"),
