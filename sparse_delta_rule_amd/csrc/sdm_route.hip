@@ -85,7 +85,7 @@ template <int THREADS> struct ExactLds {
 // the keys that come after the last one chosen. The kernels below use it for the
 // rows whose order float32 cannot tell.
 template <typename E, int THREADS>
-__device__ __noinline__ void exact_row(RouteParams p, int64_t t, ExactLds<THREADS>& lds) {
+__device__ __forceinline__ void exact_row(const RouteParams& p, int64_t t, ExactLds<THREADS>& lds) {
     const int tid = threadIdx.x;
     const E* row = static_cast<const E*>(p.logits) + t * p.keys;
     const auto larger = [](double a, double b) { return fmax(a, b); };
@@ -196,15 +196,128 @@ template <int LANES, typename T, typename F> __device__ __forceinline__ T lanes_
 
 constexpr int kSpare = 4;  // candidates beyond k
 
-// How far a float32 score + bias near c may be from its value: the scores, at most
-// 1, are within 2^-16 (a softmax's sum of 1024 terms included), the sum is rounded.
-__device__ __forceinline__ float value_slack(float c) { return 0x1p-16f + 0x1p-22f * fabsf(c); }
+// A bound on how far a float32 score + bias near c may be from its value, at least
+// twice what its roundings come to: a sigmoid's 2^-22 (exponential, sum and
+// reciprocal), a softmax's 2^-18 (its sum of at most 1024 terms, in lanes of 16
+// and 6 levels, above all), and the rounding of the sum.
+__device__ __forceinline__ float value_slack(bool softmax, float c) {
+    return (softmax ? 0x1p-17f : 0x1p-21f) + 0x1p-23f * fabsf(c);
+}
+// And relatively, of a score's own, x from where its exponent is 0.
+__device__ __forceinline__ float score_slack(float x) { return (4.0f + fabsf(x)) * 0x1p-22f; }
+
+// One row by one wavefront, KEYS / 64 keys a lane, every value in float64.
+template <typename E, int KEYS> __device__ __forceinline__ void exact_small_row(const RouteParams& p, int64_t t) {
+    constexpr int N = KEYS / 64;
+    const int lane = threadIdx.x, size = p.keys / p.groups;
+    const E* row = static_cast<const E*>(p.logits) + t * p.keys;
+    const bool biased = p.bias != nullptr, softmax = p.score == SDM_SOFTMAX;
+    auto all = [](double v, auto f) {
+        for (int n = 1; n < 64; n *= 2) v = f(v, __shfl_xor(v, n));
+        return v;
+    };
+    const auto larger = [](double a, double b) { return fmax(a, b); };
+    const auto plus = [](double a, double b) { return a + b; };
+    double x[N], s[N], c[N];
+    uint32_t gone = 0;  // bit i: key i of the lane cannot be chosen (any more)
+    double m = -FLT_MAX, z = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int n = i * 64 + lane;
+        x[i] = n < p.keys ? double(logit_at(row, n)) : -INFINITY;
+        if (n >= p.keys) gone |= 1u << i;
+        m = fmax(m, x[i]);
+    }
+    m = all(m, larger);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        s[i] = softmax ? exp(x[i] - m) : sigmoid64(x[i]);
+        z += s[i];
+    }
+    z = all(z, plus);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int n = min(i * 64 + lane, p.keys - 1);
+        const float b = biased ? p.bias[n] : 0.0f;
+        if (softmax) s[i] = z > 0 ? s[i] / z : 0.0;
+        const bool ok = x[i] > -INFINITY && !bias_excludes(b);
+        if (!ok) x[i] = -INFINITY;
+        c[i] = !ok ? -INFINITY : biased ? s[i] + double(b) : x[i];
+    }
+    if (p.groups > 1) {
+        double mine = 0;
+        for (int g = 0; g < p.groups; ++g) {
+            double hi = -INFINITY, lo = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int n = i * 64 + lane;
+                if (n / size == g && n < p.keys && x[i] > -INFINITY) {
+                    const double v = biased ? c[i] : s[i];
+                    lo = fmax(lo, fmin(hi, v));
+                    hi = fmax(hi, v);
+                }
+            }
+            for (int n = 1; n < 64; n *= 2) {
+                const double h = __shfl_xor(hi, n), w = __shfl_xor(lo, n);
+                lo = fmax(fmax(lo, w), fmin(hi, h));
+                hi = fmax(hi, h);
+            }
+            if (lane == g) mine = p.top == 2 && lo > -INFINITY ? hi + lo : hi;
+        }
+        int rank = 0;
+        for (int g = 0; g < p.groups; ++g) {
+            const double other = __shfl(mine, g);
+            rank += other > mine || (other == mine && g < lane);
+        }
+        const uint64_t kept = __ballot(lane < p.groups && rank < p.kept);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i * 64 + lane < p.keys && !(kept >> ((i * 64 + lane) / size) & 1)) gone |= 1u << i;
+    }
+    int key = 0;
+    double xk = -INFINITY, sk = 0;  // of the lane's choice: lane j has the j-th
+    for (int j = 0; j < p.k; ++j) {
+        Ranked best = {-INFINITY, 0x7fffffff};
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const Ranked r = {c[i], i * 64 + lane};
+            if (!(gone >> i & 1) && before(r, best)) best = r;
+        }
+        for (int n = 1; n < 64; n *= 2) {
+            const Ranked o = {__shfl_xor(best.c, n), __shfl_xor(best.key, n)};
+            if (before(o, best)) best = o;
+        }
+        double xb = 0, sb = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (best.key == i * 64 + lane) {
+                gone |= 1u << i;
+                xb = x[i];
+                sb = s[i];
+            }
+        xb = __shfl(xb, best.key % 64);
+        sb = __shfl(sb, best.key % 64);
+        if (lane == j) {
+            key = best.key;
+            xk = xb;
+            sk = xb > -INFINITY ? sb : 0.0;
+        }
+    }
+    if (p.normalise) {
+        if (softmax) {
+            const double top = all(fmax(xk, -double(FLT_MAX)), larger);
+            sk = xk > -INFINITY ? exp(xk - top) : 0.0;
+        }
+        const double total = all(sk, plus);
+        sk = total > 0 ? sk / total : 0.0;
+    }
+    if (lane < p.k) store_choice(p, t, lane, key, sk);
+}
 
 template <int LANES> struct SmallLds {
     double value[64], score[64];
     int key[64];
-    float worth[64];
-    ExactLds<64> exact;
+    float worth[64], slack[64];
 };
 
 // One wavefront a workgroup, 64 / LANES rows of it, VPT consecutive keys a lane.
@@ -213,7 +326,7 @@ template <int LANES> struct SmallLds {
 // is a subtraction and a maximum for each key held. kSpare candidates more than k
 // are taken that way, and put in exact order by their float64 values. Where the
 // leading bits cannot show that the candidates hold the k best, or the groups'
-// order is in doubt, the row goes to exact_row.
+// order is in doubt, the row is done again by exact_small_row.
 template <typename E, int VPT, int LANES, bool VEC>
 __global__ __launch_bounds__(64, 5) void route_small_kernel(RouteParams p) {
     __shared__ SmallLds<LANES> lds;
@@ -310,36 +423,35 @@ __global__ __launch_bounds__(64, 5) void route_small_kernel(RouteParams p) {
         if (of_group > 16) merge(__shfl_xor(hi, 16), __shfl_xor(lo, 16));
         // Without a bias and with one value a group, the order of the logits is exact.
         const bool exact_worth = !biased && p.top == 1;
-        float worth = hi;
+        float worth = hi, slack = 0;
         if (!exact_worth) {
-            if (!biased) {
-                float top = 0;
-                if (softmax) top = lanes_reduce<LANES>(max32(hi, -FLT_MAX), [](float a, float d) { return max32(a, d); });
+            if (biased) {
+                slack = value_slack(softmax, hi) + (lo > -INFINITY ? value_slack(softmax, lo) : 0.0f);
+                if (!(slack < INFINITY)) slack = 1.0f;  // of an infinite value: equal ones are in doubt
+            } else {
+                const float top = softmax ? lanes_reduce<LANES>(max32(hi, -FLT_MAX), [](float a, float d) { return max32(a, d); }) : 0.0f;
+                slack = hi > -INFINITY ? 2 * score_slack(hi - top) : 0.0f;
+                if (lo > -INFINITY) slack = 2 * score_slack(max32(fabsf(hi - top), fabsf(lo - top)));
                 hi = hi > -INFINITY ? (softmax ? exp32(hi - top) : sigmoid32(hi)) : hi;
                 lo = lo > -INFINITY ? (softmax ? exp32(lo - top) : sigmoid32(lo)) : lo;
+                slack = slack * (max32(hi, 0.0f) + max32(lo, 0.0f)) + 0x1p-120f;  // and below that, of nothing
             }
             worth = p.top == 2 && lo > -INFINITY ? hi + lo : hi;
         }
         const int g = l / of_group;
         __syncthreads();
-        if (l % of_group == 0 && g < p.groups) lds.worth[first + g] = worth;
+        if (l % of_group == 0 && g < p.groups) {
+            lds.worth[first + g] = worth;
+            lds.slack[first + g] = slack;
+        }
         __syncthreads();
         int above = 0, not_below = 0;  // groups that surely, that perhaps go before this one
         for (int h = 0; h < p.groups; ++h) {
-            const float other = lds.worth[first + h];
-            if (h == g) continue;
-            if (exact_worth || !(fmaxf(other, worth) > -INFINITY)) {
-                const bool ahead = other > worth || (other == worth && h < g);
-                above += ahead;
-                not_below += ahead;
-            } else {
-                // Scores alone are within 2^-16 of their values relatively, above underflow.
-                const float far = biased ? 4 * value_slack(fmaxf(fabsf(other), fabsf(worth)) < INFINITY
-                                                               ? fabsf(other) + fabsf(worth) : 0.0f)
-                                         : 0x1p-15f * (other + worth) + 0x1p-120f;
-                above += other > worth + far;
-                not_below += !(other < worth - far);
-            }
+            const float other = lds.worth[first + h], far = slack + lds.slack[first + h];
+            const bool exact = exact_worth | !(max32(other, worth) > -INFINITY);
+            const bool ahead = (other > worth) | ((other == worth) & (h < g));
+            above += (h != g) & (exact ? ahead : other > worth + far);
+            not_below += (h != g) & (exact ? ahead : !(other < worth - far));
         }
         mine_kept = not_below < p.kept;
         if (g < p.groups) doubt = not_below >= p.kept && above < p.kept;
@@ -368,7 +480,7 @@ __global__ __launch_bounds__(64, 5) void route_small_kernel(RouteParams p) {
                 doubt |= qk == ql;
             } else {
                 const float low_k = from_ordered(qk << 1), high_last = from_ordered((ql | kMask) << 1 | 1);
-                doubt |= !(low_k - high_last > 4 * (value_slack(low_k) + value_slack(high_last)));
+                doubt |= !(low_k - high_last > value_slack(softmax, low_k) + value_slack(softmax, high_last));
             }
         }
     }
@@ -395,10 +507,10 @@ __global__ __launch_bounds__(64, 5) void route_small_kernel(RouteParams p) {
         for (int r = 0; r < rounds; ++r) {
             const double o = lds.value[first + r];
             rank += (o > v) | ((o == v) & (lds.key[first + r] < n));
-            // The scores of a softmax are off by 2^-16, its float32 sum, of themselves, all by the same.
+            // The scores of a softmax are off by 2^-18, its float32 sum, of themselves, all by the same.
             if (softmax && biased && l < rounds && ok && o > -INFINITY) {
                 const double apart = fabs(s - lds.score[first + r]);
-                doubt |= apart > 0 && fabs(o - v) <= 0x1p-15 * apart;
+                doubt |= apart > 0 && fabs(o - v) <= 0x1p-17 * apart;
             }
         }
     }
@@ -421,7 +533,7 @@ __global__ __launch_bounds__(64, 5) void route_small_kernel(RouteParams p) {
     const uint64_t in_doubt = __ballot(doubt && row_there);
     if (chosen && row_there && !(in_doubt >> first & kRow)) store_choice(p, t, rank, n, u);
     for (int r = 0; r < kRows; ++r)
-        if (in_doubt >> (r * LANES) & kRow) exact_row<E, 64>(p, t0 + r, lds.exact);
+        if (in_doubt >> (r * LANES) & kRow) exact_small_row<E, kKeys>(p, t0 + r);
 }
 
 // ------------------------------------------------------------------ any row, simply
