@@ -23,6 +23,7 @@ struct RouteParams {
     int idx64, w_bf16;
 };
 hipError_t launch_route(const RouteParams& p, bool bf16, hipStream_t stream);
+void launch_route_block(const RouteParams& p, bool bf16, hipStream_t stream);  // any row: a workgroup each
 
 struct RouteBackwardParams {
     const void* logits;

@@ -1,0 +1,192 @@
+// Device code that the slot router's kernels share.
+#pragma once
+
+#include <float.h>
+#include <math.h>
+
+#include "../../include/sdm_memory.h"
+#include "sdm_kernels.h"
+#include "sdm_memory.h"
+
+namespace sdm {
+
+// The larger and the smaller of two that are not NaN, without the moves that a NaN would need.
+__device__ __forceinline__ float max32(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, INFINITY); }
+__device__ __forceinline__ float min32(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, -INFINITY); }
+// A logit as the definition reads it: NaN counts as -inf, +inf as the largest float32.
+__device__ __forceinline__ float clean(float x) { return min32(x != x ? -INFINITY : x, FLT_MAX); }
+template <typename E> __device__ __forceinline__ float logit_at(const E* row, int64_t i) { return clean(widen(row[i])); }
+
+__device__ __forceinline__ bool bias_excludes(float b) { return !(b > -INFINITY); }
+
+__device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
+// Within 2^-22 of its value: the hardware's base-2 exponential and reciprocal.
+__device__ __forceinline__ float exp32(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+__device__ __forceinline__ float sigmoid32(float x) { return __builtin_amdgcn_rcpf(1.0f + exp32(-x)); }
+
+// float32 as an unsigned integer of the same order (-0 as +0), and back.
+__device__ __forceinline__ uint32_t ordered(float x) {
+    const uint32_t u = __float_as_uint(x + 0.0f);
+    return u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_ordered(uint32_t u) {
+    return __uint_as_float(u ^ (~uint32_t(int32_t(u) >> 31) | 0x80000000u));
+}
+constexpr uint32_t kOut = 0x007fffffu;  // ordered(-inf): a key that is not eligible
+constexpr uint32_t kAbsent = 0;         // a key that cannot be chosen at all
+
+__device__ __forceinline__ void store_choice(const RouteParams& p, int64_t t, int j, int key, double u) {
+    const int64_t o = t * p.k + j, slot = (t % p.streams) * p.stream_slots + key;
+    if (p.idx64) static_cast<int64_t*>(p.idx)[o] = slot;
+    else static_cast<int32_t*>(p.idx)[o] = int32_t(slot);
+    const float w = float(p.scale * u);
+    if (p.w_bf16) static_cast<uint16_t*>(p.w)[o] = to_bf16_rne(w);
+    else static_cast<float*>(p.w)[o] = w;
+}
+
+// ------------------------------------------------------------------ any row, exactly
+
+// A key's rank among the keys of its row: the larger value first, then the lower key.
+struct Ranked {
+    double c;
+    int key;
+};
+__device__ __forceinline__ bool before(const Ranked& a, const Ranked& b) {
+    return a.c > b.c || (a.c == b.c && a.key < b.key);
+}
+
+template <int THREADS, typename T, typename F> __device__ __forceinline__ T block_reduce(T v, T* lds, F f) {
+    __syncthreads();
+    lds[threadIdx.x] = v;
+    __syncthreads();
+    for (int n = THREADS / 2; n > 0; n /= 2) {
+        if (int(threadIdx.x) < n) lds[threadIdx.x] = f(lds[threadIdx.x], lds[threadIdx.x + n]);
+        __syncthreads();
+    }
+    return lds[0];
+}
+
+template <int THREADS> struct ExactLds {
+    union {
+        Ranked ranked[THREADS];
+        double value[THREADS];
+    };
+    double worth[SDM_MAX_GROUPS];
+    uint8_t kept[SDM_MAX_GROUPS];
+    int chosen[SDM_MAX_WIDTH];
+};
+
+// One row by one workgroup, every value in float64: k rounds of a reduction over
+// the keys that come after the last one chosen. The kernels below use it for the
+// rows whose order float32 cannot tell.
+template <typename E, int THREADS>
+__device__ __forceinline__ void exact_row(const RouteParams& p, int64_t t, ExactLds<THREADS>& lds) {
+    const int tid = threadIdx.x;
+    const E* row = static_cast<const E*>(p.logits) + t * p.keys;
+    const auto larger = [](double a, double b) { return fmax(a, b); };
+    const auto plus = [](double a, double b) { return a + b; };
+
+    double m = 0, z = 1;
+    if (p.score == SDM_SOFTMAX) {
+        double v = -INFINITY;
+        for (int i = tid; i < p.keys; i += THREADS) v = fmax(v, double(logit_at(row, i)));
+        m = fmax(block_reduce<THREADS>(v, lds.value, larger), -double(FLT_MAX));
+        v = 0;
+        for (int i = tid; i < p.keys; i += THREADS) v += exp(double(logit_at(row, i)) - m);
+        z = block_reduce<THREADS>(v, lds.value, plus);
+    }
+    auto eligible = [&](int i) {
+        return logit_at(row, i) > -INFINITY && !(p.bias != nullptr && bias_excludes(p.bias[i]));
+    };
+    auto score = [&](int i) {
+        const double x = logit_at(row, i);
+        return p.score == SDM_SOFTMAX ? (z > 0 ? exp(x - m) / z : 0.0) : sigmoid64(x);
+    };
+    const int size = p.keys / p.groups;
+    if (p.groups > 1) {
+        for (int g = tid; g < p.groups; g += THREADS) {
+            double a = -INFINITY, b = -INFINITY;  // the two largest
+            for (int i = g * size; i < (g + 1) * size; ++i) {
+                if (!eligible(i)) continue;
+                const double c = score(i) + (p.bias != nullptr ? double(p.bias[i]) : 0.0);
+                b = fmax(b, fmin(a, c));
+                a = fmax(a, c);
+            }
+            lds.worth[g] = p.top == 2 && b > -INFINITY ? a + b : a;
+        }
+        __syncthreads();
+        for (int g = tid; g < p.groups; g += THREADS) {
+            int rank = 0;
+            for (int h = 0; h < p.groups; ++h)
+                rank += lds.worth[h] > lds.worth[g] || (lds.worth[h] == lds.worth[g] && h < g);
+            lds.kept[g] = rank < p.kept;
+        }
+        __syncthreads();
+    }
+    Ranked last = {INFINITY, -1};
+    for (int j = 0; j < p.k; ++j) {
+        Ranked best = {-INFINITY, 0x7fffffff};
+        for (int i = tid; i < p.keys; i += THREADS) {
+            if (p.groups > 1 && !lds.kept[i / size]) continue;
+            Ranked r = {-INFINITY, i};
+            if (eligible(i)) r.c = p.bias != nullptr ? score(i) + double(p.bias[i]) : double(logit_at(row, i));
+            if (before(last, r) && before(r, best)) best = r;
+        }
+        last = block_reduce<THREADS>(best, lds.ranked, [](Ranked a, Ranked b) { return before(b, a) ? b : a; });
+        if (tid == 0) lds.chosen[j] = last.key;
+    }
+    __syncthreads();
+    double top = -INFINITY, total = 0;
+    const bool relative = p.normalise && p.score == SDM_SOFTMAX;
+    if (relative) {
+        for (int j = tid; j < p.k; j += THREADS)
+            if (eligible(lds.chosen[j])) top = fmax(top, double(logit_at(row, lds.chosen[j])));
+        top = fmax(block_reduce<THREADS>(top, lds.value, larger), -double(FLT_MAX));
+    }
+    auto part = [&](int key) {
+        if (!eligible(key)) return 0.0;
+        return relative ? exp(double(logit_at(row, key)) - top) : score(key);
+    };
+    if (p.normalise) {
+        for (int j = tid; j < p.k; j += THREADS) total += part(lds.chosen[j]);
+        total = block_reduce<THREADS>(total, lds.value, plus);
+    }
+    for (int j = tid; j < p.k; j += THREADS) {
+        const double u = part(lds.chosen[j]);
+        store_choice(p, t, j, lds.chosen[j], !p.normalise ? u : total > 0 ? u / total : 0.0);
+    }
+    __syncthreads();
+}
+
+// ------------------------------------------------------------------ lanes
+
+// Lane i's value of the lane that `ctrl` names within its row of 16 lanes.
+template <int ctrl> __device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), ctrl, 0xf, 0xf, true));
+}
+template <int ctrl> __device__ __forceinline__ float dpp(float v) { return __uint_as_float(dpp<ctrl>(__float_as_uint(v))); }
+constexpr int kXor1 = 0xb1, kXor2 = 0x4e;            // quad_perm [1,0,3,2] and [2,3,0,1]
+constexpr int kHalfMirror = 0x141, kMirror = 0x140;  // lane i of 8, of 16 <- lane 7 - i, 15 - i
+
+// f over the LANES (16, 32 or 64) neighbouring lanes of a row, of 32-bit values.
+template <int LANES, typename T, typename F> __device__ __forceinline__ T lanes_reduce(T v, F f) {
+    auto with = [&](uint32_t other) {
+        T o;
+        __builtin_memcpy(&o, &other, 4);
+        v = f(v, o);
+    };
+    auto bits = [&] {
+        uint32_t u;
+        __builtin_memcpy(&u, &v, 4);
+        return u;
+    };
+    with(dpp<kXor1>(bits()));
+    with(dpp<kXor2>(bits()));
+    with(dpp<kHalfMirror>(bits()));
+    with(dpp<kMirror>(bits()));
+    if constexpr (LANES >= 32) with(uint32_t(__shfl_xor(int(bits()), 16)));
+    if constexpr (LANES >= 64) with(uint32_t(__shfl_xor(int(bits()), 32)));
+    return v;
+}
+
+}  // namespace sdm
