@@ -197,9 +197,7 @@ __global__ __launch_bounds__(64, 5) void route_small_kernel(RouteParams p) {
     for (int i = 0; i < VPT; ++i) x[i] = i < held ? clean(x[i]) : -INFINITY;
     float m = 0, z = 1;
     if (softmax && (biased || !p.normalise)) {
-        float v = -FLT_MAX;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) v = max32(v, x[i]);
+        float v = max_of(x, -FLT_MAX);
         m = lanes_reduce<LANES>(v, [](float a, float c) { return max32(a, c); });
         v = 0;
 #pragma unroll
@@ -224,7 +222,7 @@ __global__ __launch_bounds__(64, 5) void route_small_kernel(RouteParams p) {
         const int of_group = size / VPT;  // lanes of a group: a power of two
         float hi = -INFINITY, lo = -INFINITY;  // the two largest
         auto add = [&](float v) {
-            lo = __builtin_amdgcn_fmed3f(hi, lo, v);
+            lo = median32(hi, lo, v);
             hi = max32(hi, v);
         };
 #pragma unroll

@@ -15,23 +15,26 @@ __device__ __forceinline__ float block_slack(bool softmax, float c) {
     return (softmax ? 0x1p-16f : 0x1p-21f) + 0x1p-23f * fabsf(c);
 }
 
-template <int THREADS> struct BlockLds {
+template <int THREADS, bool GENERAL> struct BlockLds {
+    static constexpr int kGroups = GENERAL ? SDM_MAX_GROUPS : 1, kChosen = GENERAL ? SDM_MAX_WIDTH + 1 : 1;
     union {
         struct {
             uint32_t lane_max[THREADS];
-            uint32_t group_max[SDM_MAX_GROUPS], group_next[SDM_MAX_GROUPS];
-            double worth[SDM_MAX_GROUPS];
-            float slack[SDM_MAX_GROUPS];
-            uint8_t kept[SDM_MAX_GROUPS];
+            uint32_t group_max[kGroups], group_next[kGroups];
+            double worth[kGroups];
+            float slack[kGroups];
+            uint8_t kept[kGroups];
         } first;
         struct {
-            double value[kCandidates];
-            double sorted[SDM_MAX_WIDTH + 1], score[SDM_MAX_WIDTH + 1];
+            uint64_t order[kCandidates];  // what the candidates are ranked by: a larger one goes first
+            uint32_t tie[GENERAL ? kCandidates : 1];  // and among equals
+            double sorted[kChosen], score[kChosen];
         } second;
-        ExactLds<THREADS> exact;
+        ExactLds<GENERAL ? THREADS : 1> exact;
     };
-    uint32_t cand_key[kCandidates];
+    float cand_value[kCandidates];
     int cand[kCandidates];
+    int rank[kCandidates];
     int chosen[SDM_MAX_WIDTH];
     float wave_max[THREADS / 64], wave_sum[THREADS / 64];
     double wave_value[THREADS / 64];
@@ -39,7 +42,7 @@ template <int THREADS> struct BlockLds {
     int found, count[2], doubt;
 };
 
-// VPT keys a lane, held as ordered integers of what they are chosen by. The k-th
+// VPT keys a lane, held as what they are chosen by. The k-th
 // largest of the lanes' own maxima (or a number a little below it) is a bound that
 // at least k keys reach and, with twice as many lanes as k, about 1.1 to 1.4 k do:
 // those are put in LDS, given their exact values and ranked by counting. Where more
@@ -47,19 +50,20 @@ template <int THREADS> struct BlockLds {
 // exact k-th key is found by bisection over its bits. Rows that stay in doubt with
 // a bias (more near-ties than LDS holds, groups or softmax values that float32 cannot
 // tell apart) go to exact_row.
-template <typename E, int THREADS, int VPT, bool VEC>
-__global__ __launch_bounds__(THREADS) void route_block_kernel(RouteParams p) {
-    __shared__ BlockLds<THREADS> lds;
+template <typename E, int THREADS, int VPT, bool VEC, bool GENERAL>
+__global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL ? 4 : VPT <= 8 ? 8 : 6) void route_block_kernel(RouteParams p) {
+    __shared__ BlockLds<THREADS, GENERAL> lds;
     constexpr int kWaves = THREADS / 64;
     constexpr int kN = VEC ? 16 / int(sizeof(E)) : 1;
     const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
     const int64_t t = blockIdx.x;
     const E* row = static_cast<const E*>(p.logits) + t * p.keys;
-    const bool biased = p.bias != nullptr, softmax = p.score == SDM_SOFTMAX;
-    const int size = p.keys / p.groups;
+    const bool biased = GENERAL && p.bias != nullptr, softmax = p.score == SDM_SOFTMAX;
+    const int size = GENERAL ? p.keys / p.groups : p.keys;
     auto key_of = [&](int i) { return ((i / kN) * THREADS + tid) * kN + i % kN; };
+    const bool full = p.keys == THREADS * VPT;  // no lane has less than VPT keys
 
-    float x[VPT];
+    float c[VPT];  // the logits, and then what they are chosen by
 #pragma unroll
     for (int i = 0; i < VPT; i += kN) {
         if constexpr (VEC) {
@@ -67,26 +71,29 @@ __global__ __launch_bounds__(THREADS) void route_block_kernel(RouteParams p) {
             E e[kN];
             __builtin_memcpy(e, &raw, 16);
 #pragma unroll
-            for (int j = 0; j < kN; ++j) x[i + j] = widen(e[j]);
+            for (int j = 0; j < kN; ++j) c[i + j] = widen(e[j]);
         } else {
-            x[i] = widen(row[min(key_of(i), p.keys - 1)]);
+            c[i] = widen(row[min(key_of(i), p.keys - 1)]);
         }
     }
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) x[i] = key_of(i) < p.keys ? clean(x[i]) : -INFINITY;
+    for (int i = 0; i < VPT; ++i) c[i] = clean(c[i]);
+    if (!full) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) c[i] = key_of(i) < p.keys ? c[i] : -INFINITY;
+    }
     if (tid == 0) {
         lds.found = 0;
         lds.doubt = 0;
     }
     const bool stats = softmax && (biased || !p.normalise);
     float m = 0, z = 1;
+    float most = max_of(c, -INFINITY);
     if (stats) {
-        float v = -FLT_MAX, sum = 0;
+        float sum = 0;
+        const float v = lanes_reduce<64>(max32(most, -FLT_MAX), [](float a, float b) { return max32(a, b); });
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) v = max32(v, x[i]);
-        v = lanes_reduce<64>(v, [](float a, float b) { return max32(a, b); });
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) sum += exp32(x[i] - v);
+        for (int i = 0; i < VPT; ++i) sum += exp32(c[i] - v);
         sum = lanes_reduce<64>(sum, [](float a, float b) { return a + b; });
         if (lane == 0) {
             lds.wave_max[wave] = v;
@@ -98,7 +105,6 @@ __global__ __launch_bounds__(THREADS) void route_block_kernel(RouteParams p) {
         for (int w = 0; w < kWaves; ++w) m = max32(m, lds.wave_max[w]);
         for (int w = 0; w < kWaves; ++w) z += lds.wave_sum[w] * exp32(lds.wave_max[w] - m);
     };
-    uint32_t u[VPT];
     if (biased) {
         if (stats) {
             __syncthreads();
@@ -108,42 +114,38 @@ __global__ __launch_bounds__(THREADS) void route_block_kernel(RouteParams p) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const float b = p.bias[min(key_of(i), p.keys - 1)];
-            const float c = (softmax ? exp32(x[i] - m) * inv : sigmoid32(x[i])) + b;
-            u[i] = (x[i] > -INFINITY) & (b > -INFINITY) ? ordered(c) : kOut;
+            const float v = (softmax ? exp32(c[i] - m) * inv : sigmoid32(c[i])) + b;
+            c[i] = (c[i] > -INFINITY) & (b > -INFINITY) ? v : -INFINITY;
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) u[i] = ordered(x[i]);
+        most = max_of(c, -INFINITY);
     }
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) u[i] = key_of(i) < p.keys ? u[i] : kAbsent;
-
-    if (p.groups > 1) {
+    if (GENERAL && p.groups > 1) {
         auto& f = lds.first;
         for (int g = tid; g < p.groups; g += THREADS) f.group_max[g] = f.group_next[g] = 0;
         __syncthreads();
         // The two largest of each group. Every value but the largest is at some time the
         // smaller of a maximum and what it replaced, so the second largest gets there too.
-        auto add = [&](int n, uint32_t hi, uint32_t lo) {
-            if (hi <= kOut) return;
+        auto add = [&](int n, float hi, float lo) {
+            if (!(hi > -INFINITY)) return;
             const int g = n / size;
-            lo = max(lo, min(hi, atomicMax(&f.group_max[g], hi)));
-            if (lo > kOut) atomicMax(&f.group_next[g], lo);
+            const uint32_t h = ordered(hi);
+            const uint32_t l = max(ordered(lo), min(h, atomicMax(&f.group_max[g], h)));
+            if (l > kOut) atomicMax(&f.group_next[g], l);
         };
         const bool whole = size % kN == 0;  // a vector of keys is of one group
 #pragma unroll
         for (int i = 0; i < VPT; i += kN) {
             if (whole) {
-                uint32_t hi = 0, lo = 0;
+                float hi = -INFINITY, lo = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < kN; ++j) {
-                    lo = max(lo, min(hi, u[i + j]));
-                    hi = max(hi, u[i + j]);
+                    lo = median32(hi, lo, c[i + j]);
+                    hi = max32(hi, c[i + j]);
                 }
                 add(key_of(i), hi, lo);
             } else {
 #pragma unroll
-                for (int j = 0; j < kN; ++j) add(key_of(i + j), u[i + j], 0);
+                for (int j = 0; j < kN; ++j) add(key_of(i + j), c[i + j], -INFINITY);
             }
         }
         __syncthreads();
@@ -158,7 +160,7 @@ __global__ __launch_bounds__(THREADS) void route_block_kernel(RouteParams p) {
             float slack = 0;
             if (biased) {
                 slack = block_slack(softmax, float(hi)) + (two ? block_slack(softmax, float(lo)) : 0.0f);
-                if (!(slack < INFINITY)) slack = 1.0f;
+                if (!(slack < INFINITY)) slack = 1.0f;  // of an infinite value: equal ones are in doubt
             } else if (p.top == 2) {  // by the scores, from the two logits, in float64
                 if (any) hi = softmax ? exp(hi - from) : sigmoid64(hi);
                 if (two) lo = softmax ? exp(lo - from) : sigmoid64(lo);
@@ -184,18 +186,19 @@ __global__ __launch_bounds__(THREADS) void route_block_kernel(RouteParams p) {
         __syncthreads();
         if (lds.doubt) {
             __syncthreads();
-            exact_row<E, THREADS>(p, t, lds.exact);
+            if constexpr (GENERAL) exact_row<E, THREADS>(p, t, lds.exact);
             return;
         }
+        most = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < VPT; ++i)
-            if (key_of(i) < p.keys && !f.kept[key_of(i) / size]) u[i] = kAbsent;
+        for (int i = 0; i < VPT; ++i) {
+            const bool kept = f.kept[min(key_of(i), p.keys - 1) / size];
+            if (kept) most = max32(most, c[i]);
+            c[i] = kept ? c[i] : NAN;  // NaN: reaches no bound
+        }
     }
 
-    uint32_t most = 0;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) most = max(most, u[i]);
-    lds.first.lane_max[tid] = most;
+    lds.first.lane_max[tid] = ordered(most);
     __syncthreads();
     if (wave == 0) {
         uint32_t v[kWaves], bound = 0;
@@ -210,36 +213,40 @@ __global__ __launch_bounds__(THREADS) void route_block_kernel(RouteParams p) {
             bound = trial;
             if (n <= p.k + p.k / 8) break;
         }
-        if (lane == 0) lds.threshold = bound;
+        if (lane == 0) lds.threshold = max(bound, kOut);  // -inf: every key that there is
     }
     __syncthreads();
     // With a bias, the keys that may be among the k best are those within twice the
     // slack of a bound that k keys reach.
     auto widened = [&](uint32_t bound) {
-        if (!biased || bound <= kOut) return bound;
-        const float c = from_ordered(bound);
-        return c < INFINITY ? max(ordered(c - 2 * block_slack(softmax, c)), kOut + 1) : bound;
+        const float v = from_ordered(bound);
+        return biased && fabsf(v) < INFINITY ? max32(v - 2 * block_slack(softmax, v), -FLT_MAX) : v;
     };
     auto collect = [&](auto takes) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
-            if (takes(u[i], key_of(i))) {
+            if (takes(c[i], key_of(i)) && (full || key_of(i) < p.keys)) {
                 const int at = atomicAdd(&lds.found, 1);
                 if (at < kCandidates) {
-                    lds.cand_key[at] = u[i];
+                    lds.cand_value[at] = c[i];
                     lds.cand[at] = key_of(i);
+                    lds.rank[at] = 0;
                 }
             }
     };
-    const uint32_t low = max(widened(lds.threshold), 1u);
-    if (most >= low) collect([&](uint32_t k, int) { return k >= low; });
+    const float low = widened(lds.threshold);
+    if (most >= low) collect([&](float v, int) { return v >= low; });
     __syncthreads();
     if (lds.found > kCandidates) {
         int turn = 0;
         auto count = [&](auto counts) {  // over the row
             int n = 0;
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) n += __popcll(__ballot(counts(u[i], key_of(i))));
+            for (int i = 0; i < VPT; ++i) {
+                float v = c[i];
+                opaque(v);  // else the loops below would hold another integer for each key
+                n += __popcll(__ballot(v == v && key_of(i) < p.keys && counts(ordered(v), key_of(i))));
+            }
             if (tid == 0) lds.count[turn] = 0;
             __syncthreads();
             if (lane == 0) atomicAdd(&lds.count[turn], n);
@@ -249,78 +256,95 @@ __global__ __launch_bounds__(THREADS) void route_block_kernel(RouteParams p) {
             return n;
         };
         uint32_t kth = 0;
+#pragma unroll 1
         for (int bit = 31; bit >= 0; --bit) {
             const uint32_t trial = kth | 1u << bit;
             if (count([&](uint32_t k, int) { return k >= trial; }) >= p.k) kth = trial;
         }
         if (tid == 0) lds.found = 0;
         if (biased && kth > kOut) {
-            const uint32_t least = widened(kth);
+            const uint32_t least = ordered(widened(kth));
             const int n = count([&](uint32_t k, int) { return k >= least; });
             if (n > kCandidates) {
                 __syncthreads();
-                exact_row<E, THREADS>(p, t, lds.exact);
+                if constexpr (GENERAL) exact_row<E, THREADS>(p, t, lds.exact);
                 return;
             }
-            collect([&](uint32_t k, int) { return k >= least; });
+            collect([&](float v, int) { return ordered(v) >= least && v == v; });
         } else {
             const int need = p.k - count([&](uint32_t k, int) { return k > kth; });
             int last = 0;  // the lowest keys among those equal to the k-th, up to this one
+#pragma unroll 1
             for (int bit = 15; bit >= 0; --bit) {
                 const int trial = last | 1 << bit;
                 if (count([&](uint32_t k, int n) { return k == kth && n < trial; }) < need) last = trial;
             }
-            collect([&](uint32_t k, int n) { return k > kth || (k == kth && n <= last); });
+            collect([&](float v, int n) { return v == v && (ordered(v) > kth || (ordered(v) == kth && n <= last)); });
         }
         __syncthreads();
     }
     const int found = lds.found;
     auto& f = lds.second;
-    if (biased) {
-        for (int i = tid; i < found; i += THREADS) {
-            double v = -INFINITY;
-            if (lds.cand_key[i] > kOut) {
-                const double a = logit_at(row, lds.cand[i]);
-                v = (softmax ? exp(a - double(m)) / double(z) : sigmoid64(a)) + double(p.bias[lds.cand[i]]);
+    for (int i = tid; i < found; i += THREADS) {
+        double v = lds.cand_value[i];
+        const int n = lds.cand[i];
+        if (biased) {
+            if (v > -INFINITY) {
+                const double a = logit_at(row, n);
+                v = (softmax ? exp(a - double(m)) / double(z) : sigmoid64(a)) + double(p.bias[n]);
             }
-            f.value[i] = v;
+            const uint64_t bits = uint64_t(__double_as_longlong(v + 0.0));
+            f.order[i] = bits ^ (uint64_t(int64_t(bits) >> 63) | 1ull << 63);
+        } else {
+            f.order[i] = uint64_t(ordered(float(v))) << 32 | uint32_t(~n);
         }
-        __syncthreads();
-        for (int i = tid; i < found; i += THREADS) {
-            const double v = f.value[i];
-            const int n = lds.cand[i];
-            int rank = 0;
-            for (int j = 0; j < found; ++j) rank += (f.value[j] > v) | ((f.value[j] == v) & (lds.cand[j] < n));
-            if (rank < p.k) lds.chosen[rank] = n;
-            if (softmax && rank <= p.k) {
-                f.sorted[rank] = v;
-                f.score[rank] = v > -INFINITY ? exp(double(logit_at(row, n)) - double(m)) / double(z) : 0.0;
-            }
-        }
-        __syncthreads();
-        if (softmax) {
-            // The scores are off by 2^-17, their float32 sum, of themselves, all by the same.
-            if (tid < p.k && tid + 1 < found && f.sorted[tid + 1] > -INFINITY) {
-                const double apart = fabs(f.score[tid] - f.score[tid + 1]);
-                if (apart > 0 && f.sorted[tid] - f.sorted[tid + 1] <= 0x1p-16 * apart) lds.doubt = 1;
-            }
-            __syncthreads();
-            if (lds.doubt) {
-                exact_row<E, THREADS>(p, t, lds.exact);
-                return;
-            }
-        }
-    } else {
-        for (int i = tid; i < found; i += THREADS) {
-            const uint32_t k = lds.cand_key[i];
-            const int n = lds.cand[i];
-            int rank = 0;
-            for (int j = 0; j < found; ++j) rank += (lds.cand_key[j] > k) | ((lds.cand_key[j] == k) & (lds.cand[j] < n));
-            if (rank < p.k) lds.chosen[rank] = n;
-        }
-        __syncthreads();
-        if (stats) row_stats();
+        if (biased) f.tie[i] = uint32_t(~n);
     }
+    __syncthreads();
+    {
+        // Each candidate's rank is the number of those that go before it, counted by as
+        // many threads as there are for it.
+        int per = 64;
+        while (per < found && per < THREADS) per *= 2;
+        const int parts = THREADS / per, part = tid / per;
+        for (int i = tid % per; i < found; i += per) {
+            const uint64_t mine = f.order[i];
+            int rank = 0;
+            if (biased) {
+                const uint32_t tie = f.tie[i];
+                for (int j = part; j < found; j += parts) rank += (f.order[j] > mine) | ((f.order[j] == mine) & (f.tie[j] > tie));
+            } else {
+#pragma unroll 4
+                for (int j = part; j < found; j += parts) rank += f.order[j] > mine;
+            }
+            if (rank != 0) atomicAdd(&lds.rank[i], rank);
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < found; i += THREADS) {
+        const int rank = lds.rank[i], n = lds.cand[i];
+        if (rank < p.k) lds.chosen[rank] = n;
+        if (biased && softmax && rank <= p.k) {
+            const bool in = lds.cand_value[i] > -INFINITY;
+            const double s = in ? exp(double(logit_at(row, n)) - double(m)) / double(z) : 0.0;
+            f.sorted[rank] = in ? s + double(p.bias[n]) : -INFINITY;
+            f.score[rank] = s;
+        }
+    }
+    __syncthreads();
+    if (biased && softmax) {
+        // The scores are off by 2^-17, their float32 sum, of themselves, all by the same.
+        if (tid < p.k && tid + 1 < found && f.sorted[tid + 1] > -INFINITY) {
+            const double apart = fabs(f.score[tid] - f.score[tid + 1]);
+            if (apart > 0 && f.sorted[tid] - f.sorted[tid + 1] <= 0x1p-16 * apart) lds.doubt = 1;
+        }
+        __syncthreads();
+        if (lds.doubt) {
+            if constexpr (GENERAL) exact_row<E, THREADS>(p, t, lds.exact);
+            return;
+        }
+    }
+    if (stats && !biased) row_stats();
     const int key = tid < p.k ? lds.chosen[tid] : 0;
     const float xk = tid < p.k ? logit_at(row, key) : -INFINITY;
     const bool ok = xk > -INFINITY && !(biased && bias_excludes(p.bias[key]));
@@ -349,13 +373,16 @@ __global__ __launch_bounds__(THREADS) void route_block_kernel(RouteParams p) {
 
 template <typename E, int THREADS, int VPT> void run(const RouteParams& p, bool vec, hipStream_t stream) {
     const dim3 grid{unsigned(p.tokens)}, block{THREADS};
+    const bool general = p.bias != nullptr || p.groups > 1;
     if constexpr (VPT * sizeof(E) % 16 == 0) {
         if (vec) {
-            hipLaunchKernelGGL((route_block_kernel<E, THREADS, VPT, true>), grid, block, 0, stream, p);
+            if (general) hipLaunchKernelGGL((route_block_kernel<E, THREADS, VPT, true, true>), grid, block, 0, stream, p);
+            else hipLaunchKernelGGL((route_block_kernel<E, THREADS, VPT, true, false>), grid, block, 0, stream, p);
             return;
         }
     }
-    hipLaunchKernelGGL((route_block_kernel<E, THREADS, VPT, false>), grid, block, 0, stream, p);
+    if (general) hipLaunchKernelGGL((route_block_kernel<E, THREADS, VPT, false, true>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((route_block_kernel<E, THREADS, VPT, false, false>), grid, block, 0, stream, p);
 }
 
 template <typename E> void run_route(const RouteParams& p, hipStream_t stream) {

@@ -10,11 +10,32 @@
 
 namespace sdm {
 
-// The larger and the smaller of two that are not NaN, without the moves that a NaN would need.
-__device__ __forceinline__ float max32(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, INFINITY); }
-__device__ __forceinline__ float min32(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, -INFINITY); }
+// Largest and smallest as single instructions: the compiler adds moves that quieten
+// NaN operands first, and there are none here.
+__device__ __forceinline__ float max32(float a, float b) {
+    float r;
+    asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+__device__ __forceinline__ float max32(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+__device__ __forceinline__ float median32(float a, float b, float c) {
+    float r;
+    asm("v_med3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+template <int N> __device__ __forceinline__ float max_of(const float (&x)[N], float v) {
+    if constexpr (N % 2 == 1) v = max32(v, x[N - 1]);
+#pragma unroll
+    for (int i = 0; i + 1 < N; i += 2) v = max32(v, x[i], x[i + 1]);
+    return v;
+}
 // A logit as the definition reads it: NaN counts as -inf, +inf as the largest float32.
-__device__ __forceinline__ float clean(float x) { return min32(x != x ? -INFINITY : x, FLT_MAX); }
+// (A median of three with a quiet NaN among them is the least of the other two.)
+__device__ __forceinline__ float clean(float x) { return median32(max32(x, x), -INFINITY, FLT_MAX); }
 template <typename E> __device__ __forceinline__ float logit_at(const E* row, int64_t i) { return clean(widen(row[i])); }
 
 __device__ __forceinline__ bool bias_excludes(float b) { return !(b > -INFINITY); }
