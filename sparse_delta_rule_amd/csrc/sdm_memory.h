@@ -17,7 +17,8 @@ struct RouteParams {
     int groups, kept, top;
     int normalise;
     double scale;
-    int64_t streams, stream_slots;
+    uint32_t streams;  // at most that many: tokens are fewer than 2^32
+    int64_t stream_slots;
     void* idx;
     void* w;
     int idx64, w_bf16;
@@ -32,7 +33,8 @@ struct RouteBackwardParams {
     int keys, k;
     int score, normalise;
     double scale;
-    int64_t streams, stream_slots;
+    uint32_t streams;  // at most that many: tokens are fewer than 2^32
+    int64_t stream_slots;
     const void* idx;
     const void* dw;
     void* dlogits;

@@ -279,7 +279,7 @@ int sdm_route(const void* logits, int logit_dtype, int64_t tokens, int64_t keys,
     p.top = group_top;
     p.normalise = normalise != 0;
     p.scale = scale;
-    p.streams = streams;
+    p.streams = uint32_t(streams < UINT32_MAX ? streams : UINT32_MAX);
     p.stream_slots = stream_slots;
     p.idx = idx;
     p.w = w;
@@ -322,7 +322,7 @@ int sdm_route_backward(const void* logits, int logit_dtype, int64_t tokens, int6
     p.score = score;
     p.normalise = normalise != 0;
     p.scale = scale;
-    p.streams = streams;
+    p.streams = uint32_t(streams < UINT32_MAX ? streams : UINT32_MAX);
     p.stream_slots = stream_slots;
     p.idx = idx;
     p.dw = dw;

@@ -151,6 +151,7 @@ __global__ __launch_bounds__(64, 5) void route_small_kernel(RouteParams p) {
     constexpr int kKeys = VPT * LANES;
     constexpr int kBits = kKeys <= 64 ? 6 : kKeys <= 128 ? 7 : kKeys <= 256 ? 8 : kKeys <= 512 ? 9 : 10;
     constexpr uint32_t kMask = (1u << kBits) - 1;
+    ieee_mode_off();
     const int tid = threadIdx.x, l = tid % LANES, first = tid - l;
     const bool biased = p.bias != nullptr, softmax = p.score == SDM_SOFTMAX;
     const int size = p.keys / p.groups;
@@ -362,6 +363,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(RouteBackwardP
     __shared__ double redd[kThreads];
     __shared__ float redf[kThreads];
     __shared__ float tile[kTile];
+    ieee_mode_off();
     const int tid = threadIdx.x;
     for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
         const E* row = static_cast<const E*>(p.logits) + t * p.keys;
@@ -382,7 +384,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(RouteBackwardP
         if (tid < p.k) {
             const int64_t o = t * p.k + tid;
             key = (p.idx64 ? static_cast<const int64_t*>(p.idx)[o] : int64_t(static_cast<const int32_t*>(p.idx)[o])) -
-                  (t % p.streams) * p.stream_slots;
+                  int64_t(uint32_t(t) % p.streams) * p.stream_slots;
             if (key < 0 || key >= p.keys) key = -1;
             if (key >= 0 && !(p.bias != nullptr && bias_excludes(p.bias[key]))) x = logit_at(row, key);
             dw = p.w_bf16 ? widen(static_cast<const uint16_t*>(p.dw)[o]) : static_cast<const float*>(p.dw)[o];

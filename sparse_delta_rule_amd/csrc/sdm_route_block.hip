@@ -26,7 +26,7 @@ template <int THREADS, bool GENERAL> struct BlockLds {
             uint8_t kept[kGroups];
         } first;
         struct {
-            uint64_t order[kCandidates];  // what the candidates are ranked by: a larger one goes first
+            alignas(16) uint64_t order[kCandidates];  // what the candidates are ranked by: a larger one goes first
             uint32_t tie[GENERAL ? kCandidates : 1];  // and among equals
             double sorted[kChosen], score[kChosen];
         } second;
@@ -36,6 +36,7 @@ template <int THREADS, bool GENERAL> struct BlockLds {
     int cand[kCandidates];
     int rank[kCandidates];
     int chosen[SDM_MAX_WIDTH];
+    float chosen_value[SDM_MAX_WIDTH];
     float wave_max[THREADS / 64], wave_sum[THREADS / 64];
     double wave_value[THREADS / 64];
     uint32_t threshold;
@@ -51,10 +52,11 @@ template <int THREADS, bool GENERAL> struct BlockLds {
 // a bias (more near-ties than LDS holds, groups or softmax values that float32 cannot
 // tell apart) go to exact_row.
 template <typename E, int THREADS, int VPT, bool VEC, bool GENERAL>
-__global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL ? 4 : VPT <= 8 ? 8 : 6) void route_block_kernel(RouteParams p) {
+__global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL || VPT == 64 ? 4 : VPT <= 8 ? 8 : 6) void route_block_kernel(RouteParams p) {
     __shared__ BlockLds<THREADS, GENERAL> lds;
     constexpr int kWaves = THREADS / 64;
     constexpr int kN = VEC ? 16 / int(sizeof(E)) : 1;
+    ieee_mode_off();
     const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
     const int64_t t = blockIdx.x;
     const E* row = static_cast<const E*>(p.logits) + t * p.keys;
@@ -285,6 +287,7 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL ? 4 : VPT <= 8 
     }
     const int found = lds.found;
     auto& f = lds.second;
+    if (tid == 0 && found < kCandidates) f.order[found] = 0;
     for (int i = tid; i < found; i += THREADS) {
         double v = lds.cand_value[i];
         const int n = lds.cand[i];
@@ -314,8 +317,12 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL ? 4 : VPT <= 8 
                 const uint32_t tie = f.tie[i];
                 for (int j = part; j < found; j += parts) rank += (f.order[j] > mine) | ((f.order[j] == mine) & (f.tie[j] > tie));
             } else {
+                // Two at a time: the list is padded with a 0, before which everything goes.
 #pragma unroll 4
-                for (int j = part; j < found; j += parts) rank += f.order[j] > mine;
+                for (int j = 2 * part; j < found; j += 2 * parts) {
+                    const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(&f.order[j]);
+                    rank += (two.x > mine) + (two.y > mine);
+                }
             }
             if (rank != 0) atomicAdd(&lds.rank[i], rank);
         }
@@ -323,7 +330,10 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL ? 4 : VPT <= 8 
     __syncthreads();
     for (int i = tid; i < found; i += THREADS) {
         const int rank = lds.rank[i], n = lds.cand[i];
-        if (rank < p.k) lds.chosen[rank] = n;
+        if (rank < p.k) {
+            lds.chosen[rank] = n;
+            lds.chosen_value[rank] = lds.cand_value[i];
+        }
         if (biased && softmax && rank <= p.k) {
             const bool in = lds.cand_value[i] > -INFINITY;
             const double s = in ? exp(double(logit_at(row, n)) - double(m)) / double(z) : 0.0;
@@ -344,10 +354,13 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL ? 4 : VPT <= 8 
             return;
         }
     }
+    if (tid / 64 * 64 >= p.k && !p.normalise) return;  // the other wavefronts have no part in the weights
     if (stats && !biased) row_stats();
     const int key = tid < p.k ? lds.chosen[tid] : 0;
-    const float xk = tid < p.k ? logit_at(row, key) : -INFINITY;
-    const bool ok = xk > -INFINITY && !(biased && bias_excludes(p.bias[key]));
+    // What a key was chosen by is its logit, or -inf, where there is no bias.
+    float xk = tid < p.k ? lds.chosen_value[tid] : -INFINITY;
+    const bool ok = xk > -INFINITY;
+    if (biased && ok) xk = logit_at(row, key);
     auto block = [&](double v, auto op) {  // over the lanes, then over the wavefronts in order
         for (int n = 1; n < 64; n *= 2) v = op(v, __shfl_xor(v, n));
         __syncthreads();
@@ -387,10 +400,12 @@ template <typename E, int THREADS, int VPT> void run(const RouteParams& p, bool 
 
 template <typename E> void run_route(const RouteParams& p, hipStream_t stream) {
     const bool vec = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && p.keys * sizeof(E) % 16 == 0;
-    if (p.k <= 128 && p.keys <= 4096) {
+    if (p.k <= 128 && p.keys <= 16384) {
         if (p.keys <= 1024) run<E, 256, 4>(p, vec, stream);
         else if (p.keys <= 2048) run<E, 256, 8>(p, vec, stream);
-        else run<E, 256, 16>(p, vec, stream);
+        else if (p.keys <= 4096) run<E, 256, 16>(p, vec, stream);
+        else if (p.keys <= 8192) run<E, 256, 32>(p, vec, stream);
+        else run<E, 256, 64>(p, vec, stream);
     } else if (p.keys <= 16384) {
         if (p.keys <= 512) run<E, 512, 1>(p, vec, stream);
         else if (p.keys <= 2048) run<E, 512, 4>(p, vec, stream);

@@ -34,8 +34,10 @@ template <int N> __device__ __forceinline__ float max_of(const float (&x)[N], fl
     return v;
 }
 // A logit as the definition reads it: NaN counts as -inf, +inf as the largest float32.
-// (A median of three with a quiet NaN among them is the least of the other two.)
-__device__ __forceinline__ float clean(float x) { return median32(max32(x, x), -INFINITY, FLT_MAX); }
+// A median of three with a NaN among them is the least of the other two, of a
+// signalling NaN too while the wavefront's IEEE mode is off.
+__device__ __forceinline__ float clean(float x) { return median32(x, -INFINITY, FLT_MAX); }
+__device__ __forceinline__ void ieee_mode_off() { __builtin_amdgcn_s_setreg(1 | 9 << 6 | 0 << 11, 0); }  // MODE, bit 9
 template <typename E> __device__ __forceinline__ float logit_at(const E* row, int64_t i) { return clean(widen(row[i])); }
 
 __device__ __forceinline__ bool bias_excludes(float b) { return !(b > -INFINITY); }
@@ -57,7 +59,7 @@ constexpr uint32_t kOut = 0x007fffffu;  // ordered(-inf): a key that is not elig
 constexpr uint32_t kAbsent = 0;         // a key that cannot be chosen at all
 
 __device__ __forceinline__ void store_choice(const RouteParams& p, int64_t t, int j, int key, double u) {
-    const int64_t o = t * p.k + j, slot = (t % p.streams) * p.stream_slots + key;
+    const int64_t o = t * p.k + j, slot = int64_t(uint32_t(t) % p.streams) * p.stream_slots + key;
     if (p.idx64) static_cast<int64_t*>(p.idx)[o] = slot;
     else static_cast<int32_t*>(p.idx)[o] = int32_t(slot);
     const float w = float(p.scale * u);

@@ -201,6 +201,21 @@ def test_route_of_a_large_call():
     assert (d != 0).sum().item() == 2 * T
 
 
+@pytest.mark.parametrize("N,k", [(64, 8), (256, 12), (1000, 40), (5000, 64), (16384, 256)])
+def test_route_of_signalling_nans(N, k):
+    """Every kind of NaN counts as -inf, also those that no arithmetic makes."""
+    for dtype, bits, plain in ((torch.float32, torch.int32, (0x7f800001, -0x7fffff, 0x7fc00000)),
+                               (torch.bfloat16, torch.int16, (0x7f81, -0x7f, 0x7fc0))):
+        x = scores_like("normal", 3, N, N).to(dtype)
+        for i, pattern in enumerate(plain):
+            x.view(bits)[i, i::3] = pattern
+        assert x.isnan().sum() >= N - 3
+        check_route(x, k)
+        check_route(x, k, score="sigmoid", bias=torch.zeros(N), normalise=True)
+        check_backward(x, k)
+        check_backward(x, k, score="sigmoid", normalise=True)
+
+
 # ------------------------------------------------------------------ backward
 
 
