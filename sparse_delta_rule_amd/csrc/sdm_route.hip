@@ -198,12 +198,8 @@ __global__ __launch_bounds__(64, 5) void route_small_kernel(RouteParams p) {
     for (int i = 0; i < VPT; ++i) x[i] = i < held ? clean(x[i]) : -INFINITY;
     float m = 0, z = 1;
     if (softmax && (biased || !p.normalise)) {
-        float v = max_of(x, -FLT_MAX);
-        m = lanes_reduce<LANES>(v, [](float a, float c) { return max32(a, c); });
-        v = 0;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) v += exp32(x[i] - m);
-        z = lanes_reduce<LANES>(v, [](float a, float c) { return a + c; });
+        m = lanes_reduce<LANES>(max_of(x, -FLT_MAX), [](float a, float c) { return max32(a, c); });
+        z = lanes_reduce<LANES>(exp_sum(x, m), [](float a, float c) { return a + c; });
     }
     // What the keys are chosen by: the value, or what has its order.
     float c[VPT];

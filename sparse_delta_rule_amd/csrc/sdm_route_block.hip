@@ -26,14 +26,12 @@ template <int THREADS, bool GENERAL> struct BlockLds {
             uint8_t kept[kGroups];
         } first;
         struct {
-            alignas(16) uint64_t order[kCandidates];  // what the candidates are ranked by: a larger one goes first
-            uint32_t tie[GENERAL ? kCandidates : 1];  // and among equals
+            uint64_t value[GENERAL ? kCandidates : 1];  // with a bias: float64 values, as ordered integers
             double sorted[kChosen], score[kChosen];
         } second;
         ExactLds<GENERAL ? THREADS : 1> exact;
     };
-    float cand_value[kCandidates];
-    int cand[kCandidates];
+    alignas(16) uint64_t cand[kCandidates];  // what it is chosen by, as an ordered integer, and its key's complement
     int rank[kCandidates];
     int chosen[SDM_MAX_WIDTH];
     float chosen_value[SDM_MAX_WIDTH];
@@ -63,27 +61,33 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL || VPT == 64 ? 
     const bool biased = GENERAL && p.bias != nullptr, softmax = p.score == SDM_SOFTMAX;
     const int size = GENERAL ? p.keys / p.groups : p.keys;
     auto key_of = [&](int i) { return ((i / kN) * THREADS + tid) * kN + i % kN; };
-    const bool full = p.keys == THREADS * VPT;  // no lane has less than VPT keys
+    constexpr uint32_t kMinusInf = sizeof(E) == 2 ? 0xff80ff80u : 0xff800000u;
 
     float c[VPT];  // the logits, and then what they are chosen by
+    if constexpr (VEC) {
+        uint4 raw[VPT / kN];
 #pragma unroll
-    for (int i = 0; i < VPT; i += kN) {
-        if constexpr (VEC) {
-            const uint4 raw = *reinterpret_cast<const uint4*>(row + min(key_of(i), p.keys - kN));
+        for (int i = 0; i < VPT / kN; ++i) raw[i] = *reinterpret_cast<const uint4*>(row + min(key_of(i * kN), p.keys - kN));
+#pragma unroll
+        for (int i = 0; i < VPT / kN; ++i) {
+            const uint32_t in = uint32_t((key_of(i * kN) - p.keys) >> 31);  // all ones where the row has the vector
+            uint4 v = raw[i];
+            v.x = (v.x & in) | (kMinusInf & ~in), v.y = (v.y & in) | (kMinusInf & ~in);
+            v.z = (v.z & in) | (kMinusInf & ~in), v.w = (v.w & in) | (kMinusInf & ~in);
+            opaque(v);  // four words chosen, not each key
             E e[kN];
-            __builtin_memcpy(e, &raw, 16);
+            __builtin_memcpy(e, &v, 16);
 #pragma unroll
-            for (int j = 0; j < kN; ++j) c[i + j] = widen(e[j]);
-        } else {
-            c[i] = widen(row[min(key_of(i), p.keys - 1)]);
+            for (int j = 0; j < kN; ++j) c[i * kN + j] = widen(e[j]);
         }
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) c[i] = clean(c[i]);
-    if (!full) {
+        for (int i = 0; i < VPT; ++i) c[i] = widen(row[min(key_of(i), p.keys - 1)]);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) c[i] = key_of(i) < p.keys ? c[i] : -INFINITY;
     }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) c[i] = clean(c[i]);
     if (tid == 0) {
         lds.found = 0;
         lds.doubt = 0;
@@ -92,11 +96,8 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL || VPT == 64 ? 
     float m = 0, z = 1;
     float most = max_of(c, -INFINITY);
     if (stats) {
-        float sum = 0;
         const float v = lanes_reduce<64>(max32(most, -FLT_MAX), [](float a, float b) { return max32(a, b); });
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) sum += exp32(c[i] - v);
-        sum = lanes_reduce<64>(sum, [](float a, float b) { return a + b; });
+        const float sum = lanes_reduce<64>(exp_sum(c, v), [](float a, float b) { return a + b; });
         if (lane == 0) {
             lds.wave_max[wave] = v;
             lds.wave_sum[wave] = sum;
@@ -201,6 +202,7 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL || VPT == 64 ? 
     }
 
     lds.first.lane_max[tid] = ordered(most);
+    for (int i = tid; i < kCandidates; i += THREADS) lds.rank[i] = 0;
     __syncthreads();
     if (wave == 0) {
         uint32_t v[kWaves], bound = 0;
@@ -224,18 +226,20 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL || VPT == 64 ? 
         const float v = from_ordered(bound);
         return biased && fabsf(v) < INFINITY ? max32(v - 2 * block_slack(softmax, v), -FLT_MAX) : v;
     };
+    uint32_t zero = 0;
+    opaque(zero);  // an address that may differ between lanes: few add at a time, one by one is best
     auto collect = [&](auto takes) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
-            if (takes(c[i], key_of(i)) && (full || key_of(i) < p.keys)) {
-                const int at = atomicAdd(&lds.found, 1);
-                if (at < kCandidates) {
-                    lds.cand_value[at] = c[i];
-                    lds.cand[at] = key_of(i);
-                    lds.rank[at] = 0;
-                }
+            if (takes(c[i], key_of(i))) {
+                uint32_t n = uint32_t(key_of(i));
+                opaque(n);  // compared here, and not for all keys beforehand
+                if (int(n) >= p.keys) continue;
+                const int at = atomicAdd(&lds.found + zero, 1);
+                if (at < kCandidates) lds.cand[at] = uint64_t(ordered(c[i])) << 32 | ~n;
             }
     };
+    auto value_of = [](uint64_t cand) { return from_ordered(uint32_t(cand >> 32)); };
     const float low = widened(lds.threshold);
     if (most >= low) collect([&](float v, int) { return v >= low; });
     __syncthreads();
@@ -246,8 +250,10 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL || VPT == 64 ? 
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 float v = c[i];
-                opaque(v);  // else the loops below would hold another integer for each key
-                n += __popcll(__ballot(v == v && key_of(i) < p.keys && counts(ordered(v), key_of(i))));
+                uint32_t key = uint32_t(key_of(i));
+                opaque(v);  // else the loops below would hold another integer and a mask for each key
+                opaque(key);
+                n += __popcll(__ballot(v == v && int(key) < p.keys && counts(ordered(v), int(key))));
             }
             if (tid == 0) lds.count[turn] = 0;
             __syncthreads();
@@ -287,57 +293,54 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL || VPT == 64 ? 
     }
     const int found = lds.found;
     auto& f = lds.second;
-    if (tid == 0 && found < kCandidates) f.order[found] = 0;
-    for (int i = tid; i < found; i += THREADS) {
-        double v = lds.cand_value[i];
-        const int n = lds.cand[i];
-        if (biased) {
+    if (biased) {
+        for (int i = tid; i < found; i += THREADS) {
+            const int n = int(~uint32_t(lds.cand[i]));
+            double v = value_of(lds.cand[i]);
             if (v > -INFINITY) {
                 const double a = logit_at(row, n);
                 v = (softmax ? exp(a - double(m)) / double(z) : sigmoid64(a)) + double(p.bias[n]);
             }
             const uint64_t bits = uint64_t(__double_as_longlong(v + 0.0));
-            f.order[i] = bits ^ (uint64_t(int64_t(bits) >> 63) | 1ull << 63);
-        } else {
-            f.order[i] = uint64_t(ordered(float(v))) << 32 | uint32_t(~n);
+            f.value[i] = bits ^ (uint64_t(int64_t(bits) >> 63) | 1ull << 63);
         }
-        if (biased) f.tie[i] = uint32_t(~n);
+        __syncthreads();
+    } else if (tid == 0 && found < kCandidates) {
+        lds.cand[found] = 0;  // the list in pairs; everything goes before a 0
     }
-    __syncthreads();
-    {
-        // Each candidate's rank is the number of those that go before it, counted by as
-        // many threads as there are for it.
-        int per = 64;
-        while (per < found && per < THREADS) per *= 2;
-        const int parts = THREADS / per, part = tid / per;
-        for (int i = tid % per; i < found; i += per) {
-            const uint64_t mine = f.order[i];
-            int rank = 0;
-            if (biased) {
-                const uint32_t tie = f.tie[i];
-                for (int j = part; j < found; j += parts) rank += (f.order[j] > mine) | ((f.order[j] == mine) & (f.tie[j] > tie));
-            } else {
-                // Two at a time: the list is padded with a 0, before which everything goes.
+    // Each candidate's rank is the number of those that go before it, counted by as
+    // many threads as there are for it.
+    int per = 64;
+    while (per < found && per < THREADS) per *= 2;
+    const int parts = THREADS / per, part = tid / per;
+    if (!biased) __syncthreads();
+    for (int i = tid % per; i < found; i += per) {
+        const uint64_t mine = lds.cand[i];
+        int rank = 0;
+        if (biased) {
+            const uint64_t v = f.value[i];
+            for (int j = part; j < found; j += parts)
+                rank += (f.value[j] > v) | ((f.value[j] == v) & (uint32_t(lds.cand[j]) > uint32_t(mine)));
+        } else {
 #pragma unroll 4
-                for (int j = 2 * part; j < found; j += 2 * parts) {
-                    const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(&f.order[j]);
-                    rank += (two.x > mine) + (two.y > mine);
-                }
+            for (int j = 2 * part; j < found; j += 2 * parts) {
+                const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(&lds.cand[j]);
+                rank += (two.x > mine) + (two.y > mine);
             }
-            if (rank != 0) atomicAdd(&lds.rank[i], rank);
         }
+        if (rank != 0) atomicAdd(&lds.rank[i], rank);
     }
     __syncthreads();
     for (int i = tid; i < found; i += THREADS) {
-        const int rank = lds.rank[i], n = lds.cand[i];
+        const int rank = lds.rank[i], n = int(~uint32_t(lds.cand[i]));
+        const float v = value_of(lds.cand[i]);
         if (rank < p.k) {
             lds.chosen[rank] = n;
-            lds.chosen_value[rank] = lds.cand_value[i];
+            lds.chosen_value[rank] = v;
         }
         if (biased && softmax && rank <= p.k) {
-            const bool in = lds.cand_value[i] > -INFINITY;
-            const double s = in ? exp(double(logit_at(row, n)) - double(m)) / double(z) : 0.0;
-            f.sorted[rank] = in ? s + double(p.bias[n]) : -INFINITY;
+            const double s = v > -INFINITY ? exp(double(logit_at(row, n)) - double(m)) / double(z) : 0.0;
+            f.sorted[rank] = v > -INFINITY ? s + double(p.bias[n]) : -INFINITY;
             f.score[rank] = s;
         }
     }

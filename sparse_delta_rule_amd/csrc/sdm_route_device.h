@@ -45,6 +45,22 @@ __device__ __forceinline__ bool bias_excludes(float b) { return !(b > -INFINITY)
 __device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
 // Within 2^-22 of its value: the hardware's base-2 exponential and reciprocal.
 __device__ __forceinline__ float exp32(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+// Sum of exp(x[i] - v), v the largest x of the row's lanes or -FLT_MAX.
+template <int N> __device__ __forceinline__ float exp_sum(const float (&x)[N], float v) {
+    constexpr float kL = 1.44269504f;
+    float sum = 0;
+    if (__ballot(!(fabsf(v) < 1e30f)) == 0) {  // a branch of the wavefront
+        // 2^(x L - c) with c = v L rounded: one operation less a term, and what c's rounding
+        // puts into every term, 2^(v L - c), is taken out of the sum.
+        const float c = v * kL;
+#pragma unroll
+        for (int i = 0; i < N; ++i) sum += __builtin_amdgcn_exp2f(fmaf(x[i], kL, -c));
+        return sum * __builtin_amdgcn_exp2f(-fmaf(v, kL, -c));
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum += exp32(x[i] - v);
+    return sum;
+}
 __device__ __forceinline__ float sigmoid32(float x) { return __builtin_amdgcn_rcpf(1.0f + exp32(-x)); }
 
 // float32 as an unsigned integer of the same order (-0 as +0), and back.
