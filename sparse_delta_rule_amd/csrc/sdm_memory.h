@@ -73,6 +73,7 @@ struct MemoryGatherParams {
     int scale_bytes;
     int operands;
     int idx64, w_bf16;
+    int out_vec;  // outputs and their rows aligned to 16 bytes (gather)
 };
 hipError_t launch_gather_packed(const MemoryGatherParams& p, bool mx4, hipStream_t stream);
 hipError_t launch_weight_grad(const MemoryGatherParams& p, int bank_dtype, hipStream_t stream);

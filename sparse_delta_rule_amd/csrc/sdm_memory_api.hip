@@ -196,6 +196,7 @@ int rows_call(const char* fn, const Rows& r, MemoryGatherParams* p, bool* run, h
     p->operands = operands;
     p->idx64 = r.idx_dtype == SDM_I64;
     p->w_bf16 = r.w_dtype == SDM_BF16;
+    p->out_vec = r.head_dim % 4 == 0 && aligned(r.out[0], 16) && (operands == 1 || aligned(r.out[1], 16));
     // A pair of a token and an operand takes at most 64 threads of a launch.
     if (r.tokens > (kMaxGridThreads - 256) / (64 * operands))
         return fail(SDM_E_SHAPE, "%s: %lld tokens exceed the grid", fn, (i64)r.tokens);

@@ -172,51 +172,140 @@ __device__ __forceinline__ bool is_live(const MemoryGatherParams& p, int64_t t) 
 
 constexpr int kFlight = 8;  // rows of a pair whose loads are in flight together
 
-// A pair (token, operand) takes `lanes` neighbouring lanes, 16 columns each.
-template <bool MX4>
+// What a pair (token, operand) needs of an entry, put into LDS by the pair's own
+// lanes, kStage entries a lane: where its row begins, its weight, and the scales of
+// a row of at most four blocks. So a lane's slots, weights and scales cost one load
+// each for a whole row of lanes, and a row one LDS read.
+struct Entry {
+    int64_t row;
+    float w;
+    uint32_t scales;
+};
+constexpr int kStage = 8;
+
+struct Pair {
+    int64_t t;
+    int op, lane, lanes, width;
+    Entry* entries;  // of this pair: kStage * lanes
+};
+
+__device__ __forceinline__ Pair this_pair(const MemoryGatherParams& p, int lanes, Entry* lds) {
+    Pair r;
+    const int in_block = int(threadIdx.x) / lanes;
+    const int64_t q = int64_t(blockIdx.x) * (kThreads / lanes) + in_block;
+    r.t = p.operands == 2 ? q >> 1 : q;
+    r.op = p.operands == 2 ? int(q & 1) : 0;
+    r.lane = int(threadIdx.x) % lanes;
+    r.lanes = lanes;
+    r.width = r.op == 0 ? p.width[0] : p.width[1];
+    r.entries = lds + in_block * (kStage * lanes);
+    return r;
+}
+
+// Put the pair's entries n0, n0 + 1, ... into LDS (at most kStage * lanes of them);
+// returns how many. A wavefront's LDS accesses happen in order, and the lanes of a
+// pair are in one wavefront.
+template <bool WEIGHTS, bool SCALES>
+__device__ __forceinline__ int stage(const MemoryGatherParams& p, const Pair& r, int n0) {
+    const int count = min(r.width - n0, kStage * r.lanes);
+    const void* idx = r.op == 0 ? p.idx[0] : p.idx[1];
+    const void* w = r.op == 0 ? p.w[0] : p.w[1];
+    const int64_t first = r.t * r.width + n0;
+    int64_t slot[kStage];
+    float v[kStage] = {};
+    uint32_t sc[kStage] = {};
+    if (p.idx64) {
+#pragma unroll
+        for (int i = 0; i < kStage; ++i)
+            slot[i] = static_cast<const int64_t*>(idx)[first + min(i * r.lanes + r.lane, count - 1)];
+    } else {
+#pragma unroll
+        for (int i = 0; i < kStage; ++i)
+            slot[i] = static_cast<const int32_t*>(idx)[first + min(i * r.lanes + r.lane, count - 1)];
+    }
+    if (WEIGHTS && p.w_bf16) {
+#pragma unroll
+        for (int i = 0; i < kStage; ++i)
+            v[i] = widen(static_cast<const uint16_t*>(w)[first + min(i * r.lanes + r.lane, count - 1)]);
+    } else if (WEIGHTS) {
+#pragma unroll
+        for (int i = 0; i < kStage; ++i)
+            v[i] = static_cast<const float*>(w)[first + min(i * r.lanes + r.lane, count - 1)];
+    }
+    if (SCALES) {
+#pragma unroll
+        for (int i = 0; i < kStage; ++i) sc[i] = reinterpret_cast<const uint32_t*>(p.scales)[slot[i]];
+    }
+#pragma unroll
+    for (int i = 0; i < kStage; ++i) {
+        const int n = i * r.lanes + r.lane;
+        if (n < count) r.entries[n] = Entry{slot[i] * p.row_bytes, v[i], sc[i]};
+    }
+    __builtin_amdgcn_wave_barrier();
+    return count;
+}
+
+// The scale of a row's block as the conversions take it, from an entry's four bytes.
+__device__ __forceinline__ float scale_of(uint32_t four, int block) {
+    return __uint_as_float(four >> (8 * block) << 23 & 0x7f800000u);
+}
+
+// A pair takes `lanes` neighbouring lanes, 16 columns each. FOUR: a row has at most
+// four blocks, whose scales come with the entry.
+template <bool MX4, bool FOUR>
 __global__ __launch_bounds__(kThreads) void gather_packed_kernel(MemoryGatherParams p, int lanes) {
     using C = Codes16<MX4>;
-    const int per = kThreads / lanes;
-    const int64_t q = int64_t(blockIdx.x) * per + int(threadIdx.x) / lanes;
-    const int64_t t = q / p.operands;
-    const int op = int(q - t * p.operands);
-    if (t >= p.tokens) return;
-    const int c0 = 16 * (int(blockIdx.y) * lanes + int(threadIdx.x) % lanes);
-    if (c0 >= p.hd) return;
+    __shared__ Entry lds[kThreads * kStage];
+    const Pair r = this_pair(p, lanes, lds);
+    if (r.t >= p.tokens) return;
+    const int c0 = 16 * (int(blockIdx.y) * lanes + r.lane);
+    const int block = c0 / SDM_PACK_BLOCK;
     float acc[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-    if (is_live(p, t)) {
-        const int width = p.width[op];
-        const int idx_bytes = p.idx64 ? 8 : 4, w_bytes = p.w_bf16 ? 2 : 4;
-        const uint8_t* codes = static_cast<const uint8_t*>(p.bank) + c0 / 16 * C::kBytes;
-        const uint8_t* scales = p.scales + c0 / SDM_PACK_BLOCK;
-        for (int n0 = 0; n0 < width; n0 += kFlight) {
-            typename C::Raw raw[kFlight];
-            float s[kFlight], w[kFlight];
+    if (is_live(p, r.t)) {
+        // A lane past the row's end reads its last columns.
+        const int vec = min(c0 / 16, (p.hd - 1) / 16);
+        const char* codes = static_cast<const char*>(p.bank) + vec * C::kBytes;
+        const uint8_t* scales = p.scales + min(block, (p.hd - 1) / SDM_PACK_BLOCK);
+        for (int s0 = 0; s0 < r.width; s0 += kStage * lanes) {
+            const int count = stage<true, FOUR>(p, r, s0);
+            for (int n0 = 0; n0 < count; n0 += kFlight) {
+                typename C::Raw raw[kFlight];
+                Entry e[kFlight];
+                float s[kFlight];
 #pragma unroll
-            for (int u = 0; u < kFlight; ++u) {
-                const int64_t n = t * width + min(n0 + u, width - 1);
-                const int64_t slot = slot_at(p.idx[op], n, idx_bytes);
-                w[u] = value_at(p.w[op], n, w_bytes);
-                raw[u] = *reinterpret_cast<const typename C::Raw*>(codes + slot * p.row_bytes);
-                s[u] = __uint_as_float(uint32_t(scales[slot * p.scale_bytes]) << 23);
-            }
+                for (int u = 0; u < kFlight; ++u) e[u] = r.entries[min(n0 + u, count - 1)];
 #pragma unroll
-            for (int u = 0; u < kFlight; ++u) {
-                if (n0 + u < width) {
-                    float x[16];
-                    C::values(raw[u], s[u], x);
+                for (int u = 0; u < kFlight; ++u) raw[u] = *reinterpret_cast<const typename C::Raw*>(codes + e[u].row);
+                if constexpr (!FOUR) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[i] = fmaf(w[u], x[i], acc[i]);
+                    for (int u = 0; u < kFlight; ++u)
+                        s[u] = __uint_as_float(uint32_t(scales[e[u].row / p.row_bytes * p.scale_bytes]) << 23);
+                }
+#pragma unroll
+                for (int u = 0; u < kFlight; ++u) {
+                    if (n0 + u < count) {
+                        float x[16];
+                        C::values(raw[u], FOUR ? scale_of(e[u].scales, block) : s[u], x);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) acc[i] = fmaf(e[u].w, x[i], acc[i]);
+                    }
                 }
             }
         }
     }
-    float* out = p.out[op] + t * p.hd + c0;
+    if (c0 >= p.hd) return;
+    float* out = (r.op == 0 ? p.out[0] : p.out[1]) + r.t * p.hd + c0;
+    if (c0 + 16 <= p.hd && p.out_vec) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (c0 + i < p.hd) out[i] = acc[i];
+        for (int i = 0; i < 4; ++i)
+            reinterpret_cast<float4*>(out)[i] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (c0 + i < p.hd) out[i] = acc[i];
+    }
 }
 
 // ------------------------------------------------------------------ weight gradient
@@ -260,58 +349,81 @@ __device__ __forceinline__ float lane_sum(float v, int lanes) {
     return v;
 }
 
-template <int KIND, int VB>
+// A pair takes `lanes` neighbouring lanes, a vector of the row each (or several in
+// turn, rows of more than 64 vectors). WHOLE: a lane has one vector at most, so its
+// part of dout stays in registers.
+template <int KIND, int VB, bool FOUR, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void weight_grad_kernel(MemoryGatherParams p, int lanes) {
     using V = BankVec<KIND, VB>;
-    const int per = kThreads / lanes;
-    const int lane = int(threadIdx.x) % lanes;
-    const int64_t q = int64_t(blockIdx.x) * per + int(threadIdx.x) / lanes;
-    const int64_t t = q / p.operands;
-    const int op = int(q - t * p.operands);
-    if (t >= p.tokens) return;
-    const int width = p.width[op];
-    const int idx_bytes = p.idx64 ? 8 : 4;
-    const bool live = is_live(p, t);
+    __shared__ Entry lds[kThreads * kStage];
+    const Pair r = this_pair(p, lanes, lds);
+    if (r.t >= p.tokens) return;
+    const bool live = is_live(p, r.t);
     const int vecs = (p.hd + V::kN - 1) / V::kN;
-    for (int n0 = 0; n0 < width; n0 += kFlight) {
-        float sum[kFlight];
+    const char* bank = static_cast<const char*>(p.bank);
+    const float* dout = (r.op == 0 ? p.dout[0] : p.dout[1]) + r.t * p.hd;
+    void* dw = r.op == 0 ? p.dw[0] : p.dw[1];
+    float g[V::kN] = {};
+    auto load_dout = [&](int v) {
+        const int c0 = v * V::kN;
 #pragma unroll
-        for (int u = 0; u < kFlight; ++u) sum[u] = 0.0f;
-        if (live) {
-            int64_t slot[kFlight];
+        for (int i = 0; i < V::kN; ++i) g[i] = c0 + i < p.hd ? dout[c0 + i] : 0.0f;
+    };
+    if (WHOLE && live && r.lane < vecs) load_dout(r.lane);
+    for (int s0 = 0; s0 < r.width; s0 += kStage * lanes) {
+        const int count = live ? stage<false, FOUR>(p, r, s0) : min(r.width - s0, kStage * lanes);
+        for (int n0 = 0; n0 < count; n0 += kFlight) {
+            float sum[kFlight];
 #pragma unroll
-            for (int u = 0; u < kFlight; ++u) slot[u] = slot_at(p.idx[op], t * width + min(n0 + u, width - 1), idx_bytes);
-            for (int v = lane; v < vecs; v += lanes) {
-                const int c0 = v * V::kN;
-                float g[V::kN];
+            for (int u = 0; u < kFlight; ++u) sum[u] = 0.0f;
+            if (live) {
+                Entry e[kFlight];
 #pragma unroll
-                for (int i = 0; i < V::kN; ++i) g[i] = c0 + i < p.hd ? p.dout[op][t * p.hd + c0 + i] : 0.0f;
-                typename V::Raw raw[kFlight];
-                float s[kFlight];
+                for (int u = 0; u < kFlight; ++u) e[u] = r.entries[min(n0 + u, count - 1)];
+                for (int v = r.lane; v < (WHOLE ? lanes : vecs); v += lanes) {
+                    const int c0 = v * V::kN;
+                    const int at = WHOLE ? min(v, vecs - 1) : v;  // a lane past the row's end has only zeros in g
+                    if (!WHOLE) load_dout(v);
+                    typename V::Raw raw[kFlight];
+                    float s[kFlight];
 #pragma unroll
-                for (int u = 0; u < kFlight; ++u) {
-                    raw[u] = *reinterpret_cast<const typename V::Raw*>(static_cast<const char*>(p.bank) +
-                                                                       slot[u] * p.row_bytes + int64_t(v) * VB);
-                    if (V::kPacked)
-                        s[u] = __uint_as_float(uint32_t(p.scales[slot[u] * p.scale_bytes + c0 / SDM_PACK_BLOCK]) << 23);
-                }
+                    for (int u = 0; u < kFlight; ++u)
+                        raw[u] = *reinterpret_cast<const typename V::Raw*>(bank + e[u].row + int64_t(at) * VB);
+                    if constexpr (V::kPacked && !FOUR) {
 #pragma unroll
-                for (int u = 0; u < kFlight; ++u) {
-                    float x[V::kN];
-                    V::values(raw[u], s[u], x);
+                        for (int u = 0; u < kFlight; ++u)
+                            s[u] = __uint_as_float(uint32_t(p.scales[e[u].row / p.row_bytes * p.scale_bytes +
+                                                                     at * V::kN / SDM_PACK_BLOCK]) << 23);
+                    }
 #pragma unroll
-                    for (int i = 0; i < V::kN; ++i)
-                        if (!V::kPacked || c0 + i < p.hd) sum[u] = fmaf(g[i], x[i], sum[u]);
+                    for (int u = 0; u < kFlight; ++u) {
+                        float x[V::kN];
+                        V::values(raw[u], FOUR ? scale_of(e[u].scales, c0 / SDM_PACK_BLOCK) : s[u], x);
+                        float part = 0;
+                        if (c0 + V::kN <= p.hd) {
+#pragma unroll
+                            for (int i = 0; i < V::kN; ++i) part = fmaf(g[i], x[i], part);
+                        } else {  // columns past the row's end are not looked at: they may hold anything
+#pragma unroll
+                            for (int i = 0; i < V::kN; ++i)
+                                if (c0 + i < p.hd) part = fmaf(g[i], x[i], part);
+                        }
+                        sum[u] += part;
+                    }
                 }
             }
-        }
 #pragma unroll
-        for (int u = 0; u < kFlight; ++u) {
-            const float total = lane_sum(sum[u], lanes);
-            if (lane == u % lanes && n0 + u < width) {
-                const int64_t n = t * width + n0 + u;
-                if (p.w_bf16) static_cast<uint16_t*>(p.dw[op])[n] = to_bf16_rne(total);
-                else static_cast<float*>(p.dw[op])[n] = total;
+            for (int u = 0; u < kFlight; ++u) sum[u] = lane_sum(sum[u], lanes);
+            // Lane u stores entry u, of fewer lanes each its share.
+            for (int at = r.lane; at < kFlight; at += lanes) {
+                float total = sum[0];
+#pragma unroll
+                for (int u = 1; u < kFlight; ++u) total = at == u ? sum[u] : total;
+                if (n0 + at < count) {
+                    const int64_t n = r.t * r.width + s0 + n0 + at;
+                    if (p.w_bf16) static_cast<uint16_t*>(dw)[n] = to_bf16_rne(total);
+                    else static_cast<float*>(dw)[n] = total;
+                }
             }
         }
     }
@@ -323,11 +435,13 @@ int pow2_lanes(int64_t vecs) {
     return lanes;
 }
 
-template <int KIND, int VB> void run_weight_grad(const MemoryGatherParams& p, hipStream_t stream) {
+template <int KIND, int VB, bool FOUR> void run_weight_grad(const MemoryGatherParams& p, hipStream_t stream) {
     using V = BankVec<KIND, VB>;
-    const int lanes = pow2_lanes((p.hd + V::kN - 1) / V::kN);
-    const int64_t per = kThreads / lanes, blocks = (p.tokens * p.operands + per - 1) / per;
-    hipLaunchKernelGGL((weight_grad_kernel<KIND, VB>), dim3(unsigned(blocks)), dim3(kThreads), 0, stream, p, lanes);
+    const int vecs = (p.hd + V::kN - 1) / V::kN, lanes = pow2_lanes(vecs);
+    const int64_t per = kThreads / lanes;
+    const dim3 grid{unsigned((p.tokens * p.operands + per - 1) / per)}, block{unsigned(kThreads)};
+    if (vecs <= lanes) hipLaunchKernelGGL((weight_grad_kernel<KIND, VB, FOUR, true>), grid, block, 0, stream, p, lanes);
+    else hipLaunchKernelGGL((weight_grad_kernel<KIND, VB, FOUR, false>), grid, block, 0, stream, p, lanes);
 }
 
 template <typename E, int VB> void run_pack(const PackParams& p, bool mx4, hipStream_t stream) {
@@ -362,23 +476,29 @@ hipError_t launch_gather_packed(const MemoryGatherParams& p, bool mx4, hipStream
     const int64_t per = kThreads / lanes, blocks = (p.tokens * p.operands + per - 1) / per;
     const int slices = (p.hd + 16 * lanes - 1) / (16 * lanes);
     const dim3 grid{unsigned(blocks), unsigned(slices)}, block{unsigned(kThreads)};
-    if (mx4) hipLaunchKernelGGL(gather_packed_kernel<true>, grid, block, 0, stream, p, lanes);
-    else hipLaunchKernelGGL(gather_packed_kernel<false>, grid, block, 0, stream, p, lanes);
+    const bool four = p.scale_bytes == 4;
+    if (mx4 && four) hipLaunchKernelGGL((gather_packed_kernel<true, true>), grid, block, 0, stream, p, lanes);
+    else if (mx4) hipLaunchKernelGGL((gather_packed_kernel<true, false>), grid, block, 0, stream, p, lanes);
+    else if (four) hipLaunchKernelGGL((gather_packed_kernel<false, true>), grid, block, 0, stream, p, lanes);
+    else hipLaunchKernelGGL((gather_packed_kernel<false, false>), grid, block, 0, stream, p, lanes);
     return hipGetLastError();
 }
 
 hipError_t launch_weight_grad(const MemoryGatherParams& p, int bank_dtype, hipStream_t stream) {
     const uintptr_t at = reinterpret_cast<uintptr_t>(p.bank) | uintptr_t(p.row_bytes);
     const int vb = at % 16 == 0 ? 16 : at % 8 == 0 ? 8 : at % 4 == 0 ? 4 : 2;
-    if (bank_dtype == SDM_MX8) run_weight_grad<SDM_MX8, 16>(p, stream);
-    else if (bank_dtype == SDM_MX4) run_weight_grad<SDM_MX4, 8>(p, stream);
-    else if (bank_dtype == SDM_F32 && vb == 16) run_weight_grad<SDM_F32, 16>(p, stream);
-    else if (bank_dtype == SDM_F32 && vb == 8) run_weight_grad<SDM_F32, 8>(p, stream);
-    else if (bank_dtype == SDM_F32) run_weight_grad<SDM_F32, 4>(p, stream);
-    else if (vb == 16) run_weight_grad<SDM_BF16, 16>(p, stream);
-    else if (vb == 8) run_weight_grad<SDM_BF16, 8>(p, stream);
-    else if (vb == 4) run_weight_grad<SDM_BF16, 4>(p, stream);
-    else run_weight_grad<SDM_BF16, 2>(p, stream);
+    const bool four = p.scale_bytes == 4;
+    if (bank_dtype == SDM_MX8 && four) run_weight_grad<SDM_MX8, 16, true>(p, stream);
+    else if (bank_dtype == SDM_MX8) run_weight_grad<SDM_MX8, 16, false>(p, stream);
+    else if (bank_dtype == SDM_MX4 && four) run_weight_grad<SDM_MX4, 8, true>(p, stream);
+    else if (bank_dtype == SDM_MX4) run_weight_grad<SDM_MX4, 8, false>(p, stream);
+    else if (bank_dtype == SDM_F32 && vb == 16) run_weight_grad<SDM_F32, 16, false>(p, stream);
+    else if (bank_dtype == SDM_F32 && vb == 8) run_weight_grad<SDM_F32, 8, false>(p, stream);
+    else if (bank_dtype == SDM_F32) run_weight_grad<SDM_F32, 4, false>(p, stream);
+    else if (vb == 16) run_weight_grad<SDM_BF16, 16, false>(p, stream);
+    else if (vb == 8) run_weight_grad<SDM_BF16, 8, false>(p, stream);
+    else if (vb == 4) run_weight_grad<SDM_BF16, 4, false>(p, stream);
+    else run_weight_grad<SDM_BF16, 2, false>(p, stream);
     return hipGetLastError();
 }
 
