@@ -25,26 +25,28 @@ def _at(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _check(device: torch.device, name: str, t: torch.Tensor, dtypes, shape):
+def _check(device: int, name: str, t: torch.Tensor, dtypes, shape):
     """A contiguous tensor of the device, of one of the dtypes and of the shape (None: any)."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has unsupported dtype {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call on {device}")
+    if device < 0 or t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the call on device {device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
-def _call(device: torch.device, fn, *args):
+_current_stream = torch._C._cuda_getCurrentRawStream  # the handle alone: a tenth of the stream object's cost
+
+
+def _call(device: int, fn, *args):
     """The library's call on the device's current stream."""
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args, stream)
+    if torch.cuda.current_device() == device:
+        rc = fn(*args, _current_stream(device))
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, stream)
+            rc = fn(*args, _current_stream(device))
     if rc != 0:
         _raise(rc)
 
@@ -79,16 +81,22 @@ def sdm_route(logits: torch.Tensor, k: int, *, score: str = "softmax", bias: Opt
     [streams, keys] and [steps, streams, keys] give what ``sdm_decode_step`` and
     ``sdm_decode_steps`` take. idx and w are allocated (idx_dtype, w_dtype) when not given.
     """
-    dev = logits.device
+    dev = logits.get_device()
     tokens, keys, streams = _route_sizes(logits)
     _check(dev, "logits", logits, _VALUE, None)
     shape = logits.shape[:-1] + (k,)
     if idx is None:
-        idx = torch.empty(shape, dtype=idx_dtype, device=dev)
-    _check(dev, "idx", idx, _INDEX, shape)
+        if idx_dtype not in _INDEX:
+            raise TypeError(f"idx_dtype must be int32 or int64, got {idx_dtype}")
+        idx = torch.empty(shape, dtype=idx_dtype, device=logits.device)
+    else:
+        _check(dev, "idx", idx, _INDEX, shape)
     if w is None:
-        w = torch.empty(shape, dtype=w_dtype, device=dev)
-    _check(dev, "w", w, _VALUE, shape)
+        if w_dtype not in _VALUE:
+            raise TypeError(f"w_dtype must be float32 or bfloat16, got {w_dtype}")
+        w = torch.empty(shape, dtype=w_dtype, device=logits.device)
+    else:
+        _check(dev, "w", w, _VALUE, shape)
     if bias is not None:
         _check(dev, "bias", bias, (torch.float32,), (keys,))
     _call(dev, library().sdm_route, logits.data_ptr(), _DTYPES[logits.dtype], tokens, keys, k, _score(score),
@@ -106,7 +114,7 @@ def sdm_route_backward(logits: torch.Tensor, idx: torch.Tensor, dw: torch.Tensor
     idx as the route gave it, dw [..., k] float32 or bfloat16 the gradient of w; the other
     arguments as in the route.
     """
-    dev = logits.device
+    dev = logits.get_device()
     tokens, keys, streams = _route_sizes(logits)
     _check(dev, "logits", logits, _VALUE, None)
     if idx.dim() < 1:
@@ -119,7 +127,8 @@ def sdm_route_backward(logits: torch.Tensor, idx: torch.Tensor, dw: torch.Tensor
         _check(dev, "bias", bias, (torch.float32,), (keys,))
     if dlogits is None:
         dlogits = torch.empty_like(logits)
-    _check(dev, "dlogits", dlogits, (logits.dtype,), logits.shape)
+    else:
+        _check(dev, "dlogits", dlogits, (logits.dtype,), logits.shape)
     _call(dev, library().sdm_route_backward, logits.data_ptr(), _DTYPES[logits.dtype], tokens, keys, k, _score(score),
           _at(bias), int(normalise), scale, max(streams, 1), stream_slots, idx.data_ptr(), _DTYPES[idx.dtype],
           dw.data_ptr(), _DTYPES[dw.dtype], dlogits.data_ptr())
@@ -139,8 +148,9 @@ class PackedBank:
         if codes.dim() != 2:
             raise ValueError("codes must be [num_slots, row_bytes]")
         self.num_slots, self.head_dim, self.kind, self.device = codes.shape[0], head_dim, kind, codes.device
-        _check(self.device, "codes", codes, (torch.uint8,), (self.num_slots, row))
-        _check(self.device, "scales", scales, (torch.uint8,), (self.num_slots, scale))
+        self._device = codes.get_device()
+        _check(self._device, "codes", codes, (torch.uint8,), (self.num_slots, row))
+        _check(self._device, "scales", scales, (torch.uint8,), (self.num_slots, scale))
         self.codes, self.scales = codes, scales
         self._head = (codes.data_ptr(), scales.data_ptr(), self.dtype, self.num_slots, head_dim)
 
@@ -173,7 +183,7 @@ def sdm_bank_pack(packed: PackedBank, rows: torch.Tensor, *, slots: Optional[tor
     stores nothing; a slot given twice must be given the same row, as with
     ``row_idx = slots`` to bring a packed copy of a bank up to date.
     """
-    dev = packed.device
+    dev = packed._device
     if rows.dim() != 2:
         raise ValueError("rows must be [num_rows, head_dim]")
     _check(dev, "rows", rows, _VALUE, (rows.shape[0], packed.head_dim))
@@ -215,7 +225,7 @@ def sdm_gather_packed(packed: PackedBank, idx0: torch.Tensor, w0: torch.Tensor, 
     """``sdm_gather`` without a stash from a packed bank (``sdm_gather_packed`` of
     include/sdm_memory.h). Returns (out0, out1), float32 [tokens, head_dim]; out1 is None
     without a second operand."""
-    dev = packed.device
+    dev = packed._device
     if (idx1 is None) != (w1 is None):
         raise ValueError("give both idx1 and w1 for a second operand, or neither")
     tokens, width0, width1, valid = _gather_sizes(idx0, idx1, chunk, valid, chunk_valid, dev)
@@ -224,14 +234,15 @@ def sdm_gather_packed(packed: PackedBank, idx0: torch.Tensor, w0: torch.Tensor, 
         _check(dev, "w1", w1, (w0.dtype,), idx1.shape)
     shape = (tokens, packed.head_dim)
     if out0 is None:
-        out0 = torch.empty(shape, dtype=torch.float32, device=dev)
-    _check(dev, "out0", out0, (torch.float32,), shape)
+        out0 = torch.empty(shape, dtype=torch.float32, device=packed.device)
+    else:
+        _check(dev, "out0", out0, (torch.float32,), shape)
     if idx1 is None:
         if out1 is not None:
             raise ValueError("out1 is given without a second operand")
+    elif out1 is None:
+        out1 = torch.empty(shape, dtype=torch.float32, device=packed.device)
     else:
-        if out1 is None:
-            out1 = torch.empty(shape, dtype=torch.float32, device=dev)
         _check(dev, "out1", out1, (torch.float32,), shape)
     _call(dev, library().sdm_gather_packed, *packed._head, tokens, chunk, valid, _at(chunk_valid), _DTYPES[idx0.dtype],
           _DTYPES[w0.dtype], idx0.data_ptr(), w0.data_ptr(), width0, out0.data_ptr(), _at(idx1), _at(w1), width1,
@@ -251,11 +262,14 @@ def sdm_gather_weight_grad(bank: Union[PackedBank, torch.Tensor], idx0: torch.Te
     bank [num_slots, head_dim] float32 or bfloat16, or a PackedBank; idx0, idx1 and the
     padding as in the gather; dout0, dout1 float32 [tokens, head_dim].
     """
-    dev = bank.device
+    if w_dtype not in _VALUE:
+        raise TypeError(f"w_dtype must be float32 or bfloat16, got {w_dtype}")
     if isinstance(bank, PackedBank):
+        dev = bank._device
         head = bank._head
         hd = bank.head_dim
     else:
+        dev = bank.get_device()
         if bank.dim() != 2:
             raise ValueError("bank must be [num_slots, head_dim]")
         _check(dev, "bank", bank, _VALUE, None)
@@ -266,16 +280,18 @@ def sdm_gather_weight_grad(bank: Union[PackedBank, torch.Tensor], idx0: torch.Te
     tokens, width0, width1, valid = _gather_sizes(idx0, idx1, chunk, valid, chunk_valid, dev)
     _check(dev, "dout0", dout0, (torch.float32,), (tokens, hd))
     if dw0 is None:
-        dw0 = torch.empty(idx0.shape, dtype=w_dtype, device=dev)
-    _check(dev, "dw0", dw0, _VALUE, idx0.shape)
+        dw0 = torch.empty(idx0.shape, dtype=w_dtype, device=bank.device)
+    else:
+        _check(dev, "dw0", dw0, _VALUE, idx0.shape)
     if idx1 is None:
         if dw1 is not None:
             raise ValueError("dw1 is given without a second operand")
     else:
         _check(dev, "dout1", dout1, (torch.float32,), (tokens, hd))
         if dw1 is None:
-            dw1 = torch.empty(idx1.shape, dtype=dw0.dtype, device=dev)
-        _check(dev, "dw1", dw1, (dw0.dtype,), idx1.shape)
+            dw1 = torch.empty(idx1.shape, dtype=dw0.dtype, device=bank.device)
+        else:
+            _check(dev, "dw1", dw1, (dw0.dtype,), idx1.shape)
     _call(dev, library().sdm_gather_weight_grad, *head, tokens, chunk, valid, _at(chunk_valid), _DTYPES[idx0.dtype],
           _DTYPES[dw0.dtype], idx0.data_ptr(), dout0.data_ptr(), width0, dw0.data_ptr(), _at(idx1), _at(dout1),
           width1, _at(dw1))

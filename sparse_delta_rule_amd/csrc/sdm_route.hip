@@ -1,13 +1,10 @@
-// The slot router: sdm_route (the k best keys of each token, and their weights)
-// and sdm_route_backward (include/sdm_memory.h).
+// sdm_route (include/sdm_memory.h): the k best keys of each token and their weights.
 
 #include "sdm_route_device.h"
 
 namespace sdm {
 
 namespace {
-
-constexpr int kThreads = 256;
 
 // ------------------------------------------------------------------ few keys: several rows of a wavefront
 
@@ -348,91 +345,6 @@ __global__ __launch_bounds__(64, 5) void route_small_kernel(RouteParams p) {
         if (in_doubt >> (r * LANES) & kRow) exact_small_row<E, kKeys>(p, t0 + r);
 }
 
-// ------------------------------------------------------------------ backward
-
-constexpr int kTile = 4096;  // gradients assembled in LDS at a time
-
-// One workgroup per token: the chosen keys' part in float64, then the row in
-// tiles, each assembled in LDS from the chosen keys and written whole.
-template <typename E>
-__global__ __launch_bounds__(kThreads) void route_backward_kernel(RouteBackwardParams p) {
-    __shared__ double redd[kThreads];
-    __shared__ float redf[kThreads];
-    __shared__ float tile[kTile];
-    ieee_mode_off();
-    const int tid = threadIdx.x;
-    for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
-        const E* row = static_cast<const E*>(p.logits) + t * p.keys;
-        E* drow = static_cast<E*>(p.dlogits) + t * p.keys;
-        const bool whole = p.score == SDM_SOFTMAX && !p.normalise;
-
-        float m = 0, z = 1;
-        if (whole) {
-            float v = -INFINITY;
-            for (int i = tid; i < p.keys; i += kThreads) v = fmaxf(v, logit_at(row, i));
-            m = fmaxf(block_reduce<kThreads>(v, redf, [](float a, float b) { return fmaxf(a, b); }), -FLT_MAX);
-            v = 0;
-            for (int i = tid; i < p.keys; i += kThreads) v += expf(logit_at(row, i) - m);
-            z = block_reduce<kThreads>(v, redf, [](float a, float b) { return a + b; });
-        }
-        int64_t key = -1;
-        double x = -INFINITY, dw = 0;
-        if (tid < p.k) {
-            const int64_t o = t * p.k + tid;
-            key = (p.idx64 ? static_cast<const int64_t*>(p.idx)[o] : int64_t(static_cast<const int32_t*>(p.idx)[o])) -
-                  int64_t(uint32_t(t) % p.streams) * p.stream_slots;
-            if (key < 0 || key >= p.keys) key = -1;
-            if (key >= 0 && !(p.bias != nullptr && bias_excludes(p.bias[key]))) x = logit_at(row, key);
-            dw = p.w_bf16 ? widen(static_cast<const uint16_t*>(p.dw)[o]) : static_cast<const float*>(p.dw)[o];
-        }
-        const bool mine = x > -INFINITY;
-        if (!mine) dw = 0;  // no part in anything, whatever its gradient holds
-        double u = 0;  // score, up to a factor of the row where the weights are normalised
-        if (p.score == SDM_SIGMOID) {
-            if (mine) u = sigmoid64(x);
-        } else if (p.normalise) {
-            const double top = fmax(block_reduce<kThreads>(x, redd, [](double a, double b) { return fmax(a, b); }), -double(FLT_MAX));
-            u = exp(x - top);
-        } else if (mine) {
-            u = exp(x - double(m)) / double(z);
-        }
-        double d = p.scale * dw;
-        if (p.normalise) {
-            const double total = block_reduce<kThreads>(u, redd, [](double a, double b) { return a + b; });
-            u = total > 0 ? u / total : 0.0;
-        }
-        float sum = 0;
-        if (p.normalise || whole) {
-            const double dot = block_reduce<kThreads>(d * u, redd, [](double a, double b) { return a + b; });
-            if (whole) sum = float(dot);
-            else d -= dot;
-        }
-        float g = float(d);  // full softmax: the row below multiplies by s
-        if (!whole) {
-            d *= u;
-            if (p.score == SDM_SIGMOID && mine) d /= 1.0 + exp(x);
-            g = float(d);
-        }
-        for (int a = 0; a < p.keys; a += kTile) {
-            const int n = min(kTile, p.keys - a);
-            __syncthreads();
-            for (int i = tid; i < n; i += kThreads) tile[i] = 0;
-            __syncthreads();
-            if (mine && key >= a && key < a + n) atomicAdd(&tile[key - a], g);
-            __syncthreads();
-            for (int i = tid; i < n; i += kThreads) {
-                float v = tile[i];
-                if (whole) v = z > 0 ? expf(logit_at(row, a + i) - m) / z * (v - sum) : 0.0f;
-                drow[a + i] = narrow<E>(v);
-            }
-        }
-    }
-}
-
-}  // namespace
-
-namespace {
-
 template <typename E, int VPT, int LANES> void run_small(const RouteParams& p, bool vec, hipStream_t stream) {
     const dim3 grid{unsigned((p.tokens + 64 / LANES - 1) / (64 / LANES))}, block{64};
     if constexpr (VPT * sizeof(E) % 16 == 0) {
@@ -474,13 +386,6 @@ template <typename E> void run_route(const RouteParams& p, hipStream_t stream) {
 hipError_t launch_route(const RouteParams& p, bool bf16, hipStream_t stream) {
     if (bf16) run_route<uint16_t>(p, stream);
     else run_route<float>(p, stream);
-    return hipGetLastError();
-}
-
-hipError_t launch_route_backward(const RouteBackwardParams& p, bool bf16, hipStream_t stream) {
-    const dim3 grid{unsigned(p.tokens)}, block{unsigned(kThreads)};
-    if (bf16) hipLaunchKernelGGL(route_backward_kernel<uint16_t>, grid, block, 0, stream, p);
-    else hipLaunchKernelGGL(route_backward_kernel<float>, grid, block, 0, stream, p);
     return hipGetLastError();
 }
 

@@ -53,41 +53,17 @@ template <typename E, int THREADS, int VPT, bool VEC, bool GENERAL>
 __global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL || VPT == 64 ? 4 : VPT <= 8 ? 8 : 6) void route_block_kernel(RouteParams p) {
     __shared__ BlockLds<THREADS, GENERAL> lds;
     constexpr int kWaves = THREADS / 64;
-    constexpr int kN = VEC ? 16 / int(sizeof(E)) : 1;
+    constexpr int kN = RowKeys<E, THREADS, VPT, VEC>::kN;
     ieee_mode_off();
     const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
     const int64_t t = blockIdx.x;
     const E* row = static_cast<const E*>(p.logits) + t * p.keys;
     const bool biased = GENERAL && p.bias != nullptr, softmax = p.score == SDM_SOFTMAX;
     const int size = GENERAL ? p.keys / p.groups : p.keys;
-    auto key_of = [&](int i) { return ((i / kN) * THREADS + tid) * kN + i % kN; };
-    constexpr uint32_t kMinusInf = sizeof(E) == 2 ? 0xff80ff80u : 0xff800000u;
-
+    using Row = RowKeys<E, THREADS, VPT, VEC>;
+    auto key_of = [&](int i) { return Row::key_of(i, tid); };
     float c[VPT];  // the logits, and then what they are chosen by
-    if constexpr (VEC) {
-        uint4 raw[VPT / kN];
-#pragma unroll
-        for (int i = 0; i < VPT / kN; ++i) raw[i] = *reinterpret_cast<const uint4*>(row + min(key_of(i * kN), p.keys - kN));
-#pragma unroll
-        for (int i = 0; i < VPT / kN; ++i) {
-            const uint32_t in = uint32_t((key_of(i * kN) - p.keys) >> 31);  // all ones where the row has the vector
-            uint4 v = raw[i];
-            v.x = (v.x & in) | (kMinusInf & ~in), v.y = (v.y & in) | (kMinusInf & ~in);
-            v.z = (v.z & in) | (kMinusInf & ~in), v.w = (v.w & in) | (kMinusInf & ~in);
-            opaque(v);  // four words chosen, not each key
-            E e[kN];
-            __builtin_memcpy(e, &v, 16);
-#pragma unroll
-            for (int j = 0; j < kN; ++j) c[i * kN + j] = widen(e[j]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) c[i] = widen(row[min(key_of(i), p.keys - 1)]);
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) c[i] = key_of(i) < p.keys ? c[i] : -INFINITY;
-    }
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) c[i] = clean(c[i]);
+    Row::load(row, p.keys, tid, c);
     if (tid == 0) {
         lds.found = 0;
         lds.doubt = 0;

@@ -228,4 +228,43 @@ template <int LANES, typename T, typename F> __device__ __forceinline__ T lanes_
     return v;
 }
 
+// ------------------------------------------------------------------ a row in a workgroup's registers
+
+// VPT keys a lane of a workgroup of THREADS: vectors of 16 bytes, the lanes' side by
+// side (VEC), or one by one.
+template <typename E, int THREADS, int VPT, bool VEC> struct RowKeys {
+    static constexpr int kN = VEC ? 16 / int(sizeof(E)) : 1;
+    static __device__ __forceinline__ int key_of(int i, int tid) { return ((i / kN) * THREADS + tid) * kN + i % kN; }
+
+    // Clean logits; -inf past the row's end.
+    static __device__ __forceinline__ void load(const E* row, int keys, int tid, float (&c)[VPT]) {
+        constexpr uint32_t kMinusInf = sizeof(E) == 2 ? 0xff80ff80u : 0xff800000u;
+        if constexpr (VEC) {
+            uint4 raw[VPT / kN];
+#pragma unroll
+            for (int i = 0; i < VPT / kN; ++i)
+                raw[i] = *reinterpret_cast<const uint4*>(row + min(key_of(i * kN, tid), keys - kN));
+#pragma unroll
+            for (int i = 0; i < VPT / kN; ++i) {
+                const uint32_t in = uint32_t((key_of(i * kN, tid) - keys) >> 31);  // all ones where the row has the vector
+                uint4 v = raw[i];
+                v.x = (v.x & in) | (kMinusInf & ~in), v.y = (v.y & in) | (kMinusInf & ~in);
+                v.z = (v.z & in) | (kMinusInf & ~in), v.w = (v.w & in) | (kMinusInf & ~in);
+                opaque(v);  // four words chosen, not each key
+                E e[kN];
+                __builtin_memcpy(e, &v, 16);
+#pragma unroll
+                for (int j = 0; j < kN; ++j) c[i * kN + j] = widen(e[j]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) c[i] = widen(row[min(key_of(i, tid), keys - 1)]);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) c[i] = key_of(i, tid) < keys ? c[i] : -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) c[i] = clean(c[i]);
+    }
+};
+
 }  // namespace sdm
