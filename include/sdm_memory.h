@@ -95,7 +95,7 @@ int64_t sdm_packed_scale_bytes(int packed_dtype, int64_t head_dim);
  *               must fit the type (SDM_E_RANGE).
  *   w           [tokens, k] SDM_F32 or SDM_BF16 (w_dtype), written.
  * Weights are computed in float64 for the chosen keys (a softmax's sum over all
- * keys in float32 where no bias is given), rounded to float32 and then to w_dtype.
+ * keys in float32), rounded to float32 and then to w_dtype.
  * Errors: SDM_E_DTYPE, SDM_E_SHAPE, SDM_E_RANGE, SDM_E_NULL, SDM_E_ALIGN,
  * SDM_E_OVERLAP, SDM_E_HIP.
  */

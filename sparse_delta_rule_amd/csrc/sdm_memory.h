@@ -7,6 +7,14 @@
 
 namespace sdm {
 
+// Between a wavefront's LDS writes and its reads of what other lanes wrote: its LDS
+// accesses happen in order by themselves, so only the compiler has to keep to it.
+__device__ __forceinline__ void wave_lds_order() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // ------------------------------------------------------------------ route
 struct RouteParams {
     const void* logits;

@@ -132,34 +132,32 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(PackParams p) {
 
 // ------------------------------------------------------------------ gather
 
-// 16 columns of a packed row: their codes, and their values as float32.
-template <bool MX4> struct Codes16;
-template <> struct Codes16<false> {
-    using Raw = uint4;
-    static constexpr int kBytes = 16;
-    static __device__ __forceinline__ void values(const Raw& v, float s, float (&x)[16]) {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// N consecutive columns of a packed row (16, or 4): their codes, and their values as float32.
+template <bool MX4, int N> struct Codes {
+    static constexpr int kBytes = MX4 ? N / 2 : N;
+    using Raw = typename RawVec<kBytes>::T;
+    static __device__ __forceinline__ void values(const Raw& v, float s, float (&x)[N]) {
+        uint32_t w[kBytes < 4 ? 1 : kBytes / 4] = {};
+        __builtin_memcpy(w, &v, kBytes);
+        if constexpr (MX4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const F32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[i], s, false);
-            const F32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[i], s, true);
-            x[4 * i] = a.x, x[4 * i + 1] = a.y, x[4 * i + 2] = b.x, x[4 * i + 3] = b.y;
-        }
-    }
-};
-template <> struct Codes16<true> {
-    using Raw = uint2;
-    static constexpr int kBytes = 8;
-    static __device__ __forceinline__ void values(const Raw& v, float s, float (&x)[16]) {
-        const uint32_t w[2] = {v.x, v.y};
+            for (int i = 0; i < (N + 7) / 8; ++i) {
+                const F32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], s, 0);
+                const F32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], s, 1);
+                x[8 * i] = a.x, x[8 * i + 1] = a.y, x[8 * i + 2] = b.x, x[8 * i + 3] = b.y;
+                if constexpr (N >= 8) {
+                    const F32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], s, 2);
+                    const F32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], s, 3);
+                    x[8 * i + 4] = c.x, x[8 * i + 5] = c.y, x[8 * i + 6] = d.x, x[8 * i + 7] = d.y;
+                }
+            }
+        } else {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const F32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], s, 0);
-            const F32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], s, 1);
-            const F32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], s, 2);
-            const F32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], s, 3);
-            float* y = x + 8 * i;
-            y[0] = a.x, y[1] = a.y, y[2] = b.x, y[3] = b.y, y[4] = c.x, y[5] = c.y, y[6] = d.x, y[7] = d.y;
+            for (int i = 0; i < N / 4; ++i) {
+                const F32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[i], s, false);
+                const F32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[i], s, true);
+                x[4 * i] = a.x, x[4 * i + 1] = a.y, x[4 * i + 2] = b.x, x[4 * i + 3] = b.y;
+            }
         }
     }
 };
@@ -177,9 +175,9 @@ constexpr int kFlight = 8;  // rows of a pair whose loads are in flight together
 // a row of at most four blocks. So a lane's slots, weights and scales cost one load
 // each for a whole row of lanes, and a row one LDS read.
 struct Entry {
-    int64_t row;
+    int64_t row;      // where the row begins (FOUR, and a float bank); else its slot
     float w;
-    uint32_t scales;
+    uint32_t scales;  // FOUR: of the row's blocks
 };
 constexpr int kStage = 8;
 
@@ -192,7 +190,7 @@ struct Pair {
 __device__ __forceinline__ Pair this_pair(const MemoryGatherParams& p, int lanes, Entry* lds) {
     Pair r;
     const int in_block = int(threadIdx.x) / lanes;
-    const int64_t q = int64_t(blockIdx.x) * (kThreads / lanes) + in_block;
+    const int64_t q = int64_t(blockIdx.x) * (int(blockDim.x) / lanes) + in_block;
     r.t = p.operands == 2 ? q >> 1 : q;
     r.op = p.operands == 2 ? int(q & 1) : 0;
     r.lane = int(threadIdx.x) % lanes;
@@ -202,16 +200,15 @@ __device__ __forceinline__ Pair this_pair(const MemoryGatherParams& p, int lanes
     return r;
 }
 
-// Put the pair's entries n0, n0 + 1, ... into LDS (at most kStage * lanes of them);
-// returns how many. A wavefront's LDS accesses happen in order, and the lanes of a
-// pair are in one wavefront.
-template <bool WEIGHTS, bool SCALES>
-__device__ __forceinline__ int stage(const MemoryGatherParams& p, const Pair& r, int n0) {
-    const int count = min(r.width - n0, kStage * r.lanes);
+// Put the pair's entries from n0 up to `end` into LDS (at most kStage * lanes of them);
+// returns how many. The lanes of a pair are in one wavefront.
+template <bool WEIGHTS, bool FOUR, bool OFFSETS>
+__device__ __forceinline__ int stage(const MemoryGatherParams& p, const Pair& r, int n0, int end) {
+    const int count = min(end - n0, kStage * r.lanes);
     const void* idx = r.op == 0 ? p.idx[0] : p.idx[1];
     const void* w = r.op == 0 ? p.w[0] : p.w[1];
     const int64_t first = r.t * r.width + n0;
-    int64_t slot[kStage];
+    int64_t slot[kStage] = {};
     float v[kStage] = {};
     uint32_t sc[kStage] = {};
     if (p.idx64) {
@@ -232,16 +229,16 @@ __device__ __forceinline__ int stage(const MemoryGatherParams& p, const Pair& r,
         for (int i = 0; i < kStage; ++i)
             v[i] = static_cast<const float*>(w)[first + min(i * r.lanes + r.lane, count - 1)];
     }
-    if (SCALES) {
+    if (FOUR) {
 #pragma unroll
         for (int i = 0; i < kStage; ++i) sc[i] = reinterpret_cast<const uint32_t*>(p.scales)[slot[i]];
     }
 #pragma unroll
     for (int i = 0; i < kStage; ++i) {
         const int n = i * r.lanes + r.lane;
-        if (n < count) r.entries[n] = Entry{slot[i] * p.row_bytes, v[i], sc[i]};
+        if (n < count) r.entries[n] = Entry{OFFSETS ? slot[i] * p.row_bytes : slot[i], v[i], sc[i]};
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_order();
     return count;
 }
 
@@ -250,46 +247,47 @@ __device__ __forceinline__ float scale_of(uint32_t four, int block) {
     return __uint_as_float(four >> (8 * block) << 23 & 0x7f800000u);
 }
 
-// A pair takes `lanes` neighbouring lanes, 16 columns each. FOUR: a row has at most
+// A pair takes `lanes` neighbouring lanes, N columns each. FOUR: a row has at most
 // four blocks, whose scales come with the entry.
-template <bool MX4, bool FOUR>
+template <bool MX4, bool FOUR, int N>
 __global__ __launch_bounds__(kThreads) void gather_packed_kernel(MemoryGatherParams p, int lanes) {
-    using C = Codes16<MX4>;
-    __shared__ Entry lds[kThreads * kStage];
+    using C = Codes<MX4, N>;
+    constexpr int kAhead = N == 16 ? kFlight : 2 * kFlight;  // rows in flight
+    extern __shared__ Entry lds[];
     const Pair r = this_pair(p, lanes, lds);
     if (r.t >= p.tokens) return;
-    const int c0 = 16 * (int(blockIdx.y) * lanes + r.lane);
+    const int c0 = N * (int(blockIdx.y) * lanes + r.lane);
     const int block = c0 / SDM_PACK_BLOCK;
-    float acc[16];
+    float acc[N];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
     if (is_live(p, r.t)) {
         // A lane past the row's end reads its last columns.
-        const int vec = min(c0 / 16, (p.hd - 1) / 16);
+        const int vec = min(c0 / N, (p.hd - 1) / N);
         const char* codes = static_cast<const char*>(p.bank) + vec * C::kBytes;
         const uint8_t* scales = p.scales + min(block, (p.hd - 1) / SDM_PACK_BLOCK);
         for (int s0 = 0; s0 < r.width; s0 += kStage * lanes) {
-            const int count = stage<true, FOUR>(p, r, s0);
-            for (int n0 = 0; n0 < count; n0 += kFlight) {
-                typename C::Raw raw[kFlight];
-                Entry e[kFlight];
-                float s[kFlight];
+            const int count = stage<true, FOUR, FOUR>(p, r, s0, r.width);
+            for (int n0 = 0; n0 < count; n0 += kAhead) {
+                typename C::Raw raw[kAhead];
+                Entry e[kAhead];
+                float s[kAhead];
 #pragma unroll
-                for (int u = 0; u < kFlight; ++u) e[u] = r.entries[min(n0 + u, count - 1)];
+                for (int u = 0; u < kAhead; ++u) e[u] = r.entries[min(n0 + u, count - 1)];
 #pragma unroll
-                for (int u = 0; u < kFlight; ++u) raw[u] = *reinterpret_cast<const typename C::Raw*>(codes + e[u].row);
+                for (int u = 0; u < kAhead; ++u) raw[u] = *reinterpret_cast<const typename C::Raw*>(codes + e[u].row * (FOUR ? 1 : p.row_bytes));
                 if constexpr (!FOUR) {
 #pragma unroll
-                    for (int u = 0; u < kFlight; ++u)
-                        s[u] = __uint_as_float(uint32_t(scales[e[u].row / p.row_bytes * p.scale_bytes]) << 23);
+                    for (int u = 0; u < kAhead; ++u)
+                        s[u] = __uint_as_float(uint32_t(scales[e[u].row * p.scale_bytes]) << 23);
                 }
 #pragma unroll
-                for (int u = 0; u < kFlight; ++u) {
+                for (int u = 0; u < kAhead; ++u) {
                     if (n0 + u < count) {
-                        float x[16];
+                        float x[N];
                         C::values(raw[u], FOUR ? scale_of(e[u].scales, block) : s[u], x);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) acc[i] = fmaf(e[u].w, x[i], acc[i]);
+                        for (int i = 0; i < N; ++i) acc[i] = fmaf(e[u].w, x[i], acc[i]);
                     }
                 }
             }
@@ -297,13 +295,13 @@ __global__ __launch_bounds__(kThreads) void gather_packed_kernel(MemoryGatherPar
     }
     if (c0 >= p.hd) return;
     float* out = (r.op == 0 ? p.out[0] : p.out[1]) + r.t * p.hd + c0;
-    if (c0 + 16 <= p.hd && p.out_vec) {
+    if (c0 + N <= p.hd && p.out_vec) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < N / 4; ++i)
             reinterpret_cast<float4*>(out)[i] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int i = 0; i < N; ++i)
             if (c0 + i < p.hd) out[i] = acc[i];
     }
 }
@@ -329,11 +327,11 @@ template <int VB> struct BankVec<SDM_BF16, VB> {
         for (int i = 0; i < kN; ++i) x[i] = widen(e[i]);
     }
 };
-template <> struct BankVec<SDM_MX8, 16> : Codes16<false> {
+template <> struct BankVec<SDM_MX8, 16> : Codes<false, 16> {
     static constexpr int kN = 16;
     static constexpr bool kPacked = true;
 };
-template <> struct BankVec<SDM_MX4, 8> : Codes16<true> {
+template <> struct BankVec<SDM_MX4, 8> : Codes<true, 16> {
     static constexpr int kN = 16;
     static constexpr bool kPacked = true;
 };
@@ -350,14 +348,17 @@ __device__ __forceinline__ float lane_sum(float v, int lanes) {
 }
 
 // A pair takes `lanes` neighbouring lanes, a vector of the row each (or several in
-// turn, rows of more than 64 vectors). WHOLE: a lane has one vector at most, so its
+// turn, rows of more than 64 vectors), for the entries of one segment of the width.
+// WHOLE: a lane has one vector at most, so its
 // part of dout stays in registers.
 template <int KIND, int VB, bool FOUR, bool WHOLE>
-__global__ __launch_bounds__(kThreads) void weight_grad_kernel(MemoryGatherParams p, int lanes) {
+__global__ __launch_bounds__(kThreads) void weight_grad_kernel(MemoryGatherParams p, int lanes, int per_segment) {
     using V = BankVec<KIND, VB>;
-    __shared__ Entry lds[kThreads * kStage];
+    constexpr bool kOffsets = FOUR || !V::kPacked;
+    extern __shared__ Entry lds[];
     const Pair r = this_pair(p, lanes, lds);
     if (r.t >= p.tokens) return;
+    const int begin = int(blockIdx.y) * per_segment, end = min(begin + per_segment, r.width);
     const bool live = is_live(p, r.t);
     const int vecs = (p.hd + V::kN - 1) / V::kN;
     const char* bank = static_cast<const char*>(p.bank);
@@ -370,8 +371,8 @@ __global__ __launch_bounds__(kThreads) void weight_grad_kernel(MemoryGatherParam
         for (int i = 0; i < V::kN; ++i) g[i] = c0 + i < p.hd ? dout[c0 + i] : 0.0f;
     };
     if (WHOLE && live && r.lane < vecs) load_dout(r.lane);
-    for (int s0 = 0; s0 < r.width; s0 += kStage * lanes) {
-        const int count = live ? stage<false, FOUR>(p, r, s0) : min(r.width - s0, kStage * lanes);
+    for (int s0 = begin; s0 < end; s0 += kStage * lanes) {
+        const int count = live ? stage<false, FOUR, kOffsets>(p, r, s0, end) : min(end - s0, kStage * lanes);
         for (int n0 = 0; n0 < count; n0 += kFlight) {
             float sum[kFlight];
 #pragma unroll
@@ -388,12 +389,11 @@ __global__ __launch_bounds__(kThreads) void weight_grad_kernel(MemoryGatherParam
                     float s[kFlight];
 #pragma unroll
                     for (int u = 0; u < kFlight; ++u)
-                        raw[u] = *reinterpret_cast<const typename V::Raw*>(bank + e[u].row + int64_t(at) * VB);
+                        raw[u] = *reinterpret_cast<const typename V::Raw*>(bank + e[u].row * (kOffsets ? 1 : p.row_bytes) + int64_t(at) * VB);
                     if constexpr (V::kPacked && !FOUR) {
 #pragma unroll
                         for (int u = 0; u < kFlight; ++u)
-                            s[u] = __uint_as_float(uint32_t(p.scales[e[u].row / p.row_bytes * p.scale_bytes +
-                                                                     at * V::kN / SDM_PACK_BLOCK]) << 23);
+                            s[u] = __uint_as_float(uint32_t(p.scales[e[u].row * p.scale_bytes + at * V::kN / SDM_PACK_BLOCK]) << 23);
                     }
 #pragma unroll
                     for (int u = 0; u < kFlight; ++u) {
@@ -435,13 +435,45 @@ int pow2_lanes(int64_t vecs) {
     return lanes;
 }
 
+// Wavefronts that a launch wants at least: 4 on each of the 256 CUs.
+constexpr int64_t kManyWaves = 1024;
+
+struct PairGrid {
+    dim3 grid, block;
+    size_t lds;
+};
+// Workgroups of one wavefront where there are few, so that they spread over the card.
+PairGrid pair_grid(const MemoryGatherParams& p, int lanes, int rows_of_grid) {
+    const int64_t waves = (p.tokens * p.operands * lanes + 63) / 64 * rows_of_grid;
+    const int threads = waves < 2 * kManyWaves ? 64 : kThreads, per = threads / lanes;
+    return {dim3(unsigned((p.tokens * p.operands + per - 1) / per), unsigned(rows_of_grid)), dim3(unsigned(threads)),
+            size_t(threads) * kStage * sizeof(Entry)};
+}
+
 template <int KIND, int VB, bool FOUR> void run_weight_grad(const MemoryGatherParams& p, hipStream_t stream) {
     using V = BankVec<KIND, VB>;
     const int vecs = (p.hd + V::kN - 1) / V::kN, lanes = pow2_lanes(vecs);
-    const int64_t per = kThreads / lanes;
-    const dim3 grid{unsigned((p.tokens * p.operands + per - 1) / per)}, block{unsigned(kThreads)};
-    if (vecs <= lanes) hipLaunchKernelGGL((weight_grad_kernel<KIND, VB, FOUR, true>), grid, block, 0, stream, p, lanes);
-    else hipLaunchKernelGGL((weight_grad_kernel<KIND, VB, FOUR, false>), grid, block, 0, stream, p, lanes);
+    // Few pairs: the entries of each are split over wavefronts, kFlight at least a piece.
+    const int widest = p.operands == 2 && p.width[1] > p.width[0] ? p.width[1] : p.width[0];
+    const int64_t waves = (p.tokens * p.operands * lanes + 63) / 64;
+    int segments = (widest + kFlight - 1) / kFlight;
+    if (waves * segments > kManyWaves) segments = waves >= kManyWaves ? 1 : int(kManyWaves / waves);
+    const int per_segment = ((widest + segments - 1) / segments + kFlight - 1) / kFlight * kFlight;
+    const PairGrid g = pair_grid(p, lanes, (widest + per_segment - 1) / per_segment);
+    if (vecs <= lanes)
+        hipLaunchKernelGGL((weight_grad_kernel<KIND, VB, FOUR, true>), g.grid, g.block, g.lds, stream, p, lanes, per_segment);
+    else
+        hipLaunchKernelGGL((weight_grad_kernel<KIND, VB, FOUR, false>), g.grid, g.block, g.lds, stream, p, lanes, per_segment);
+}
+
+template <int N> void run_gather_packed(const MemoryGatherParams& p, bool mx4, hipStream_t stream) {
+    const int lanes = pow2_lanes((p.hd + N - 1) / N);
+    const PairGrid g = pair_grid(p, lanes, (p.hd + N * lanes - 1) / (N * lanes));
+    const bool four = p.scale_bytes == 4;
+    if (mx4 && four) hipLaunchKernelGGL((gather_packed_kernel<true, true, N>), g.grid, g.block, g.lds, stream, p, lanes);
+    else if (mx4) hipLaunchKernelGGL((gather_packed_kernel<true, false, N>), g.grid, g.block, g.lds, stream, p, lanes);
+    else if (four) hipLaunchKernelGGL((gather_packed_kernel<false, true, N>), g.grid, g.block, g.lds, stream, p, lanes);
+    else hipLaunchKernelGGL((gather_packed_kernel<false, false, N>), g.grid, g.block, g.lds, stream, p, lanes);
 }
 
 template <typename E, int VB> void run_pack(const PackParams& p, bool mx4, hipStream_t stream) {
@@ -472,15 +504,11 @@ hipError_t launch_pack(const PackParams& p, bool bf16, bool mx4, hipStream_t str
 }
 
 hipError_t launch_gather_packed(const MemoryGatherParams& p, bool mx4, hipStream_t stream) {
-    const int lanes = pow2_lanes((p.hd + 15) / 16);
-    const int64_t per = kThreads / lanes, blocks = (p.tokens * p.operands + per - 1) / per;
-    const int slices = (p.hd + 16 * lanes - 1) / (16 * lanes);
-    const dim3 grid{unsigned(blocks), unsigned(slices)}, block{unsigned(kThreads)};
-    const bool four = p.scale_bytes == 4;
-    if (mx4 && four) hipLaunchKernelGGL((gather_packed_kernel<true, true>), grid, block, 0, stream, p, lanes);
-    else if (mx4) hipLaunchKernelGGL((gather_packed_kernel<true, false>), grid, block, 0, stream, p, lanes);
-    else if (four) hipLaunchKernelGGL((gather_packed_kernel<false, true>), grid, block, 0, stream, p, lanes);
-    else hipLaunchKernelGGL((gather_packed_kernel<false, false>), grid, block, 0, stream, p, lanes);
+    // Few pairs: 4 columns a lane instead of 16, four times the wavefronts and twice the
+    // rows in flight (an element's chain of additions is one lane's in either).
+    const int64_t waves = p.tokens * p.operands * ((p.hd + 15) / 16) / 64;
+    if (waves < kManyWaves && p.hd <= 4096) run_gather_packed<4>(p, mx4, stream);
+    else run_gather_packed<16>(p, mx4, stream);
     return hipGetLastError();
 }
 

@@ -20,57 +20,65 @@ __device__ __forceinline__ float value_slack(bool softmax, float c) {
 // And relatively, of a score's own, x from where its exponent is 0.
 __device__ __forceinline__ float score_slack(float x) { return (4.0f + fabsf(x)) * 0x1p-22f; }
 
-// One row by one wavefront, KEYS / 64 keys a lane, every value in float64.
-template <typename E, int KEYS> __device__ __forceinline__ void exact_small_row(const RouteParams& p, int64_t t) {
+// One row by one wavefront, KEYS / 64 keys a lane, every value in float64 and in LDS:
+// it runs for few rows, and its registers would cost all of them occupancy.
+template <int KEYS> struct ExactSmallLds {
+    double value[KEYS];  // score + bias, or the score
+    float x[KEYS];       // -inf where the key is not eligible
+};
+template <typename E, int KEYS>
+__device__ __forceinline__ void exact_small_row(const RouteParams& p, int64_t t, ExactSmallLds<KEYS>& lds) {
     constexpr int N = KEYS / 64;
     const int lane = threadIdx.x, size = p.keys / p.groups;
     const E* row = static_cast<const E*>(p.logits) + t * p.keys;
     const bool biased = p.bias != nullptr, softmax = p.score == SDM_SOFTMAX;
     auto all = [](double v, auto f) {
+#pragma unroll 1
         for (int n = 1; n < 64; n *= 2) v = f(v, __shfl_xor(v, n));
         return v;
     };
     const auto larger = [](double a, double b) { return fmax(a, b); };
     const auto plus = [](double a, double b) { return a + b; };
-    double x[N], s[N], c[N];
+    // A lane reads and writes its own keys alone.
+    auto x = [&](int i) -> float& { return lds.x[i * 64 + lane]; };
+    auto v = [&](int i) -> double& { return lds.value[i * 64 + lane]; };
     uint32_t gone = 0;  // bit i: key i of the lane cannot be chosen (any more)
     double m = -FLT_MAX, z = 0;
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < N; ++i) {
         const int n = i * 64 + lane;
-        x[i] = n < p.keys ? double(logit_at(row, n)) : -INFINITY;
+        x(i) = n < p.keys ? logit_at(row, n) : -INFINITY;
         if (n >= p.keys) gone |= 1u << i;
-        m = fmax(m, x[i]);
+        m = fmax(m, double(x(i)));
     }
     m = all(m, larger);
-#pragma unroll
+    auto raw_score = [&](float a) { return softmax ? exp(double(a) - m) : sigmoid64(a); };
+#pragma unroll 1
     for (int i = 0; i < N; ++i) {
-        s[i] = softmax ? exp(x[i] - m) : sigmoid64(x[i]);
-        z += s[i];
+        v(i) = raw_score(x(i));
+        z += v(i);
     }
-    z = all(z, plus);
-#pragma unroll
+    z = softmax ? all(z, plus) : 1.0;
+#pragma unroll 1
     for (int i = 0; i < N; ++i) {
-        const int n = min(i * 64 + lane, p.keys - 1);
-        const float b = biased ? p.bias[n] : 0.0f;
-        if (softmax) s[i] = z > 0 ? s[i] / z : 0.0;
-        const bool ok = x[i] > -INFINITY && !bias_excludes(b);
-        if (!ok) x[i] = -INFINITY;
-        c[i] = !ok ? -INFINITY : biased ? s[i] + double(b) : x[i];
+        const float b = biased ? p.bias[min(i * 64 + lane, p.keys - 1)] : 0.0f;
+        if (bias_excludes(b)) x(i) = -INFINITY;
+        v(i) = x(i) > -INFINITY ? v(i) / z + double(b) : -INFINITY;
     }
     if (p.groups > 1) {
         double mine = 0;
+#pragma unroll 1
         for (int g = 0; g < p.groups; ++g) {
             double hi = -INFINITY, lo = -INFINITY;
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < N; ++i) {
                 const int n = i * 64 + lane;
-                if (n / size == g && n < p.keys && x[i] > -INFINITY) {
-                    const double v = biased ? c[i] : s[i];
-                    lo = fmax(lo, fmin(hi, v));
-                    hi = fmax(hi, v);
+                if (n / size == g && n < p.keys) {
+                    lo = fmax(lo, fmin(hi, v(i)));
+                    hi = fmax(hi, v(i));
                 }
             }
+#pragma unroll 1
             for (int n = 1; n < 64; n *= 2) {
                 const double h = __shfl_xor(hi, n), w = __shfl_xor(lo, n);
                 lo = fmax(fmax(lo, w), fmin(hi, h));
@@ -84,43 +92,43 @@ template <typename E, int KEYS> __device__ __forceinline__ void exact_small_row(
             rank += other > mine || (other == mine && g < lane);
         }
         const uint64_t kept = __ballot(lane < p.groups && rank < p.kept);
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < N; ++i)
             if (i * 64 + lane < p.keys && !(kept >> ((i * 64 + lane) / size) & 1)) gone |= 1u << i;
     }
     int key = 0;
-    double xk = -INFINITY, sk = 0;  // of the lane's choice: lane j has the j-th
+    float xk = -INFINITY;  // of the lane's choice: lane j has the j-th
+#pragma unroll 1
     for (int j = 0; j < p.k; ++j) {
         Ranked best = {-INFINITY, 0x7fffffff};
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < N; ++i) {
-            const Ranked r = {c[i], i * 64 + lane};
+            const Ranked r = {biased ? v(i) : double(x(i)), i * 64 + lane};
             if (!(gone >> i & 1) && before(r, best)) best = r;
         }
+#pragma unroll 1
         for (int n = 1; n < 64; n *= 2) {
             const Ranked o = {__shfl_xor(best.c, n), __shfl_xor(best.key, n)};
             if (before(o, best)) best = o;
         }
-        double xb = 0, sb = 0;
-#pragma unroll
+        float xb = 0;
+#pragma unroll 1
         for (int i = 0; i < N; ++i)
             if (best.key == i * 64 + lane) {
                 gone |= 1u << i;
-                xb = x[i];
-                sb = s[i];
+                xb = x(i);
             }
         xb = __shfl(xb, best.key % 64);
-        sb = __shfl(sb, best.key % 64);
         if (lane == j) {
             key = best.key;
             xk = xb;
-            sk = xb > -INFINITY ? sb : 0.0;
         }
     }
+    double sk = xk > -INFINITY ? raw_score(xk) / z : 0.0;
     if (p.normalise) {
         if (softmax) {
-            const double top = all(fmax(xk, -double(FLT_MAX)), larger);
-            sk = xk > -INFINITY ? exp(xk - top) : 0.0;
+            const double top = all(fmax(double(xk), -double(FLT_MAX)), larger);
+            sk = xk > -INFINITY ? exp(double(xk) - top) : 0.0;
         }
         const double total = all(sk, plus);
         sk = total > 0 ? sk / total : 0.0;
@@ -128,10 +136,15 @@ template <typename E, int KEYS> __device__ __forceinline__ void exact_small_row(
     if (lane < p.k) store_choice(p, t, lane, key, sk);
 }
 
-template <int LANES> struct SmallLds {
-    double value[64], score[64];
-    int key[64];
-    float worth[64], slack[64];
+template <int KEYS> struct SmallLds {
+    union {
+        struct {
+            double value[64], score[64];
+            int key[64];
+            float worth[64], slack[64];
+        };
+        ExactSmallLds<KEYS> exact;
+    };
 };
 
 // One wavefront a workgroup, 64 / LANES rows of it, VPT consecutive keys a lane.
@@ -142,10 +155,10 @@ template <int LANES> struct SmallLds {
 // leading bits cannot show that the candidates hold the k best, or the groups'
 // order is in doubt, the row is done again by exact_small_row.
 template <typename E, int VPT, int LANES, bool VEC>
-__global__ __launch_bounds__(64, 5) void route_small_kernel(RouteParams p) {
-    __shared__ SmallLds<LANES> lds;
+__global__ __launch_bounds__(64, 8) void route_small_kernel(RouteParams p) {
     constexpr int kRows = 64 / LANES;
     constexpr int kKeys = VPT * LANES;
+    __shared__ SmallLds<kKeys> lds;
     constexpr int kBits = kKeys <= 64 ? 6 : kKeys <= 128 ? 7 : kKeys <= 256 ? 8 : kKeys <= 512 ? 9 : 10;
     constexpr uint32_t kMask = (1u << kBits) - 1;
     ieee_mode_off();
@@ -263,7 +276,41 @@ __global__ __launch_bounds__(64, 5) void route_small_kernel(RouteParams p) {
             not_below += (h != g) & (exact ? ahead : !(other < worth - far));
         }
         mine_kept = not_below < p.kept;
-        if (g < p.groups) doubt = not_below >= p.kept && above < p.kept;
+        if (__ballot(g < p.groups && not_below >= p.kept && above < p.kept) != 0) {
+            // Some group of the wavefront's rows is in doubt (of 32768 rows in 8 groups, 5): the
+            // same in float64, a softmax's sum with it.
+            double sum = 0, most = -INFINITY, next = -INFINITY;
+            const double at = softmax ? lanes_reduce<LANES>(max_of(x, -FLT_MAX), [](float a, float d) { return max32(a, d); }) : 0.0f;
+            auto score = [&](float a) { return softmax ? exp(double(a) - at) : sigmoid64(a); };
+            if (biased && softmax) {
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) sum += score(x[i]);
+                for (int n = 1; n < LANES; n *= 2) sum += __shfl_xor(sum, n);
+            } else {
+                sum = 1;
+            }
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const double v = c[i] > -INFINITY ? score(x[i]) / sum + (biased ? double(b[i]) : 0.0) : -INFINITY;
+                next = fmax(next, fmin(most, v));
+                most = fmax(most, v);
+            }
+            for (int n = 1; n < of_group; n *= 2) {
+                const double h = __shfl_xor(most, n), w = __shfl_xor(next, n);
+                next = fmax(fmax(next, w), fmin(most, h));
+                most = fmax(most, h);
+            }
+            const double exactly = p.top == 2 && next > -INFINITY ? most + next : most;
+            __syncthreads();
+            if (l % of_group == 0 && g < p.groups) lds.value[first + g] = exactly;
+            __syncthreads();
+            int rank = 0;
+            for (int h = 0; h < p.groups; ++h) {
+                const double other = lds.value[first + h];
+                rank += (other > exactly) | ((other == exactly) & (h < g));
+            }
+            mine_kept = rank < p.kept;
+        }
     }
     uint32_t key[VPT];
 #pragma unroll
@@ -342,7 +389,10 @@ __global__ __launch_bounds__(64, 5) void route_small_kernel(RouteParams p) {
     const uint64_t in_doubt = __ballot(doubt && row_there);
     if (chosen && row_there && !(in_doubt >> first & kRow)) store_choice(p, t, rank, n, u);
     for (int r = 0; r < kRows; ++r)
-        if (in_doubt >> (r * LANES) & kRow) exact_small_row<E, kKeys>(p, t0 + r);
+        if (in_doubt >> (r * LANES) & kRow) {
+            __syncthreads();
+            exact_small_row<E, kKeys>(p, t0 + r, lds.exact);
+        }
 }
 
 template <typename E, int VPT, int LANES> void run_small(const RouteParams& p, bool vec, hipStream_t stream) {
@@ -362,10 +412,15 @@ template <typename E, int LANES> void run_small(const RouteParams& p, int vpt, b
     else run_small<E, 16, LANES>(p, vec, stream);
 }
 
+constexpr int64_t kFewTokens = 1024;
+
 template <typename E> void run_route(const RouteParams& p, hipStream_t stream) {
-    // 16 keys a lane at most, and a lane for each candidate.
+    // A lane for each candidate, and 16 keys a lane at most; of few tokens, 4 keys a lane:
+    // a wavefront alone is as fast as its lanes are short (one token of 256 keys: 7.5 us
+    // with 16 lanes of 16 keys, 6.3 with 64 of 4), and the card is not full either way.
+    const int most = p.tokens <= kFewTokens ? 4 : 16;
     int lanes = 16;
-    while (lanes < 64 && (lanes * 16 < p.keys || lanes < p.k + kSpare)) lanes *= 2;
+    while (lanes < 64 && (lanes * most < p.keys || lanes < p.k + kSpare)) lanes *= 2;
     int vpt = 4;
     while (vpt < 16 && lanes * vpt < p.keys) vpt *= 2;
     const int size = p.keys / p.groups;

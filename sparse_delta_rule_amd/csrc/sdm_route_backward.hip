@@ -90,13 +90,13 @@ __global__ __launch_bounds__(64 * kWaves) void route_backward_sparse_kernel(Rout
     for (int a = 0; a < whole; a += kTile) {
         const int n = min(kTile, whole - a);
         for (int i = lane * 4; i < n; i += 256) *reinterpret_cast<float4*>(tile + i) = make_float4(0, 0, 0, 0);
-        __builtin_amdgcn_wave_barrier();  // a wavefront's LDS accesses happen in order
+        wave_lds_order();
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int at = r * p.keys + c[i].key - a;
             if (c[i].key >= 0 && at >= 0 && at < n) atomicAdd(tile + at, g[i]);
         }
-        __builtin_amdgcn_wave_barrier();
+        wave_lds_order();
         constexpr int kN = 16 / int(sizeof(E));
         E* to = out + a;
         if (reinterpret_cast<uintptr_t>(to) % 16 == 0) {
@@ -110,7 +110,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_backward_sparse_kernel(Rout
         } else {
             for (int i = lane; i < n; i += 64) to[i] = narrow<E>(tile[i]);
         }
-        __builtin_amdgcn_wave_barrier();
+        wave_lds_order();
     }
 }
 
