@@ -142,6 +142,7 @@ template <int KEYS> struct SmallLds {
             double value[64], score[64];
             int key[64];
             float worth[64], slack[64];
+            uint32_t group_max[64], group_next[64];
         };
         ExactSmallLds<KEYS> exact;
     };
@@ -155,7 +156,7 @@ template <int KEYS> struct SmallLds {
 // leading bits cannot show that the candidates hold the k best, or the groups'
 // order is in doubt, the row is done again by exact_small_row.
 template <typename E, int VPT, int LANES, bool VEC>
-__global__ __launch_bounds__(64, 8) void route_small_kernel(RouteParams p) {
+__global__ __launch_bounds__(64, 6) void route_small_kernel(RouteParams p) {
     constexpr int kRows = 64 / LANES;
     constexpr int kKeys = VPT * LANES;
     __shared__ SmallLds<kKeys> lds;
@@ -224,25 +225,60 @@ __global__ __launch_bounds__(64, 8) void route_small_kernel(RouteParams p) {
         for (int i = 0; i < VPT; ++i) c[i] = x[i];
     }
     bool doubt = false;
-    bool mine_kept = true;
+    bool mine_kept = true;         // this lane's keys, where a group is whole lanes
+    uint64_t kept_groups = ~0ull;  // of the row, where it is not
+    // A group of whole lanes, a power of two of them, is put together by those lanes;
+    // others in LDS, and lane g of the row has group g.
+    const bool whole = size % VPT == 0 && (size / VPT & (size / VPT - 1)) == 0;
+    const float per_size = 1.0f / float(size);
+    auto group_of = [&](int n) { return int((float(n) + 0.5f) * per_size); };  // exact: n is far below 2^16
     if (p.groups > 1) {
-        const int of_group = size / VPT;  // lanes of a group: a power of two
-        float hi = -INFINITY, lo = -INFINITY;  // the two largest
+        const int of_group = whole ? size / VPT : 1;  // lanes of a group
+        float hi = -INFINITY, lo = -INFINITY;          // the two largest
         auto add = [&](float v) {
             lo = median32(hi, lo, v);
             hi = max32(hi, v);
         };
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) add(c[i]);
         auto merge = [&](float h, float w) {
             add(h);
             lo = max32(lo, w);  // w <= h: above hi only if h was
         };
-        if (of_group > 1) merge(dpp<kXor1>(hi), dpp<kXor1>(lo));
-        if (of_group > 2) merge(dpp<kXor2>(hi), dpp<kXor2>(lo));
-        if (of_group > 4) merge(dpp<kHalfMirror>(hi), dpp<kHalfMirror>(lo));
-        if (of_group > 8) merge(dpp<kMirror>(hi), dpp<kMirror>(lo));
-        if (of_group > 16) merge(__shfl_xor(hi, 16), __shfl_xor(lo, 16));
+        if (whole) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) add(c[i]);
+            if (of_group > 1) merge(dpp<kXor1>(hi), dpp<kXor1>(lo));
+            if (of_group > 2) merge(dpp<kXor2>(hi), dpp<kXor2>(lo));
+            if (of_group > 4) merge(dpp<kHalfMirror>(hi), dpp<kHalfMirror>(lo));
+            if (of_group > 8) merge(dpp<kMirror>(hi), dpp<kMirror>(lo));
+            if (of_group > 16) merge(__shfl_xor(hi, 16), __shfl_xor(lo, 16));
+        } else {
+            lds.group_max[tid] = lds.group_next[tid] = 0;
+            __syncthreads();
+            int at = group_of(l * VPT);
+            // Every value but the largest is at some time the smaller of a maximum and what
+            // it replaced, so the second largest gets there too.
+            auto put_down = [&] {
+                if (hi > -INFINITY) {
+                    const uint32_t h = ordered(hi);
+                    const uint32_t w = max(ordered(lo), min(h, atomicMax(&lds.group_max[first + at], h)));
+                    if (w > kOut) atomicMax(&lds.group_next[first + at], w);
+                }
+                hi = lo = -INFINITY;
+            };
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int g = group_of(l * VPT + i);  // past the end only -inf is added, and put down nowhere
+                if (g != at) {
+                    put_down();
+                    at = g;
+                }
+                add(c[i]);
+            }
+            put_down();
+            __syncthreads();
+            hi = lds.group_max[tid] > kOut ? from_ordered(lds.group_max[tid]) : -INFINITY;
+            lo = lds.group_next[tid] > kOut ? from_ordered(lds.group_next[tid]) : -INFINITY;
+        }
         // Without a bias and with one value a group, the order of the logits is exact.
         const bool exact_worth = !biased && p.top == 1;
         float worth = hi, slack = 0;
@@ -276,7 +312,12 @@ __global__ __launch_bounds__(64, 8) void route_small_kernel(RouteParams p) {
             not_below += (h != g) & (exact ? ahead : !(other < worth - far));
         }
         mine_kept = not_below < p.kept;
-        if (__ballot(g < p.groups && not_below >= p.kept && above < p.kept) != 0) {
+        const bool unsure = g < p.groups && not_below >= p.kept && above < p.kept;
+        if (!whole) {
+            kept_groups = __ballot(g < p.groups && not_below < p.kept) >> first;
+            mine_kept = true;
+            doubt = unsure;
+        } else if (__ballot(unsure) != 0) {
             // Some group of the wavefront's rows is in doubt (of 32768 rows in 8 groups, 5): the
             // same in float64, a softmax's sum with it.
             double sum = 0, most = -INFINITY, next = -INFINITY;
@@ -316,7 +357,8 @@ __global__ __launch_bounds__(64, 8) void route_small_kernel(RouteParams p) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const uint32_t k = (ordered(c[i]) >> 1 & ~kMask) | (kMask - uint32_t(l * VPT + i));
-        key[i] = (i < held) & mine_kept ? k : kAbsent;
+        const bool kept = mine_kept & (whole || (kept_groups >> (group_of(l * VPT + i) & 63) & 1) != 0);
+        key[i] = (i < held) & kept ? k : kAbsent;
     }
     uint32_t last = 0x80000000u, mine = 0, at_k = 0;
     for (int r = 0; r < rounds; ++r) {
@@ -423,10 +465,7 @@ template <typename E> void run_route(const RouteParams& p, hipStream_t stream) {
     while (lanes < 64 && (lanes * most < p.keys || lanes < p.k + kSpare)) lanes *= 2;
     int vpt = 4;
     while (vpt < 16 && lanes * vpt < p.keys) vpt *= 2;
-    const int size = p.keys / p.groups;
-    // A group is whole lanes, a power of two of them.
-    const bool groups_fit = p.groups == 1 || (size % vpt == 0 && (size / vpt & (size / vpt - 1)) == 0 && p.groups <= lanes);
-    if (lanes * vpt >= p.keys && lanes >= p.k + kSpare && groups_fit) {
+    if (lanes * vpt >= p.keys && lanes >= p.k + kSpare && p.groups <= lanes) {
         const bool vec = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && p.keys * sizeof(E) % 16 == 0;
         if (lanes == 16) run_small<E, 16>(p, vpt, vec, stream);
         else if (lanes == 32) run_small<E, 32>(p, vpt, vec, stream);

@@ -22,6 +22,7 @@ template <int THREADS, bool GENERAL> struct BlockLds {
             uint32_t lane_max[THREADS];
             uint32_t group_max[kGroups], group_next[kGroups];
             double worth[kGroups];
+            unsigned long long exact_max[kGroups], exact_next[kGroups];
             float slack[kGroups];
             uint8_t kept[kGroups];
         } first;
@@ -46,9 +47,8 @@ template <int THREADS, bool GENERAL> struct BlockLds {
 // at least k keys reach and, with twice as many lanes as k, about 1.1 to 1.4 k do:
 // those are put in LDS, given their exact values and ranked by counting. Where more
 // reach it than LDS holds (ties, masked rows, large keys all in a few lanes) the
-// exact k-th key is found by bisection over its bits. Rows that stay in doubt with
-// a bias (more near-ties than LDS holds, groups or softmax values that float32 cannot
-// tell apart) go to exact_row.
+// exact k-th key is found by bisection over its bits. With a bias, a row of more near-ties
+// at its k-th key than LDS holds goes to exact_row.
 template <typename E, int THREADS, int VPT, bool VEC, bool GENERAL>
 __global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL || VPT == 64 ? 4 : VPT <= 8 ? 8 : 6) void route_block_kernel(RouteParams p) {
     __shared__ BlockLds<THREADS, GENERAL> lds;
@@ -98,35 +98,76 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL || VPT == 64 ? 
         }
         most = max_of(c, -INFINITY);
     }
+    auto block = [&](double v, auto op) {  // over the lanes, then over the wavefronts in order
+        for (int n = 1; n < 64; n *= 2) v = op(v, __shfl_xor(v, n));
+        __syncthreads();
+        if (lane == 0) lds.wave_value[wave] = v;
+        __syncthreads();
+        v = lds.wave_value[0];
+        for (int w = 1; w < kWaves; ++w) v = op(v, lds.wave_value[w]);
+        return v;
+    };
+    auto block_sum = [&](double v) { return block(v, [](double a, double b) { return a + b; }); };
+    // A key's group: (n + 1/2) / size is at least 1 / (2 size) from a whole number, and a
+    // float32's roundings are less than 2^-7 / size there.
+    const float per_size = 1.0f / float(size);
+    auto group_of = [&](int n) { return int((float(n) + 0.5f) * per_size); };
+    double exact_z = 0;  // a softmax's sum in float64, where float32's leaves something in doubt
+    auto exact_sum = [&] {
+        double v = 0;
+        for (int n = tid; n < p.keys; n += THREADS) v += exp(double(logit_at(row, n)) - double(m));
+        exact_z = block_sum(v);
+    };
+    auto exact_score = [&](float a) { return softmax ? exp(double(a) - double(m)) / exact_z : sigmoid64(a); };
     if (GENERAL && p.groups > 1) {
         auto& f = lds.first;
         for (int g = tid; g < p.groups; g += THREADS) f.group_max[g] = f.group_next[g] = 0;
         __syncthreads();
         // The two largest of each group. Every value but the largest is at some time the
         // smaller of a maximum and what it replaced, so the second largest gets there too.
-        auto add = [&](int n, float hi, float lo) {
+        auto put = [&](int g, float hi, float lo) {
             if (!(hi > -INFINITY)) return;
-            const int g = n / size;
             const uint32_t h = ordered(hi);
             const uint32_t l = max(ordered(lo), min(h, atomicMax(&f.group_max[g], h)));
             if (l > kOut) atomicMax(&f.group_next[g], l);
         };
-        const bool whole = size % kN == 0;  // a vector of keys is of one group
-#pragma unroll
-        for (int i = 0; i < VPT; i += kN) {
-            if (whole) {
-                float hi = -INFINITY, lo = -INFINITY;
-#pragma unroll
-                for (int j = 0; j < kN; ++j) {
-                    lo = median32(hi, lo, c[i + j]);
-                    hi = max32(hi, c[i + j]);
-                }
-                add(key_of(i), hi, lo);
+        // A lane's keys ascend, so its groups do: it keeps the two largest of the group it is
+        // in, and the wavefront puts them down when some lane comes to another one, once
+        // for all its lanes where they are in one group.
+        int at = group_of(key_of(0));
+        float hi = -INFINITY, lo = -INFINITY;
+        auto add = [&](float v) {
+            lo = median32(hi, lo, v);
+            hi = max32(hi, v);
+        };
+        auto put_down = [&] {
+            if (__ballot(at != __builtin_amdgcn_readfirstlane(at)) == 0) {
+                auto merge = [&](float h, float w) {
+                    add(h);
+                    lo = max32(lo, w);
+                };
+                merge(dpp<kXor1>(hi), dpp<kXor1>(lo));
+                merge(dpp<kXor2>(hi), dpp<kXor2>(lo));
+                merge(dpp<kHalfMirror>(hi), dpp<kHalfMirror>(lo));
+                merge(dpp<kMirror>(hi), dpp<kMirror>(lo));
+                merge(__shfl_xor(hi, 16), __shfl_xor(lo, 16));
+                merge(__shfl_xor(hi, 32), __shfl_xor(lo, 32));
+                if (lane == 0) put(at, hi, lo);
             } else {
-#pragma unroll
-                for (int j = 0; j < kN; ++j) add(key_of(i + j), c[i + j], -INFINITY);
+                put(at, hi, lo);
             }
+            hi = lo = -INFINITY;
+        };
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int g = group_of(min(key_of(i), p.keys - 1));  // past the end: -inf, in no way of the last group's
+            if (__ballot(g != at) != 0) {
+                put_down();
+                at = g;
+            }
+            add(c[i]);
         }
+        put_down();
         __syncthreads();
         uint32_t top = 0;
         if (softmax && !biased)
@@ -163,15 +204,38 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL || VPT == 64 ? 
             if (not_below >= p.kept && above < p.kept) lds.doubt = 1;
         }
         __syncthreads();
-        if (lds.doubt) {
+        if (lds.doubt) {  // a bias, and groups that float32 cannot tell apart: the same in float64
+            if (softmax) exact_sum();
+            for (int g = tid; g < p.groups; g += THREADS) f.exact_max[g] = f.exact_next[g] = 0;
             __syncthreads();
-            if constexpr (GENERAL) exact_row<E, THREADS>(p, t, lds.exact);
-            return;
+            for (int n = tid; n < p.keys; n += THREADS) {
+                const float a = logit_at(row, n);
+                if (!(a > -INFINITY) || bias_excludes(p.bias[n])) continue;
+                const unsigned long long h = ordered64(exact_score(a) + double(p.bias[n]));
+                const int g = group_of(n);
+                const unsigned long long l = min(h, atomicMax(&f.exact_max[g], h));
+                if (l > kOut64) atomicMax(&f.exact_next[g], l);
+            }
+            __syncthreads();
+            for (int g = tid; g < p.groups; g += THREADS) {
+                double v = f.exact_max[g] > kOut64 ? from_ordered64(f.exact_max[g]) : -INFINITY;
+                if (p.top == 2 && f.exact_next[g] > kOut64) v += from_ordered64(f.exact_next[g]);
+                f.worth[g] = v;
+            }
+            __syncthreads();
+            for (int g = tid; g < p.groups; g += THREADS) {
+                int rank = 0;
+                for (int h = 0; h < p.groups; ++h)
+                    rank += (f.worth[h] > f.worth[g]) | ((f.worth[h] == f.worth[g]) & (h < g));
+                f.kept[g] = rank < p.kept;
+            }
+            __syncthreads();
+            if (tid == 0) lds.doubt = 0;
         }
         most = -INFINITY;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const bool kept = f.kept[min(key_of(i), p.keys - 1) / size];
+            const bool kept = f.kept[group_of(min(key_of(i), p.keys - 1))];
             if (kept) most = max32(most, c[i]);
             c[i] = kept ? c[i] : NAN;  // NaN: reaches no bound
         }
@@ -269,44 +333,68 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL || VPT == 64 ? 
     }
     const int found = lds.found;
     auto& f = lds.second;
-    if (biased) {
-        for (int i = tid; i < found; i += THREADS) {
-            const int n = int(~uint32_t(lds.cand[i]));
-            double v = value_of(lds.cand[i]);
-            if (v > -INFINITY) {
-                const double a = logit_at(row, n);
-                v = (softmax ? exp(a - double(m)) / double(z) : sigmoid64(a)) + double(p.bias[n]);
+    // Each candidate's rank is the number of those that go before it, counted by as
+    // many threads as there are for it.
+    auto rank_all = [&] {
+        int per = 64;
+        while (per < found && per < THREADS) per *= 2;
+        const int parts = THREADS / per, part = tid / per;
+        for (int i = tid % per; i < found; i += per) {
+            const uint64_t mine = lds.cand[i];
+            int rank = 0;
+            if (biased) {
+                const uint64_t v = f.value[i];
+                for (int j = part; j < found; j += parts)
+                    rank += (f.value[j] > v) | ((f.value[j] == v) & (uint32_t(lds.cand[j]) > uint32_t(mine)));
+            } else {
+#pragma unroll 4
+                for (int j = 2 * part; j < found; j += 2 * parts) {
+                    const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(&lds.cand[j]);
+                    rank += (two.x > mine) + (two.y > mine);
+                }
             }
-            const uint64_t bits = uint64_t(__double_as_longlong(v + 0.0));
-            f.value[i] = bits ^ (uint64_t(int64_t(bits) >> 63) | 1ull << 63);
+            if (rank != 0) atomicAdd(&lds.rank[i], rank);
         }
-        __syncthreads();
+    };
+    if (biased) {
+        // The candidates' exact values. A softmax's float32 sum is off by up to 2^-17 of itself,
+        // by the same for all scores: where that could change the order of two that
+        // follow each other, the sum is taken in float64 and the order again.
+        exact_z = double(z);
+        for (int turn = 0; turn < 2; ++turn) {
+            for (int i = tid; i < found; i += THREADS) {
+                const int n = int(~uint32_t(lds.cand[i]));
+                double v = -INFINITY;
+                if (value_of(lds.cand[i]) > -INFINITY) v = exact_score(logit_at(row, n)) + double(p.bias[n]);
+                f.value[i] = ordered64(v);
+                lds.rank[i] = 0;
+            }
+            __syncthreads();
+            rank_all();
+            __syncthreads();
+            if (!softmax || turn == 1) break;
+            for (int i = tid; i < found; i += THREADS)
+                if (lds.rank[i] <= p.k) {
+                    f.sorted[lds.rank[i]] = from_ordered64(f.value[i]);
+                    f.score[lds.rank[i]] = exact_score(logit_at(row, int(~uint32_t(lds.cand[i]))));
+                }
+            __syncthreads();
+            if (tid < p.k && tid + 1 < found && f.sorted[tid + 1] > -INFINITY) {
+                const double apart = fabs(f.score[tid] - f.score[tid + 1]);
+                if (apart > 0 && f.sorted[tid] - f.sorted[tid + 1] <= 0x1p-16 * apart) lds.doubt = 1;
+            }
+            __syncthreads();
+            if (!lds.doubt) break;
+            exact_sum();
+        }
     } else if (tid == 0 && found < kCandidates) {
         lds.cand[found] = 0;  // the list in pairs; everything goes before a 0
     }
-    // Each candidate's rank is the number of those that go before it, counted by as
-    // many threads as there are for it.
-    int per = 64;
-    while (per < found && per < THREADS) per *= 2;
-    const int parts = THREADS / per, part = tid / per;
-    if (!biased) __syncthreads();
-    for (int i = tid % per; i < found; i += per) {
-        const uint64_t mine = lds.cand[i];
-        int rank = 0;
-        if (biased) {
-            const uint64_t v = f.value[i];
-            for (int j = part; j < found; j += parts)
-                rank += (f.value[j] > v) | ((f.value[j] == v) & (uint32_t(lds.cand[j]) > uint32_t(mine)));
-        } else {
-#pragma unroll 4
-            for (int j = 2 * part; j < found; j += 2 * parts) {
-                const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(&lds.cand[j]);
-                rank += (two.x > mine) + (two.y > mine);
-            }
-        }
-        if (rank != 0) atomicAdd(&lds.rank[i], rank);
+    if (!biased) {
+        __syncthreads();
+        rank_all();
+        __syncthreads();
     }
-    __syncthreads();
     for (int i = tid; i < found; i += THREADS) {
         const int rank = lds.rank[i], n = int(~uint32_t(lds.cand[i]));
         const float v = value_of(lds.cand[i]);
@@ -314,25 +402,8 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL || VPT == 64 ? 
             lds.chosen[rank] = n;
             lds.chosen_value[rank] = v;
         }
-        if (biased && softmax && rank <= p.k) {
-            const double s = v > -INFINITY ? exp(double(logit_at(row, n)) - double(m)) / double(z) : 0.0;
-            f.sorted[rank] = v > -INFINITY ? s + double(p.bias[n]) : -INFINITY;
-            f.score[rank] = s;
-        }
     }
     __syncthreads();
-    if (biased && softmax) {
-        // The scores are off by 2^-17, their float32 sum, of themselves, all by the same.
-        if (tid < p.k && tid + 1 < found && f.sorted[tid + 1] > -INFINITY) {
-            const double apart = fabs(f.score[tid] - f.score[tid + 1]);
-            if (apart > 0 && f.sorted[tid] - f.sorted[tid + 1] <= 0x1p-16 * apart) lds.doubt = 1;
-        }
-        __syncthreads();
-        if (lds.doubt) {
-            if constexpr (GENERAL) exact_row<E, THREADS>(p, t, lds.exact);
-            return;
-        }
-    }
     if (tid / 64 * 64 >= p.k && !p.normalise) return;  // the other wavefronts have no part in the weights
     if (stats && !biased) row_stats();
     const int key = tid < p.k ? lds.chosen[tid] : 0;
@@ -340,24 +411,15 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL || VPT == 64 ? 
     float xk = tid < p.k ? lds.chosen_value[tid] : -INFINITY;
     const bool ok = xk > -INFINITY;
     if (biased && ok) xk = logit_at(row, key);
-    auto block = [&](double v, auto op) {  // over the lanes, then over the wavefronts in order
-        for (int n = 1; n < 64; n *= 2) v = op(v, __shfl_xor(v, n));
-        __syncthreads();
-        if (lane == 0) lds.wave_value[wave] = v;
-        __syncthreads();
-        v = lds.wave_value[0];
-        for (int w = 1; w < kWaves; ++w) v = op(v, lds.wave_value[w]);
-        return v;
-    };
     double s = 0;
     if (p.normalise && softmax) {
         const double top = block(ok ? double(xk) : -double(FLT_MAX), [](double a, double b) { return fmax(a, b); });
         if (ok) s = exp(double(xk) - top);
     } else if (ok) {
-        s = softmax ? exp(double(xk) - double(m)) / double(z) : sigmoid64(xk);
+        s = softmax ? exp(double(xk) - double(m)) / (biased ? exact_z : double(z)) : sigmoid64(xk);
     }
     if (p.normalise) {
-        const double total = block(s, [](double a, double b) { return a + b; });
+        const double total = block_sum(s);
         s = total > 0 ? s / total : 0.0;
     }
     if (tid < p.k) store_choice(p, t, tid, key, s);

@@ -71,6 +71,14 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 __device__ __forceinline__ float from_ordered(uint32_t u) {
     return __uint_as_float(u ^ (~uint32_t(int32_t(u) >> 31) | 0x80000000u));
 }
+__device__ __forceinline__ uint64_t ordered64(double x) {
+    const uint64_t u = uint64_t(__double_as_longlong(x + 0.0));
+    return u ^ (uint64_t(int64_t(u) >> 63) | 1ull << 63);
+}
+__device__ __forceinline__ double from_ordered64(uint64_t u) {
+    return __longlong_as_double(int64_t(u ^ (~uint64_t(int64_t(u) >> 63) | 1ull << 63)));
+}
+constexpr uint64_t kOut64 = 0x000fffffffffffffull;  // ordered64(-inf)
 constexpr uint32_t kOut = 0x007fffffu;  // ordered(-inf): a key that is not eligible
 constexpr uint32_t kAbsent = 0;         // a key that cannot be chosen at all
 
@@ -111,6 +119,7 @@ template <int THREADS> struct ExactLds {
         double value[THREADS];
     };
     double worth[SDM_MAX_GROUPS];
+    unsigned long long most[SDM_MAX_GROUPS], next[SDM_MAX_GROUPS];
     uint8_t kept[SDM_MAX_GROUPS];
     int chosen[SDM_MAX_WIDTH];
 };
@@ -143,15 +152,19 @@ __device__ __forceinline__ void exact_row(const RouteParams& p, int64_t t, Exact
     };
     const int size = p.keys / p.groups;
     if (p.groups > 1) {
+        for (int g = tid; g < p.groups; g += THREADS) lds.most[g] = lds.next[g] = 0;
+        __syncthreads();
+        for (int i = tid; i < p.keys; i += THREADS) {  // the two largest of each group
+            if (!eligible(i)) continue;
+            const unsigned long long c = ordered64(score(i) + (p.bias != nullptr ? double(p.bias[i]) : 0.0));
+            const unsigned long long less = min(c, atomicMax(&lds.most[i / size], c));
+            if (less > kOut64) atomicMax(&lds.next[i / size], less);
+        }
+        __syncthreads();
         for (int g = tid; g < p.groups; g += THREADS) {
-            double a = -INFINITY, b = -INFINITY;  // the two largest
-            for (int i = g * size; i < (g + 1) * size; ++i) {
-                if (!eligible(i)) continue;
-                const double c = score(i) + (p.bias != nullptr ? double(p.bias[i]) : 0.0);
-                b = fmax(b, fmin(a, c));
-                a = fmax(a, c);
-            }
-            lds.worth[g] = p.top == 2 && b > -INFINITY ? a + b : a;
+            double v = lds.most[g] > kOut64 ? from_ordered64(lds.most[g]) : -INFINITY;
+            if (p.top == 2 && lds.next[g] > kOut64) v += from_ordered64(lds.next[g]);
+            lds.worth[g] = v;
         }
         __syncthreads();
         for (int g = tid; g < p.groups; g += THREADS) {

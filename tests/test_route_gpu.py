@@ -318,3 +318,25 @@ def test_route_gradient_against_differences(score, normalise):
         # a third derivative below 1 a weight times h^2 / 6, and float32 weights' roundings over 2 h
         far = dw.double().abs().sum(1) * (h * h / 6 + (2.0 ** -23 + 2 * softmax_slack(x[:1].cpu().numpy())) / (2 * h))
         assert ((slope - grad[:, i].double()).abs() <= far).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("N,groups,kept,top,k", [(72, 2, 1, 2, 7), (80, 8, 2, 2, 16), (34, 2, 1, 1, 6), (995, 5, 3, 2, 30), (33, 33, 7, 1, 5),
+                                                 (1120, 16, 8, 2, 18), (9000, 90, 3, 2, 150), (40000, 10, 4, 2, 256)])
+@pytest.mark.parametrize("kind", ["normal", "masked"])
+def test_route_in_groups_that_float32_cannot_tell_apart(N, groups, kept, top, k, kind, score):
+    """Groups of any size, whose values a bias makes equal but for its own rounding."""
+    x = scores_like(kind, 2, N, N)
+    s = ref.scores(np.where(np.isfinite(x[1].double().numpy()), x[1].double().numpy(), -1e30), score)
+    bias = torch.from_numpy((0.25 - s).astype(np.float32))
+    check_route(x, k, score=score, bias=bias, groups=groups, kept=kept, top=top, normalise=True)
+    check_route(x, k, score=score, groups=groups, kept=kept, top=top)
+
+
+@pytest.mark.parametrize("N,k", [(2048, 64), (5000, 256), (20000, 32)])
+def test_route_of_equal_scores_with_a_bias(N, k):
+    """More equal keys than a workgroup holds candidates: a router before its first step."""
+    x = torch.zeros((2, N))
+    x[1, 7::13] = -INF
+    check_route(x, k, score="sigmoid", bias=torch.zeros(N), normalise=True)
+    check_route(x, k, score="softmax", bias=torch.zeros(N), groups=4, kept=3, top=2)
