@@ -49,9 +49,10 @@ __device__ __forceinline__ float exp32(float x) { return __builtin_amdgcn_exp2f(
 template <int N> __device__ __forceinline__ float exp_sum(const float (&x)[N], float v) {
     constexpr float kL = 1.44269504f;
     float sum = 0;
-    if (__ballot(!(fabsf(v) < 1e30f)) == 0) {  // a branch of the wavefront
+    if (__ballot(!(fabsf(v) < 65536.0f)) == 0) {  // a branch of the wavefront
         // 2^(x L - c) with c = v L rounded: one operation less a term, and what c's rounding
-        // puts into every term, 2^(v L - c), is taken out of the sum.
+        // puts into every term, 2^(v L - c) (at most 2^(2^-8) for such v), is taken out of
+        // the sum.
         const float c = v * kL;
 #pragma unroll
         for (int i = 0; i < N; ++i) sum += __builtin_amdgcn_exp2f(fmaf(x[i], kL, -c));

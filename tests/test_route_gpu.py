@@ -340,3 +340,16 @@ def test_route_of_equal_scores_with_a_bias(N, k):
     x[1, 7::13] = -INF
     check_route(x, k, score="sigmoid", bias=torch.zeros(N), normalise=True)
     check_route(x, k, score="softmax", bias=torch.zeros(N), groups=4, kept=3, top=2)
+
+
+@pytest.mark.parametrize("size", [3e2, 7e4, 1e9, 1e15, 1e25, 1e37])
+@pytest.mark.parametrize("T,N,k", [(5, 64, 6), (3, 256, 8), (2, 3000, 200), (2, 16384, 64)])
+def test_route_of_large_logits(T, N, k, size):
+    """Logits far from 0, all of them and by turns, where a term's exponent is a difference of large numbers."""
+    near = torch.randn((T, N), generator=torch.Generator().manual_seed(N)) * 0.25 + 1
+    for x in (near * size, near * -size, near * size * (torch.arange(N) % 3 - 1)):
+        for score in ("softmax", "sigmoid"):
+            for normalise in (False, True):
+                check_route(x, k, score=score, normalise=normalise)
+                check_backward(x, k, score=score, normalise=normalise)
+        check_route(x, k, score="softmax", bias=torch.linspace(-0.1, 0.1, N), normalise=True)
