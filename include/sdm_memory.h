@@ -27,7 +27,7 @@ extern "C" {
 #endif
 
 #define SDM_MAX_KEYS 65536  /* most keys of a route */
-#define SDM_MAX_ROUTE_TOKENS (1LL << 25) /* most tokens of a route */
+#define SDM_MAX_ROUTE_TOKENS (1LL << 21) /* most tokens of a route: 1024 threads each of a grid */
 #define SDM_MAX_GROUPS 256  /* most groups of a route */
 #define SDM_PACK_BLOCK 32   /* columns of a packed row that share a scale */
 

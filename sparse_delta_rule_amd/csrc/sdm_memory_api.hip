@@ -68,7 +68,7 @@ int check_route(const char* fn, int logit_dtype, int64_t tokens, int64_t keys, i
         return fail(SDM_E_DTYPE, "%s: weights must be float32 or bfloat16 (dtype %d)", fn, w_dtype);
     if (tokens < 0) return fail(SDM_E_SHAPE, "%s: tokens = %lld < 0", fn, (i64)tokens);
     if (tokens > SDM_MAX_ROUTE_TOKENS)
-        return fail(SDM_E_SHAPE, "%s: at most 2^25 tokens per call, got %lld", fn, (i64)tokens);
+        return fail(SDM_E_SHAPE, "%s: at most 2^21 tokens per call, got %lld", fn, (i64)tokens);
     if (keys < 1 || keys > SDM_MAX_KEYS)
         return fail(SDM_E_RANGE, "%s: keys must be in 1..%d, got %lld", fn, SDM_MAX_KEYS, (i64)keys);
     if (k < 1 || k > SDM_MAX_WIDTH || k > choice)

@@ -49,7 +49,11 @@ __device__ __forceinline__ uint32_t block_max(uint32_t m) {
 }
 
 // A thread takes eight columns of a row, four neighbouring lanes a block of 32;
-// a row's threads are neighbours.
+// a row's threads are neighbours. The scale comes from the largest magnitude's own
+// bits, and the conversions divide by it and round to nearest even, exactly. Bound by
+// its memory traffic: 1048576 rows of 100 float32 columns to 4 bits in 87 us, 5.5 TB/s
+// of bytes read and written (a large copy: 5.1); 262144 rows of 256 bytes to scattered
+// slots in 21 us, 4.9 TB/s.
 template <typename E, int VB, bool MX4>
 __global__ __launch_bounds__(kThreads) void pack_kernel(PackParams p) {
     const int blocks = (p.hd + SDM_PACK_BLOCK - 1) / SDM_PACK_BLOCK;
@@ -249,6 +253,13 @@ __device__ __forceinline__ float scale_of(uint32_t four, int block) {
 
 // A pair takes `lanes` neighbouring lanes, N columns each. FOUR: a row has at most
 // four blocks, whose scales come with the entry.
+//
+// Bound, over a large bank, by requests: a row's codes and its scales are a request
+// each, 3.13 M rows of 128 columns (24466 tokens, 128 entries each) take 143 us over
+// 2^24 slots, 43.8 G requests/s, and reads of random rows of up to 128 bytes alone reach
+// 42-45 G/s on this card. Where the scales stay in the L2 caches the codes' requests are
+// left (2^17 slots: 70 us), and in caches altogether (2^14 slots: 53 us) the VALU
+// instructions, 37 for each row of a wavefront's eight.
 template <bool MX4, bool FOUR, int N>
 __global__ __launch_bounds__(kThreads) void gather_packed_kernel(MemoryGatherParams p, int lanes) {
     using C = Codes<MX4, N>;
@@ -350,7 +361,8 @@ __device__ __forceinline__ float lane_sum(float v, int lanes) {
 // A pair takes `lanes` neighbouring lanes, a vector of the row each (or several in
 // turn, rows of more than 64 vectors), for the entries of one segment of the width.
 // WHOLE: a lane has one vector at most, so its
-// part of dout stays in registers.
+// part of dout stays in registers. Bound as the gather is: 1.57 M rows of 128 8-bit
+// columns over 2^24 slots in 74 us, 42.3 G requests/s.
 template <int KIND, int VB, bool FOUR, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void weight_grad_kernel(MemoryGatherParams p, int lanes, int per_segment) {
     using V = BankVec<KIND, VB>;

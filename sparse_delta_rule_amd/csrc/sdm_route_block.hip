@@ -49,8 +49,17 @@ template <int THREADS, bool GENERAL> struct BlockLds {
 // reach it than LDS holds (ties, masked rows, large keys all in a few lanes) the
 // exact k-th key is found by bisection over its bits. With a bias, a row of more near-ties
 // at its k-th key than LDS holds goes to exact_row.
+//
+// What bounds it, at 4096 rows of 16384 bfloat16 keys with their softmax (53 us; the
+// logits alone take 26 at a copy's rate): 537 VALU instructions for each 64 x 32 keys,
+// 31 us of issue, and the phases between the barriers, which three rows of a CU
+// cover only in part. 512 rows of 2048 keys, 256 chosen (18 us) are two rows a CU and
+// the latency of their phases.
+//
+// GENERAL: with a bias or groups. Without either nothing is ever in doubt, and the
+// kernel needs half the registers.
 template <typename E, int THREADS, int VPT, bool VEC, bool GENERAL>
-__global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL || VPT == 64 ? 4 : VPT <= 8 ? 8 : 6) void route_block_kernel(RouteParams p) {
+__global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL ? 4 : VPT <= 8 ? 8 : 6) void route_block_kernel(RouteParams p) {
     __shared__ BlockLds<THREADS, GENERAL> lds;
     constexpr int kWaves = THREADS / 64;
     constexpr int kN = RowKeys<E, THREADS, VPT, VEC>::kN;
@@ -439,19 +448,17 @@ template <typename E, int THREADS, int VPT> void run(const RouteParams& p, bool 
     else hipLaunchKernelGGL((route_block_kernel<E, THREADS, VPT, false, false>), grid, block, 0, stream, p);
 }
 
-// Lanes at least twice k, so that few keys reach the lanes' bound, and as many keys a
-// lane as its registers hold: a wavefront's own work is shared by more of them. (4096
-// rows of 16384, 64 chosen: 54 us with 256 threads of 64 keys, 64 us with 512 of 32.)
-// With a bias or groups 32 keys a lane are the most that fit.
+// Lanes at least twice k, so that few keys reach the lanes' bound; of those, few
+// lanes of many keys: what a wavefront does besides its keys is then shared by more
+// of them. 32 keys a lane are the most that leave three workgroups of 512 to a CU
+// (4096 rows of 16384, 64 chosen: 53 us; 256 lanes of 64 keys take as long and spill).
 template <typename E> void run_route(const RouteParams& p, hipStream_t stream) {
     const bool vec = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && p.keys * sizeof(E) % 16 == 0;
-    const bool general = p.bias != nullptr || p.groups > 1;
-    if (p.k <= 128 && p.keys <= (general ? 8192 : 16384)) {
+    if (p.k <= 128 && p.keys <= 8192) {
         if (p.keys <= 1024) run<E, 256, 4>(p, vec, stream);
         else if (p.keys <= 2048) run<E, 256, 8>(p, vec, stream);
         else if (p.keys <= 4096) run<E, 256, 16>(p, vec, stream);
-        else if (p.keys <= 8192) run<E, 256, 32>(p, vec, stream);
-        else run<E, 256, 64>(p, vec, stream);
+        else run<E, 256, 32>(p, vec, stream);
     } else if (p.keys <= 16384) {
         if (p.keys <= 512) run<E, 512, 1>(p, vec, stream);
         else if (p.keys <= 2048) run<E, 512, 4>(p, vec, stream);

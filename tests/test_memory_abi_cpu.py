@@ -4,6 +4,7 @@ never dereferenced device addresses; no call here reaches a launch)."""
 
 import os
 import re
+import subprocess
 
 import pytest
 import torch
@@ -28,6 +29,16 @@ def test_every_declared_function_is_exported():
                      "sdm_packed_scale_bytes", "sdm_route", "sdm_route_backward"]
     for name in names:
         assert hasattr(sdm.library(), name), name
+
+
+@pytest.mark.parametrize("compiler,std", [("gcc", "-std=c11"), ("g++", "-std=c++17")])
+def test_the_header_is_plain_c(compiler, std, tmp_path):
+    name = tmp_path / ("a.c" if compiler == "gcc" else "a.cpp")
+    name.write_text('#include "sdm_memory.h"\nint (*f)(void*, void*, int, int64_t, int64_t, const void*, int, int64_t, int64_t,'
+                    " const void*, const void*, int, void*) = sdm_bank_pack;\n")
+    r = subprocess.run([compiler, std, "-Wall", "-Wextra", "-Werror", "-fsyntax-only", "-I", os.path.dirname(HEADER), str(name)],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
 
 
 def test_constants_match_the_header():
@@ -91,7 +102,7 @@ ROUTE = dict(logits=A, logit_dtype=F32, tokens=16, keys=256, k=8, score=0, bias=
     (dict(streams=0), E_SHAPE, "streams = 0"),
     (dict(stream_slots=-1), E_SHAPE, "stream_slots = -1"),
     (dict(streams=1 << 40, stream_slots=1 << 40), E_SHAPE, "overflow"),
-    (dict(tokens=(1 << 25) + 1), E_SHAPE, "at most 2^25 tokens"),
+    (dict(tokens=(1 << 21) + 1), E_SHAPE, "at most 2^21 tokens"),
     (dict(stream_slots=1 << 28, idx_dtype=I32), E_RANGE, "does not fit"),
     (dict(logits=None), E_NULL, "required"),
     (dict(idx=None), E_NULL, "required"),

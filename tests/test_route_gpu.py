@@ -353,3 +353,20 @@ def test_route_of_large_logits(T, N, k, size):
                 check_route(x, k, score=score, normalise=normalise)
                 check_backward(x, k, score=score, normalise=normalise)
         check_route(x, k, score="softmax", bias=torch.linspace(-0.1, 0.1, N), normalise=True)
+
+
+def test_route_of_the_most_tokens():
+    """2^21 tokens, as many as a call takes, in both kernels: the last ones as the first."""
+    T = 1 << 21
+    for N in (12, 1100):
+        x = torch.zeros((T, N), dtype=torch.bfloat16, device=DEV)
+        hot = torch.arange(T, device=DEV) * 7919 % N
+        x[torch.arange(T, device=DEV), hot] = 2.0
+        idx, w = sdm_route(x, 1, idx_dtype=torch.int32)
+        assert torch.equal(idx[:, 0].long(), hot)
+        d = sdm_route_backward(x, idx, torch.ones_like(w))
+        top = d[torch.arange(T, device=DEV), hot]
+        assert (top == top[0]).all() and (top > 0).all()
+        assert (d != 0).sum().item() == T * N
+    with pytest.raises(SdmError, match="at most 2"):
+        sdm_route(torch.zeros((T + 1, 4), device=DEV), 1)
