@@ -94,7 +94,7 @@ __device__ __forceinline__ void exact_small_row(const RouteParams& p, int64_t t,
         const uint64_t kept = __ballot(lane < p.groups && rank < p.kept);
 #pragma unroll 1
         for (int i = 0; i < N; ++i)
-            if (i * 64 + lane < p.keys && !(kept >> ((i * 64 + lane) / size) & 1)) gone |= 1u << i;
+            if (i * 64 + lane < p.keys && !bit_of(kept, (i * 64 + lane) / size)) gone |= 1u << i;
     }
     int key = 0;
     float xk = -INFINITY;  // of the lane's choice: lane j has the j-th
@@ -318,7 +318,7 @@ __global__ __launch_bounds__(64, 6) void route_small_kernel(RouteParams p) {
         mine_kept = not_below < p.kept;
         const bool unsure = g < p.groups && not_below >= p.kept && above < p.kept;
         if (!whole) {
-            kept_groups = __ballot(g < p.groups && not_below < p.kept) >> first;
+            kept_groups = row_bits<LANES>(__ballot(g < p.groups && not_below < p.kept), tid);
             mine_kept = true;
             doubt = unsure;
         } else if (__ballot(unsure) != 0) {
@@ -361,7 +361,7 @@ __global__ __launch_bounds__(64, 6) void route_small_kernel(RouteParams p) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const uint32_t k = (ordered(c[i]) >> 1 & ~kMask) | (kMask - uint32_t(l * VPT + i));
-        const bool kept = mine_kept & (whole || (kept_groups >> (group_of(l * VPT + i) & 63) & 1) != 0);
+        const bool kept = mine_kept & (whole || bit_of(kept_groups, group_of(l * VPT + i) & 63));
         key[i] = (i < held) & kept ? k : kAbsent;
     }
     uint32_t last = 0x80000000u, mine = 0, at_k = 0;
@@ -433,7 +433,7 @@ __global__ __launch_bounds__(64, 6) void route_small_kernel(RouteParams p) {
     }
     constexpr uint64_t kRow = LANES == 64 ? ~0ull : (1ull << (LANES % 64)) - 1;
     const uint64_t in_doubt = __ballot(doubt && row_there);
-    if (chosen && row_there && !(in_doubt >> first & kRow)) store_choice(p, t, rank, n, u);
+    if (chosen && row_there && row_bits<LANES>(in_doubt, tid) == 0) store_choice(p, t, rank, n, u);
     for (int r = 0; r < kRows; ++r)
         if (in_doubt >> (r * LANES) & kRow) {
             __syncthreads();

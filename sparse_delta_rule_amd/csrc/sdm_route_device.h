@@ -38,6 +38,17 @@ template <int N> __device__ __forceinline__ float max_of(const float (&x)[N], fl
 // signalling NaN too while the wavefront's IEEE mode is off.
 __device__ __forceinline__ float clean(float x) { return median32(x, -INFINITY, FLT_MAX); }
 __device__ __forceinline__ void ieee_mode_off() { __builtin_amdgcn_s_setreg(1 | 9 << 6 | 0 << 11, 0); }  // MODE, bit 9
+// Bits of a ballot by 32-bit shifts: gfx950 has given wrong results, other ones on each
+// run, for a 64-bit shift whose amount the compiler had put into the last vector register
+// that the kernel allocates (v79 of 80).
+__device__ __forceinline__ uint32_t half_of(uint64_t bits, int i) { return i & 32 ? uint32_t(bits >> 32) : uint32_t(bits); }
+__device__ __forceinline__ bool bit_of(uint64_t bits, int i) { return half_of(bits, i) >> (i & 31) & 1; }
+// Those of the LANES lanes that lane `tid` belongs to.
+template <int LANES> __device__ __forceinline__ uint64_t row_bits(uint64_t bits, int tid) {
+    if constexpr (LANES == 64) return bits;
+    if constexpr (LANES == 32) return half_of(bits, tid);
+    return half_of(bits, tid) >> (tid & 16) & 0xffff;
+}
 template <typename E> __device__ __forceinline__ float logit_at(const E* row, int64_t i) { return clean(widen(row[i])); }
 
 __device__ __forceinline__ bool bias_excludes(float b) { return !(b > -INFINITY); }

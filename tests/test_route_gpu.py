@@ -370,3 +370,23 @@ def test_route_of_the_most_tokens():
         assert (d != 0).sum().item() == T * N
     with pytest.raises(SdmError, match="at most 2"):
         sdm_route(torch.zeros((T + 1, 4), device=DEV), 1)
+
+
+# Every wavefront kernel (16, 32 and 64 lanes a row, 4 to 16 keys a lane) with groups that
+# are not whole lanes, and enough rows that several wavefronts share each compute unit.
+@pytest.mark.parametrize("dtype", (torch.float32, torch.bfloat16))
+@pytest.mark.parametrize("score,top,with_bias", [("softmax", 1, True), ("sigmoid", 1, False), ("softmax", 2, False), ("sigmoid", 2, True)])
+@pytest.mark.parametrize("N,groups,kept,k", [(60, 12, 5, 4), (96, 16, 13, 4), (240, 16, 7, 6), (240, 15, 11, 20), (384, 16, 13, 4),
+                                             (432, 4, 3, 1), (448, 16, 11, 8), (504, 8, 5, 20), (505, 5, 2, 8), (768, 16, 9, 8),
+                                             (1000, 40, 31, 4)])
+def test_route_in_groups_of_many_rows(N, groups, kept, k, score, top, with_bias, dtype):
+    g = torch.Generator().manual_seed(N + groups)
+    x = (torch.randn((4099, N), generator=g) * 1.5).to(dtype)
+    x[torch.rand((4099, N), generator=g) < 0.3] = -INF
+    bias = torch.rand(N, generator=g) * 0.5 if with_bias else None
+    kw = dict(score=score, groups=groups, kept=kept, top=top, normalise=top == 1)
+    idx, w = check_route(x, k, bias=bias, **kw)
+    for _ in range(3):
+        i2, w2 = sdm_route(x.to(DEV), k, bias=None if bias is None else bias.to(DEV), score=score, groups=groups,
+                           kept_groups=kept, group_top=top, normalise=top == 1)
+        assert torch.equal(i2, idx) and torch.equal(w2, w)
