@@ -73,8 +73,10 @@ int64_t sdm_packed_scale_bytes(int packed_dtype, int64_t head_dim);
  * is the sum of its group_top largest eligible c (-inf if none is eligible),
  * only the kept_groups best groups' keys can be chosen.
  * The k keys of largest c are chosen, in descending order. Values are compared
- * as computed in float64 (without a bias: the order of x), and every tie goes
- * to the lowest key or group, so the choice is a function of the inputs alone.
+ * as computed in float64 (keys without a bias: by x, which has the same order;
+ * groups always by their values, so that groups of saturated scores are equal),
+ * and every tie goes to the lowest key or group, so the choice is a function of
+ * the inputs alone.
  *     u_j = s of chosen key j (0 if not eligible)
  *     w_j = scale * u_j / (normalise ? sum_j u_j : 1)     (0 where that sum is 0)
  *     idx_j = (t mod streams) * stream_slots + key

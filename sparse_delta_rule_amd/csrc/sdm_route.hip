@@ -283,23 +283,21 @@ __global__ __launch_bounds__(64, 6) void route_small_kernel(RouteParams p) {
             hi = lds.group_max[tid] > kOut ? from_ordered(lds.group_max[tid]) : -INFINITY;
             lo = lds.group_next[tid] > kOut ? from_ordered(lds.group_next[tid]) : -INFINITY;
         }
-        // Without a bias and with one value a group, the order of the logits is exact.
-        const bool exact_worth = !biased && p.top == 1;
-        float worth = hi, slack = 0;
-        if (!exact_worth) {
-            if (biased) {
-                slack = value_slack(softmax, hi) + (lo > -INFINITY ? value_slack(softmax, lo) : 0.0f);
-                if (!(slack < INFINITY)) slack = 1.0f;  // of an infinite value: equal ones are in doubt
-            } else {
-                const float top = softmax ? lanes_reduce<LANES>(max32(hi, -FLT_MAX), [](float a, float d) { return max32(a, d); }) : 0.0f;
-                slack = hi > -INFINITY ? 2 * score_slack(hi - top) : 0.0f;
-                if (lo > -INFINITY) slack = 2 * score_slack(max32(fabsf(hi - top), fabsf(lo - top)));
-                hi = hi > -INFINITY ? (softmax ? exp32(hi - top) : sigmoid32(hi)) : hi;
-                lo = lo > -INFINITY ? (softmax ? exp32(lo - top) : sigmoid32(lo)) : lo;
-                slack = slack * (max32(hi, 0.0f) + max32(lo, 0.0f)) + 0x1p-120f;  // and below that, of nothing
-            }
-            worth = p.top == 2 && lo > -INFINITY ? hi + lo : hi;
+        // Groups are compared by their scores, also without a bias: logits whose float64 scores
+        // are equal (of a sigmoid, all above 37) are equal here.
+        float slack = 0;
+        if (biased) {
+            slack = value_slack(softmax, hi) + (lo > -INFINITY ? value_slack(softmax, lo) : 0.0f);
+            if (!(slack < INFINITY)) slack = 1.0f;  // of an infinite value: equal ones are in doubt
+        } else {
+            const float top = softmax ? lanes_reduce<LANES>(max32(hi, -FLT_MAX), [](float a, float d) { return max32(a, d); }) : 0.0f;
+            slack = hi > -INFINITY ? 2 * score_slack(hi - top) : 0.0f;
+            if (lo > -INFINITY) slack = 2 * score_slack(max32(fabsf(hi - top), fabsf(lo - top)));
+            hi = hi > -INFINITY ? (softmax ? exp32(hi - top) : sigmoid32(hi)) : hi;
+            lo = lo > -INFINITY ? (softmax ? exp32(lo - top) : sigmoid32(lo)) : lo;
+            slack = slack * (max32(hi, 0.0f) + max32(lo, 0.0f)) + 0x1p-120f;  // and below that, of nothing
         }
+        const float worth = p.top == 2 && lo > -INFINITY ? hi + lo : hi;
         const int g = l / of_group;
         __syncthreads();
         if (l % of_group == 0 && g < p.groups) {
@@ -310,7 +308,7 @@ __global__ __launch_bounds__(64, 6) void route_small_kernel(RouteParams p) {
         int above = 0, not_below = 0;  // groups that surely, that perhaps go before this one
         for (int h = 0; h < p.groups; ++h) {
             const float other = lds.worth[first + h], far = slack + lds.slack[first + h];
-            const bool exact = exact_worth | !(max32(other, worth) > -INFINITY);
+            const bool exact = !(max32(other, worth) > -INFINITY);
             const bool ahead = (other > worth) | ((other == worth) & (h < g));
             above += (h != g) & (exact ? ahead : other > worth + far);
             not_below += (h != g) & (exact ? ahead : !(other < worth - far));

@@ -190,7 +190,7 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL ? 4 : VPT <= 8 
             if (biased) {
                 slack = block_slack(softmax, float(hi)) + (two ? block_slack(softmax, float(lo)) : 0.0f);
                 if (!(slack < INFINITY)) slack = 1.0f;  // of an infinite value: equal ones are in doubt
-            } else if (p.top == 2) {  // by the scores, from the two logits, in float64
+            } else {  // by the scores, from the logits, in float64
                 if (any) hi = softmax ? exp(hi - from) : sigmoid64(hi);
                 if (two) lo = softmax ? exp(lo - from) : sigmoid64(lo);
             }

@@ -390,3 +390,15 @@ def test_route_in_groups_of_many_rows(N, groups, kept, k, score, top, with_bias,
         i2, w2 = sdm_route(x.to(DEV), k, bias=None if bias is None else bias.to(DEV), score=score, groups=groups,
                            kept_groups=kept, group_top=top, normalise=top == 1)
         assert torch.equal(i2, idx) and torch.equal(w2, w)
+
+
+# Logits whose float64 scores are equal though they are not: a sigmoid of 37 and more is 1,
+# a softmax's terms 746 below the largest are 0. Groups of equal scores go by their number.
+@pytest.mark.parametrize("score", ("softmax", "sigmoid"))
+@pytest.mark.parametrize("top", (1, 2))
+@pytest.mark.parametrize("T,N,groups,kept,k", [(1500, 64, 8, 3, 4), (40, 256, 8, 4, 8), (1500, 256, 8, 4, 8), (1500, 384, 16, 5, 4),
+                                               (40, 1000, 40, 11, 8), (20, 2000, 20, 7, 8), (7, 8192, 256, 100, 32)])
+def test_route_in_groups_of_saturated_scores(T, N, groups, kept, k, top, score):
+    x = torch.randn((T, N), generator=torch.Generator().manual_seed(N + T)) * 1e3
+    check_route(x, k, score=score, groups=groups, kept=kept, top=top, normalise=True)
+    check_route(x.bfloat16(), k, score=score, groups=groups, kept=kept, top=top)
