@@ -16,7 +16,7 @@ __device__ __forceinline__ float block_slack(bool softmax, float c) {
 }
 
 template <int THREADS, bool GENERAL> struct BlockLds {
-    static constexpr int kGroups = GENERAL ? SDM_MAX_GROUPS : 1, kChosen = GENERAL ? SDM_MAX_WIDTH + 1 : 1;
+    static constexpr int kGroups = GENERAL ? SDM_MAX_GROUPS : 1, kChosen = GENERAL ? SDM_MAX_WIDTH : 1;
     union {
         struct {
             uint32_t lane_max[THREADS];
@@ -367,8 +367,10 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL ? 4 : VPT <= 8 
     };
     if (biased) {
         // The candidates' exact values. A softmax's float32 sum is off by up to 2^-17 of itself,
-        // by the same for all scores: where that could change the order of two that
-        // follow each other, the sum is taken in float64 and the order again.
+        // by the same for all scores, so two values change places if they are nearer than that of
+        // their scores' difference. If none of the k chosen may have done so with the next, and
+        // none of the others with the last of them, the choice stands; else the sum is taken in
+        // float64 and the order again.
         exact_z = double(z);
         for (int turn = 0; turn < 2; ++turn) {
             for (int i = tid; i < found; i += THREADS) {
@@ -382,16 +384,22 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL ? 4 : VPT <= 8 
             rank_all();
             __syncthreads();
             if (!softmax || turn == 1) break;
+            auto score_of = [&](int i) { return exact_score(logit_at(row, int(~uint32_t(lds.cand[i])))); };
             for (int i = tid; i < found; i += THREADS)
-                if (lds.rank[i] <= p.k) {
+                if (lds.rank[i] < p.k) {
                     f.sorted[lds.rank[i]] = from_ordered64(f.value[i]);
-                    f.score[lds.rank[i]] = exact_score(logit_at(row, int(~uint32_t(lds.cand[i]))));
+                    f.score[lds.rank[i]] = score_of(i);
                 }
             __syncthreads();
-            if (tid < p.k && tid + 1 < found && f.sorted[tid + 1] > -INFINITY) {
-                const double apart = fabs(f.score[tid] - f.score[tid + 1]);
-                if (apart > 0 && f.sorted[tid] - f.sorted[tid + 1] <= 0x1p-16 * apart) lds.doubt = 1;
-            }
+            auto near = [](double v, double w, double apart) {
+                return w > -INFINITY && apart > 0 && fabs(v - w) <= 0x1p-16 * apart;
+            };
+            if (tid + 1 < p.k && near(f.sorted[tid], f.sorted[tid + 1], fabs(f.score[tid] - f.score[tid + 1])))
+                lds.doubt = 1;
+            for (int i = tid; i < found; i += THREADS)
+                if (lds.rank[i] >= p.k &&
+                    near(f.sorted[p.k - 1], from_ordered64(f.value[i]), fabs(f.score[p.k - 1] - score_of(i))))
+                    lds.doubt = 1;
             __syncthreads();
             if (!lds.doubt) break;
             exact_sum();

@@ -402,3 +402,29 @@ def test_route_in_groups_of_saturated_scores(T, N, groups, kept, k, top, score):
     x = torch.randn((T, N), generator=torch.Generator().manual_seed(N + T)) * 1e3
     check_route(x, k, score=score, groups=groups, kept=kept, top=top, normalise=True)
     check_route(x.bfloat16(), k, score=score, groups=groups, kept=kept, top=top)
+
+
+@pytest.mark.parametrize("k", [1, 3])
+@pytest.mark.parametrize("dtype", (torch.float32, torch.bfloat16))
+def test_route_of_a_near_tie_behind_equal_keys(k, dtype):
+    """Two keys of equal logit and bias, and a third of a far larger score whose value is nearly
+    theirs: neighbours in the order of a float32 softmax's sum that are equal tell nothing of it."""
+    wrong = []
+    for seed in range(150):
+        g = torch.Generator().manual_seed(seed)
+        N = 2048
+        x = torch.randn((1, N), generator=g).to(dtype)
+        low, far, first = 300 + seed, 1500 - seed, torch.tensor([40, 1900])
+        x[0, far] = 6.0 + 0.01 * seed  # a score of a tenth to a third
+        x[0, low] = x[0, low + 700] = -2.0
+        bias = torch.full((N,), -3.0)  # the other keys: far from the best
+        s = ref.scores(x[0].double().numpy(), "softmax")
+        bias[far] = 0.25
+        bias[low] = bias[low + 700] = float(s[far] + 0.25 - s[low])  # within 2^-25 of a tie
+        if k == 3:
+            bias[first] = torch.tensor([3.0, 2.5])
+        idx, _ = sdm_route(x.to(DEV), k, bias=bias.to(DEV))
+        keys, _ = ref.route(x.double().numpy(), k, bias=bias.numpy())
+        if not np.array_equal(idx.cpu().numpy(), keys):
+            wrong.append(seed)
+    assert wrong == []
