@@ -297,7 +297,9 @@ __global__ __launch_bounds__(64, 6) void route_small_kernel(RouteParams p) {
             lo = lo > -INFINITY ? (softmax ? exp32(lo - top) : sigmoid32(lo)) : lo;
             slack = slack * (max32(hi, 0.0f) + max32(lo, 0.0f)) + 0x1p-120f;  // and below that, of nothing
         }
-        const float worth = p.top == 2 && lo > -INFINITY ? hi + lo : hi;
+        // Two of the lowest values add up to -inf in float32, which is a group's without a key;
+        // at the lowest finite one its slack keeps them apart and in doubt.
+        const float worth = p.top == 2 && lo > -INFINITY ? max32(hi + lo, -FLT_MAX) : hi;
         const int g = l / of_group;
         __syncthreads();
         if (l % of_group == 0 && g < p.groups) {

@@ -428,3 +428,24 @@ def test_route_of_a_near_tie_behind_equal_keys(k, dtype):
         if not np.array_equal(idx.cpu().numpy(), keys):
             wrong.append(seed)
     assert wrong == []
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,N,groups", [(3, 64, 2), (1500, 64, 8), (3, 90, 5), (1500, 256, 8), (3, 1000, 10), (3, 3000, 6)])
+def test_route_in_groups_at_the_lowest_bias(T, N, groups, score):
+    """A mask of the type's lowest value: two such keys sum to more than float32 holds, and still
+    go before a group that has no eligible key."""
+    size = N // groups
+    x = scores_like("normal", T, N, N)
+    lowest = -float(np.finfo(np.float32).max)
+    bias = torch.full((N,), -INF)
+    bias[(groups - 1) * size:] = lowest
+    check_route(x, 2, score=score, bias=bias, groups=groups, kept=1, top=2, normalise=True)
+    bias[:size] = lowest  # equal values but for float64: the lower group
+    check_route(x, 2, score=score, bias=bias, groups=groups, kept=1, top=2)
+    bias[size] = lowest  # one such key is more than two
+    check_route(x, 1, score=score, bias=bias, groups=groups, kept=1, top=2)
+    bias[:size] = lowest / 2 * 1.5
+    check_route(x, 2, score=score, bias=bias, groups=groups, kept=1, top=2)
+    bias[1::2] = -INF
+    check_route(x, 4, score=score, bias=bias, groups=groups, kept=2, top=2)
