@@ -410,10 +410,7 @@ __global__ __launch_bounds__(64, 6) void route_small_kernel(RouteParams p) {
             const double o = lds.value[first + r];
             rank += (o > v) | ((o == v) & (lds.key[first + r] < n));
             // The scores of a softmax are off by 2^-18, its float32 sum, of themselves, all by the same.
-            if (softmax && biased && l < rounds && ok && o > -INFINITY) {
-                const double apart = fabs(s - lds.score[first + r]);
-                doubt |= apart > 0 && fabs(o - v) <= 0x1p-17 * apart;
-            }
+            if (softmax && biased && l < rounds && ok) doubt |= near(v, o, fabs(s - lds.score[first + r]), 0x1p-17);
         }
     }
     double u = s;

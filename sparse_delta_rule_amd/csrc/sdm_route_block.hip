@@ -391,14 +391,11 @@ __global__ __launch_bounds__(THREADS, THREADS == 1024 || GENERAL ? 4 : VPT <= 8 
                     f.score[lds.rank[i]] = score_of(i);
                 }
             __syncthreads();
-            auto near = [](double v, double w, double apart) {
-                return w > -INFINITY && apart > 0 && fabs(v - w) <= 0x1p-16 * apart;
-            };
-            if (tid + 1 < p.k && near(f.sorted[tid], f.sorted[tid + 1], fabs(f.score[tid] - f.score[tid + 1])))
+            if (tid + 1 < p.k && near(f.sorted[tid], f.sorted[tid + 1], fabs(f.score[tid] - f.score[tid + 1]), 0x1p-16))
                 lds.doubt = 1;
             for (int i = tid; i < found; i += THREADS)
-                if (lds.rank[i] >= p.k &&
-                    near(f.sorted[p.k - 1], from_ordered64(f.value[i]), fabs(f.score[p.k - 1] - score_of(i))))
+                if (lds.rank[i] >= p.k && near(f.sorted[p.k - 1], from_ordered64(f.value[i]),
+                                               fabs(f.score[p.k - 1] - score_of(i)), 0x1p-16))
                     lds.doubt = 1;
             __syncthreads();
             if (!lds.doubt) break;

@@ -114,6 +114,14 @@ __device__ __forceinline__ bool before(const Ranked& a, const Ranked& b) {
     return a.c > b.c || (a.c == b.c && a.key < b.key);
 }
 
+// Whether the order of two values v and w, scores that are `apart` plus a bias each, may be another
+// one with a softmax's sum in float64 than with one that is off by half of `off` of itself: that
+// moves the values by so much of `apart` against each other. Four roundings to float64, two
+// values' with either sum, make equal or unequal what is nearer yet.
+__device__ __forceinline__ bool near(double v, double w, double apart, double off) {
+    return w > -INFINITY && apart > 0 && fabs(v - w) <= off * apart + 0x1p-50 * fmin(fabs(v), fabs(w));
+}
+
 template <int THREADS, typename T, typename F> __device__ __forceinline__ T block_reduce(T v, T* lds, F f) {
     __syncthreads();
     lds[threadIdx.x] = v;

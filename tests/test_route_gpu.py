@@ -449,3 +449,22 @@ def test_route_in_groups_at_the_lowest_bias(T, N, groups, score):
     check_route(x, 2, score=score, bias=bias, groups=groups, kept=1, top=2)
     bias[1::2] = -INF
     check_route(x, 4, score=score, bias=bias, groups=groups, kept=2, top=2)
+
+
+@pytest.mark.parametrize("T,N", [(6000, 64), (6000, 256), (1024, 1000), (6000, 3000)])
+def test_route_of_scores_that_a_large_bias_makes_equal(T, N):
+    """Two keys of a bias of 1e9, a step of which in float64 is 2^-23: scores nearer than that are equal
+    or not by where a step falls, which a float32 softmax's sum does not tell."""
+    g = torch.Generator().manual_seed(N)
+    x = torch.randn((T, N), generator=g)
+    at = torch.randperm(N, generator=g)[:2].sort().values
+    x[:, at] = float(4 + np.log(N / 64)) + torch.rand((T, 1), generator=g) + torch.tensor([0, 2.0 ** -21])
+    bias = torch.zeros(N)
+    bias[at] = 1e9
+    idx, _ = sdm_route(x.to(DEV), 1, bias=bias.to(DEV))
+    X = x.double().numpy()
+    e = np.exp(X - X.max(1, keepdims=True))
+    v = (e / e.sum(1, keepdims=True))[:, at.numpy()] + 1e9
+    want = at.numpy()[(v[:, 1] > v[:, 0]).astype(int)]
+    bad = (idx[:, 0].cpu().numpy() != want).sum()
+    assert bad == 0, f"{bad} of {T} rows"
