@@ -186,6 +186,13 @@ __global__ __launch_bounds__(THREADS) void route_backward_whole_kernel(RouteBack
             if (Row::key_of(i, tid) < p.keys) out[Row::key_of(i, tid)] = narrow<E>(c[i]);
         }
     }
+    if (!(fabsf(f) < INFINITY)) {  // a masked key's gradient is 0 all the same
+#pragma unroll 1
+        for (int i = 0; i < VPT; ++i) {
+            const int n = Row::key_of(i, tid);
+            if (n < p.keys && !(logit_at(row, n) > -INFINITY)) out[n] = E(0);
+        }
+    }
     for (int j = lds.head[tid]; j >= 0; j = lds.next[j]) {
         double all = 0;  // of the key, should it have been given more than once
         for (int i = lds.head[tid]; i >= 0; i = lds.next[i])

@@ -468,3 +468,27 @@ def test_route_of_scores_that_a_large_bias_makes_equal(T, N):
     want = at.numpy()[(v[:, 1] > v[:, 0]).astype(int)]
     bad = (idx[:, 0].cpu().numpy() != want).sum()
     assert bad == 0, f"{bad} of {T} rows"
+
+
+@pytest.mark.parametrize("bad", [INF, -INF, NAN], ids=["inf", "-inf", "nan"])
+@pytest.mark.parametrize("T,N,k", [(4, 61, 8), (3, 256, 8), (2, 5001, 200), (2, 16384, 64), (1, 40000, 256)])
+@pytest.mark.parametrize("score,normalise", [("softmax", False), ("softmax", True), ("sigmoid", False), ("sigmoid", True)])
+def test_route_backward_of_a_gradient_that_is_not_finite(T, N, k, bad, score, normalise):
+    """A key at -inf has the gradient 0 whatever the others' is; a full softmax's other keys are none of them finite."""
+    x = scores_like("masked", T, N, N)
+    x[0] = scores_like("normal", 1, N, 1)[0]
+    x[0, ::3] = -INF
+    for dtype in (torch.float32, torch.bfloat16):
+        d = x.to(dtype).to(DEV)
+        idx, _ = sdm_route(d, k, score=score, normalise=normalise)
+        dw = torch.randn(idx.shape, generator=torch.Generator().manual_seed(1)).to(DEV)
+        dw[:, 0] = bad
+        got = sdm_route_backward(d, idx, dw, score=score, normalise=normalise)
+        masked = d == -INF
+        assert not (got[masked] != 0).any()
+        chosen = torch.zeros_like(masked).scatter_(1, idx, True)
+        if normalise or score == "sigmoid":
+            assert not (got[~chosen] != 0).any()
+            assert not got.gather(1, idx)[:, 0].isfinite().any()
+        else:
+            assert not got[~masked].isfinite().any()
