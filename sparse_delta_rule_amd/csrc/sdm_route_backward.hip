@@ -83,7 +83,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_backward_sparse_kernel(Rout
     for (int i = 0; i < PER; ++i) {
         double d = p.scale * u[i] * (c[i].dw - dot);
         if (p.score == SDM_SIGMOID) d /= 1.0 + exp(double(c[i].x));  // 1 - s; x = -inf gives 1
-        g[i] = c[i].x > -INFINITY ? float(d) : 0.0f;
+        g[i] = c[i].x > -INFINITY && !(p.normalise && total == 0) ? float(d) : 0.0f;
     }
     E* out = static_cast<E*>(p.dlogits) + t0 * p.keys;
     const int whole = there * p.keys;  // of one row where it does not fit the tile

@@ -492,3 +492,19 @@ def test_route_backward_of_a_gradient_that_is_not_finite(T, N, k, bad, score, no
             assert not got.gather(1, idx)[:, 0].isfinite().any()
         else:
             assert not got[~masked].isfinite().any()
+
+
+def test_route_backward_where_the_weights_sum_to_zero():
+    """Renormalised sigmoid scores that are all 0 in float64: the gradient is 0, also of an infinite one."""
+    x = torch.full((3, 50), -800.0)
+    x[1] = -3e38
+    x[2, 7] = 1.0  # a row whose sum is not 0
+    for dtype in (torch.float32, torch.bfloat16):
+        d = x.to(dtype).to(DEV)
+        idx, w = sdm_route(d, 4, score="sigmoid", normalise=True)
+        assert not w[:2].any()
+        for bad in (INF, NAN, 1.0):
+            dw = torch.full((3, 4), bad, device=DEV)
+            got = sdm_route_backward(d, idx, dw, score="sigmoid", normalise=True)
+            assert not (got[:2] != 0).any()
+            assert got[2, 7].isnan() == (bad != 1.0)
