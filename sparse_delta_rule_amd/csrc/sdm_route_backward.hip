@@ -186,11 +186,16 @@ __global__ __launch_bounds__(THREADS) void route_backward_whole_kernel(RouteBack
             if (Row::key_of(i, tid) < p.keys) out[Row::key_of(i, tid)] = narrow<E>(c[i]);
         }
     }
-    if (!(fabsf(f) < INFINITY)) {  // a masked key's gradient is 0 all the same
+    if (!(fabsf(f) < INFINITY)) {
+        // Past float32, or not finite: the row again with the factor in float64. A masked key's
+        // gradient is 0 all the same.
+        const double factor = -dot / z;
 #pragma unroll 1
         for (int i = 0; i < VPT; ++i) {
             const int n = Row::key_of(i, tid);
-            if (n < p.keys && !(logit_at(row, n) > -INFINITY)) out[n] = E(0);
+            if (n >= p.keys) continue;
+            const float x = logit_at(row, n);
+            out[n] = narrow<E>(x > -INFINITY ? float(factor * exp32(x - m)) : 0.0f);
         }
     }
     for (int j = lds.head[tid]; j >= 0; j = lds.next[j]) {

@@ -508,3 +508,30 @@ def test_route_backward_where_the_weights_sum_to_zero():
             got = sdm_route_backward(d, idx, dw, score="sigmoid", normalise=True)
             assert not (got[:2] != 0).any()
             assert got[2, 7].isnan() == (bad != 1.0)
+
+
+@pytest.mark.parametrize("dtype", (torch.float32, torch.bfloat16))
+@pytest.mark.parametrize("T,N,k", [(3, 200, 8), (2, 5000, 64), (2, 16384, 64), (1, 40000, 256)])
+def test_route_backward_of_large_gradients(T, N, k, dtype):
+    """Sums of du s past float32's range, with gradients inside it."""
+    x = (scores_like("normal", T, N, N) * 0.1).to(dtype)
+    check_backward(x, k, scale=2.0 ** 127, dw=torch.full((T, k), N / 16.0))  # a sum of about 2^127 k / 16
+
+    # And where the keys of the largest scores get gradients past it themselves: k + 1 of them,
+    # all but one chosen, and masked keys and some 60 below behind them.
+    x = scores_like("normal", T, N, N).to(dtype)
+    x[:, :N // 2] = -INF
+    x[:, :k + 1] = torch.linspace(60, 50, k + 1).to(dtype)
+    idx = torch.arange(1, k + 1).repeat(T, 1)
+    idx[:, 0] = 0
+    du = 2.0 ** 100
+    want, _ = ref.route_backward(x.double().numpy(), idx.numpy(), np.full((T, k), du), scale=du)
+    got = sdm_route_backward(x.to(DEV), idx.to(DEV), torch.full((T, k), du, device=DEV), scale=du).double().cpu().numpy()
+    assert (got[:, 0] == np.inf).all()
+    want, got, X = want[:, k + 1:], got[:, k + 1:], x.double().numpy()[:, k + 1:]
+    assert 0 < np.abs(want).max() < 2.0 ** 126
+    # A float32 exponential of a distance d: 2.25 d 2^-24 (the distance's rounding, the product with log2 e
+    # and that constant's own) and 4 2^-24, in the key's own term and in the row's sum; six roundings
+    # of their product; and the result's.
+    eps = 2.0 ** -24 * (2.25 * (60 - X[np.isfinite(X)].min()) + 8)
+    assert (np.abs(got - want) <= (2 * eps + 6 * 2.0 ** -24 + HALF_STEP[dtype] * 1.001) * np.abs(want)).all()
