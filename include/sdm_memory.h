@@ -117,9 +117,12 @@ int sdm_route(const void* logits, int logit_dtype, int64_t tokens, int64_t keys,
  *     sigmoid:    dlogits_i = s_i (1 - s_i) du_i
  * 0 where U is 0, for a chosen key that is not eligible, and for a key at -inf.
  * A renormalised softmax's gradient is 0 outside the chosen keys.
- * The part of the chosen keys is computed in float64; a full softmax's other keys
- * in float32, where a score below 2^-126 may count as 0. Each value is rounded to
- * float32 and then to the logits' type.
+ * The part of the chosen keys is computed in float64, with a full softmax's sum over
+ * all keys taken from float32 exponentials relative to the row's largest logit, whose
+ * own is exactly 1, and added in float64: 1 - s of a key far above the rest is as
+ * precise as the others' terms. A full softmax's other keys are computed in float32,
+ * where a score below 2^-126 may count as 0. Each value is rounded to float32 and then
+ * to the logits' type.
  *
  * Arguments: as sdm_route (bias only tells which keys are eligible), with
  *   dw       [tokens, k] of w_dtype.

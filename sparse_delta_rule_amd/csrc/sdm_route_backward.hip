@@ -117,8 +117,8 @@ __global__ __launch_bounds__(64 * kWaves) void route_backward_sparse_kernel(Rout
 // ------------------------------------------------------------------ a full softmax
 
 template <int THREADS> struct WholeLds {
-    float wave_max[THREADS / 64], wave_sum[THREADS / 64];
-    double wave_value[THREADS / 64];
+    float wave_max[THREADS / 64];
+    double wave_sum[THREADS / 64], wave_value[THREADS / 64];
     int head[THREADS];  // a lane's list of the chosen keys it holds: -1, or the first's number
     int next[SDM_MAX_WIDTH];
     int key[SDM_MAX_WIDTH];
@@ -128,8 +128,8 @@ template <int THREADS> struct WholeLds {
 // A workgroup a token, the row in its registers: read once, written once. Every key
 // gets -s_i sum_j du_j s_j, and each lane then stores its chosen keys' own gradients,
 // computed in float64, over that: a lane's stores to one address happen in order.
-// Bound by its memory traffic: 4096 rows of 16384 bfloat16 keys in 50 us, 5.4 TB/s of
-// bytes read and written (a large copy: 5.1).
+// Bound by its memory traffic: 4096 rows of 16384 bfloat16 keys in 51 us, 5.3 TB/s of
+// bytes read and written (a large copy: 6.2; with a float32 sum over the row 50 us).
 template <typename E, int THREADS, int VPT, bool VEC>
 __global__ __launch_bounds__(THREADS) void route_backward_whole_kernel(RouteBackwardParams p) {
     using Row = RowKeys<E, THREADS, VPT, VEC>;
@@ -146,17 +146,23 @@ __global__ __launch_bounds__(THREADS) void route_backward_whole_kernel(RouteBack
     if (tid < p.k) mine = choice_at<E>(p, t, tid);
     lds.head[tid] = -1;
     const float v = lanes_reduce<64>(max_of(c, -FLT_MAX), [](float a, float b) { return max32(a, b); });
-    const float sum = lanes_reduce<64>(exp_sum(c, v), [](float a, float b) { return a + b; });
+    // The largest term is exactly 1 and the others are added to it in float64, so that 1 - s
+    // of a key far above the rest has the precision of the others' terms.
+    double sum = 0;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) sum += double(exp32(c[i] - v));
+    for (int n = 1; n < 64; n *= 2) sum += __shfl_xor(sum, n);
     if (lane == 0) {
         lds.wave_max[wave] = v;
         lds.wave_sum[wave] = sum;
     }
     __syncthreads();
-    float m = -FLT_MAX, z = 0;
+    float m = -FLT_MAX;
+    double z = 0;
     for (int w = 0; w < THREADS / 64; ++w) m = max32(m, lds.wave_max[w]);
-    for (int w = 0; w < THREADS / 64; ++w) z += lds.wave_sum[w] * exp32(lds.wave_max[w] - m);
+    for (int w = 0; w < THREADS / 64; ++w) z += lds.wave_sum[w] * double(exp32(lds.wave_max[w] - m));
     const double du = p.scale * mine.dw;
-    const double s = mine.x > -INFINITY ? exp(double(mine.x) - double(m)) / double(z) : 0.0;
+    const double s = mine.x > -INFINITY ? exp(double(mine.x) - double(m)) / z : 0.0;
     double dot = du * s;
     if (wave * 64 < p.k) {
         for (int n = 1; n < 64; n *= 2) dot += __shfl_xor(dot, n);
@@ -172,7 +178,8 @@ __global__ __launch_bounds__(THREADS) void route_backward_whole_kernel(RouteBack
     __syncthreads();
     dot = 0;
     for (int w = 0; w * 64 < p.k; ++w) dot += lds.wave_value[w];
-    const float f = z > 0 ? -float(dot) / z : 0.0f;
+    const double factor = z > 0 ? -dot / z : 0.0;
+    const float f = float(factor);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) c[i] = exp32(c[i] - m) * f;
 #pragma unroll
@@ -189,7 +196,6 @@ __global__ __launch_bounds__(THREADS) void route_backward_whole_kernel(RouteBack
     if (!(fabsf(f) < INFINITY)) {
         // Past float32, or not finite: the row again with the factor in float64. A masked key's
         // gradient is 0 all the same.
-        const double factor = -dot / z;
 #pragma unroll 1
         for (int i = 0; i < VPT; ++i) {
             const int n = Row::key_of(i, tid);

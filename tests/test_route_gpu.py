@@ -535,3 +535,40 @@ def test_route_backward_of_large_gradients(T, N, k, dtype):
     # of their product; and the result's.
     eps = 2.0 ** -24 * (2.25 * (60 - X[np.isfinite(X)].min()) + 8)
     assert (np.abs(got - want) <= (2 * eps + 6 * 2.0 ** -24 + HALF_STEP[dtype] * 1.001) * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("peak", [10, 17, 20, 24, 30, 40])
+@pytest.mark.parametrize("T,N,k", [(2, 256, 1), (3, 255, 4), (2, 1000, 8), (2, 5000, 33), (2, 16384, 64), (1, 40000, 256)])
+def test_route_backward_of_a_peaked_row(T, N, k, peak):
+    """One chosen key far above the rest: 1 - s is what the others' scores sum to, and keeps its
+    relative precision, so a chosen key's gradient is right relative to what cancels in exact
+    arithmetic only, B_j = |du_j| (1 - s_j) + sum over m != j of |du_m| s_m, times s_j."""
+    x = scores_like("normal", T, N, N) * 0.5
+    hot = torch.arange(T) * 37 + 5
+    x[torch.arange(T), hot] = x.amax(1) + peak
+    idx = sdm_route(x.to(DEV), k)[0].cpu()
+    dw = torch.randn((T, k), generator=torch.Generator().manual_seed(peak))
+    got = sdm_route_backward(x.to(DEV), idx.to(DEV), dw.to(DEV), scale=1.5).double().cpu().numpy()
+    X = x.double().numpy()
+    # A float32 exponential of a distance d: 2.25 d 2^-24 (the distance's rounding, the product with
+    # log2 e and that constant's own), 4 2^-24 itself, again 4 where a wavefront's sum is moved to
+    # the row's largest. The row's sum then is off by at most eps of what the other keys add, in
+    # relation to all by eps (1 - s_max), and s_j (du_j - dot) by at most 2 eps s_j B_j.
+    eps = 2.0 ** -24 * (2.25 * (X.max() - X.min()) + 8)
+    for t in range(T):
+        e = np.exp(X[t] - X[t].max())
+        rest = np.array([np.delete(e, j).sum() for j in idx[t].numpy()])
+        z, s = e.sum(), e / e.sum()
+        d, at = 1.5 * dw[t].double().numpy(), idx[t].numpy()
+        other = np.array([np.delete(d * s[at], j).sum() for j in range(k)])
+        size = np.array([np.delete(np.abs(d) * s[at], j).sum() for j in range(k)])
+        want = s[at] * (d * (rest / z) - other)
+        B = s[at] * (np.abs(d) * (rest / z) + size)
+        # the result's rounding, and float64's own where 1 - s is taken as a difference: at most 64 additions
+        # of a lane, 6 levels of lanes, 16 wavefronts and a division, 2^-53 each
+        slack = 2.0 ** -24 * 1.01 * np.abs(want) + 2 * eps * B + 2.0 ** -46 * s[at] * np.abs(d)
+        far = np.abs(got[t][at] - want)
+        assert (far <= slack).all(), (t, (far / slack).max())
+        dot = (d * s[at]).sum()
+        out = np.setdiff1d(np.arange(N), at)
+        assert (np.abs(got[t][out] + s[out] * dot) <= 2 * eps * s[out] * (np.abs(d) * s[at]).sum() + 2.0 ** -149).all()
