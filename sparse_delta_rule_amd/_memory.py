@@ -137,22 +137,26 @@ def sdm_route_backward(logits: torch.Tensor, idx: torch.Tensor, dw: torch.Tensor
 
 class PackedBank:
     """A bank in 8 ("mx8") or 4 ("mx4") bits: its code and scale arrays, laid out as
-    include/sdm_memory.h says. Holds the two tensors, which must not be resized."""
+    include/sdm_memory.h says. Holds the two tensors, which must not be resized, and
+    their addresses: its fields cannot be replaced, and a copy is a bank of the copied
+    tensors."""
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, head_dim: int, kind: str = "mx8"):
-        try:
-            self.dtype = _KINDS[kind]
-        except KeyError:
-            raise ValueError(f"kind must be one of {sorted(_KINDS)}, got {kind!r}") from None
         row, scale = self.row_bytes(head_dim, kind)
         if codes.dim() != 2:
             raise ValueError("codes must be [num_slots, row_bytes]")
-        self.num_slots, self.head_dim, self.kind, self.device = codes.shape[0], head_dim, kind, codes.device
-        self._device = codes.get_device()
-        _check(self._device, "codes", codes, (torch.uint8,), (self.num_slots, row))
-        _check(self._device, "scales", scales, (torch.uint8,), (self.num_slots, scale))
-        self.codes, self.scales = codes, scales
-        self._head = (codes.data_ptr(), scales.data_ptr(), self.dtype, self.num_slots, head_dim)
+        num_slots, device = codes.shape[0], codes.get_device()
+        _check(device, "codes", codes, (torch.uint8,), (num_slots, row))
+        _check(device, "scales", scales, (torch.uint8,), (num_slots, scale))
+        self.__dict__.update(codes=codes, scales=scales, num_slots=num_slots, head_dim=head_dim, kind=kind,
+                             dtype=_KINDS[kind], device=codes.device, _device=device,
+                             _head=(codes.data_ptr(), scales.data_ptr(), _KINDS[kind], num_slots, head_dim))
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"{name} of a packed bank cannot be replaced: make another bank")
+
+    def __reduce__(self):
+        return PackedBank, (self.codes, self.scales, self.head_dim, self.kind)
 
     @staticmethod
     def row_bytes(head_dim: int, kind: str = "mx8") -> tuple:

@@ -2,6 +2,9 @@
 tests/memory_ref.py, sdm_gather_packed bit for bit against sdm_gather on the
 values, sdm_gather_weight_grad within what its roundings allow."""
 
+import copy
+import pickle
+
 import numpy as np
 import pytest
 import torch
@@ -342,3 +345,24 @@ def test_weight_grad_against_differences():
         # the loss is linear in the weight: only the roundings of 10 products and of w + h are left
         far = ((w0.double().abs() + 1)[:, :, None] * values.double()[i0].abs() * dout.double().abs()[:, None]).sum((1, 2))
         assert ((loss[0] - loss[1] - dw[:, n].double()).abs() <= 2 * gamma(12) * far).all()
+
+
+def test_a_bank_keeps_its_arrays():
+    """Calls go by the arrays that the bank was made of: another one, or another size, is another bank."""
+    packed = PackedBank.empty(16, 128, "mx8", DEV)
+    for name, other in (("codes", packed.codes.clone()), ("scales", packed.scales.clone()), ("head_dim", 64),
+                        ("num_slots", 32), ("dtype", 5)):
+        with pytest.raises(AttributeError, match="cannot be replaced"):
+            setattr(packed, name, other)
+    assert packed.head_dim == 128 and packed.num_slots == 16 and packed.kind == "mx8" and packed.codes.shape == (16, 128)
+    rows = torch.randn((16, 128), device=DEV)
+    sdm_bank_pack(packed, rows)
+    for copied in (copy.deepcopy(packed), pickle.loads(pickle.dumps(packed))):
+        assert copied._head[:2] == (copied.codes.data_ptr(), copied.scales.data_ptr())
+        assert copied.codes.data_ptr() != packed.codes.data_ptr() and copied._head[2:] == packed._head[2:]
+        assert torch.equal(copied.codes, packed.codes) and torch.equal(copied.scales, packed.scales)
+        idx, w = torch.arange(16, device=DEV)[:, None], torch.ones((16, 1), device=DEV)
+        before = sdm_gather_packed(packed, idx, w, chunk=1)[0]
+        sdm_bank_pack(copied, rows * 2)  # and leaves the first one as it is
+        assert torch.equal(sdm_gather_packed(packed, idx, w, chunk=1)[0], before)
+        assert torch.equal(sdm_gather_packed(copied, idx, w, chunk=1)[0], 2 * before)
