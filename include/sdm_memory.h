@@ -43,7 +43,8 @@ extern "C" {
  *            largest value is 448; 0x7f and 0xff are not a number.
  *   SDM_MX4  half of byte c / 2 (the low half for even c): sign, 2 bits of
  *            exponent (bias 1), 1 of fraction: 0, 0.5, 1, 1.5, 2, 3, 4, 6.
- * A float32 holds every such value exactly.
+ * A float32 holds every such value exactly, but those of a caller's own bytes that are
+ * past its range (scales above 2^119), which read as infinite.
  */
 enum {
     SDM_MX8 = 4,
@@ -115,7 +116,9 @@ int sdm_route(const void* logits, int logit_dtype, int64_t tokens, int64_t keys,
  *     otherwise:  du_j = scale * dw_j
  *     softmax:    dlogits_i = s_i (du_i - sum_j du_j s_j)     (du_i = 0 if i is not chosen)
  *     sigmoid:    dlogits_i = s_i (1 - s_i) du_i
- * 0 where U is 0, for a chosen key that is not eligible, and for a key at -inf.
+ * du_j is 0 for a chosen key that is not eligible, and all of a row's where U is 0;
+ * dlogits is 0 for a key at -inf, also where other gradients are not finite. A key that
+ * its bias alone excludes is in a softmax's sum all the same, and has that part.
  * A renormalised softmax's gradient is 0 outside the chosen keys.
  * The part of the chosen keys is computed in float64, with a full softmax's sum over
  * all keys taken from float32 exponentials relative to the row's largest logit, whose

@@ -54,7 +54,8 @@ template <typename E> __device__ __forceinline__ float logit_at(const E* row, in
 __device__ __forceinline__ bool bias_excludes(float b) { return !(b > -INFINITY); }
 
 __device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
-// Within 2^-22 of its value: the hardware's base-2 exponential and reciprocal.
+// Within (4 + 2 |x|) 2^-24 of its value: the hardware's base-2 exponential, of a product that is
+// rounded, with a rounded constant.
 __device__ __forceinline__ float exp32(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
 // Sum of exp(x[i] - v), v the largest x of the row's lanes or -FLT_MAX.
 template <int N> __device__ __forceinline__ float exp_sum(const float (&x)[N], float v) {

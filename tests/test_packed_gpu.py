@@ -366,3 +366,27 @@ def test_a_bank_keeps_its_arrays():
         sdm_bank_pack(copied, rows * 2)  # and leaves the first one as it is
         assert torch.equal(sdm_gather_packed(packed, idx, w, chunk=1)[0], before)
         assert torch.equal(sdm_gather_packed(copied, idx, w, chunk=1)[0], 2 * before)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_every_code_with_every_scale(kind):
+    """A bank's bytes may be the caller's own: each code's value times each scale, as float32, past its
+    range infinite, and the scale 255 not-a-number."""
+    lines = np.zeros((256, 256), np.uint8)
+    lines[:] = np.arange(256)  # mx8: each code; mx4: each pair of codes
+    hd = 256 if kind == "mx8" else 512
+    scales = np.repeat(np.arange(256, dtype=np.uint8)[:, None], ref.scale_bytes(hd), 1)
+    bank = PackedBank(torch.from_numpy(lines).to(DEV), torch.from_numpy(scales).to(DEV), hd, kind)
+    with np.errstate(over="ignore", invalid="ignore"):
+        want = ref.unpack(lines, scales, hd, kind).astype(np.float32)
+    every = torch.arange(256, device=DEV)[:, None]
+    for n in (256, 256 * 40):  # few and many columns a lane
+        back, _ = sdm_gather_packed(bank, every.repeat(n // 256, 1), torch.ones((n, 1), device=DEV), chunk=n)
+        assert np.array_equal(back[-256:].cpu().numpy(), want, equal_nan=True)
+    # rows of four blocks, whose scales come with the entry
+    short = PackedBank(torch.from_numpy(lines[:, 96:160] if kind == "mx4" else lines[:, 64:192]).contiguous().to(DEV),
+                       torch.from_numpy(scales[:, :4]).contiguous().to(DEV), 128, kind)
+    part = want[:, 192:320] if kind == "mx4" else want[:, 64:192]
+    for n in (256, 256 * 400):
+        back, _ = sdm_gather_packed(short, every.repeat(n // 256, 1), torch.ones((n, 1), device=DEV), chunk=n)
+        assert np.array_equal(back[-256:].cpu().numpy(), part, equal_nan=True)
