@@ -52,7 +52,7 @@ __device__ __forceinline__ uint32_t block_max(uint32_t m) {
 // a row's threads are neighbours. The scale comes from the largest magnitude's own
 // bits, and the conversions divide by it and round to nearest even, exactly. Bound by
 // its memory traffic: 1048576 rows of 100 float32 columns to 4 bits in 87 us, 5.5 TB/s
-// of bytes read and written (a large copy: 5.1); 262144 rows of 256 bytes to scattered
+// of bytes read and written (a large copy: 6.2); 262144 rows of 256 bytes to scattered
 // slots in 21 us, 4.9 TB/s.
 template <typename E, int VB, bool MX4>
 __global__ __launch_bounds__(kThreads) void pack_kernel(PackParams p) {

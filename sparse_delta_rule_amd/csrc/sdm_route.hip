@@ -157,8 +157,8 @@ template <int KEYS> struct SmallLds {
 // that are not whole lanes is in doubt, the row is done again by exact_small_row.
 //
 // What bounds it, at 32768 rows of 256 float32 keys, 8 chosen of 4 of 8 groups with a
-// bias (27 us; the logits and the choice alone take 7 at a copy's rate): 1570 VALU
-// instructions for four rows, a third of them the twelve rounds, 22 us of issue.
+// bias (26 us; the logits and the choice alone take 6 at a copy's rate): 1410 VALU
+// instructions for four rows, a third of them the twelve rounds, 19 us of issue.
 template <typename E, int VPT, int LANES, bool VEC>
 __global__ __launch_bounds__(64, 6) void route_small_kernel(RouteParams p) {
     constexpr int kRows = 64 / LANES;

@@ -48,10 +48,11 @@ template <int THREADS, bool GENERAL> struct BlockLds {
 // those are put in LDS, given their exact values and ranked by counting. Where more
 // reach it than LDS holds (ties, masked rows, large keys all in a few lanes) the
 // exact k-th key is found by bisection over its bits. With a bias, a row of more near-ties
-// at its k-th key than LDS holds goes to exact_row.
+// at its k-th key than LDS holds goes to exact_row (a softmax's slack does not shrink with its
+// scores, so 16384 flat ones, of logits of a spread of 0.2, are near-ties: about 100 times as long).
 //
 // What bounds it, at 4096 rows of 16384 bfloat16 keys with their softmax (53 us; the
-// logits alone take 26 at a copy's rate): 537 VALU instructions for each 64 x 32 keys,
+// logits alone take 22 at a copy's rate): 537 VALU instructions for each 64 x 32 keys,
 // 31 us of issue, and the phases between the barriers, which three rows of a CU
 // cover only in part. 512 rows of 2048 keys, 256 chosen (18 us) are two rows a CU and
 // the latency of their phases.
