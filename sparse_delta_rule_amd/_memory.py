@@ -152,11 +152,16 @@ class PackedBank:
                              dtype=_KINDS[kind], device=codes.device, _device=device,
                              _head=(codes.data_ptr(), scales.data_ptr(), _KINDS[kind], num_slots, head_dim))
 
+    _FIELDS = frozenset(("codes", "scales", "num_slots", "head_dim", "kind", "dtype", "device", "_device", "_head"))
+
     def __setattr__(self, name, value):
-        raise AttributeError(f"{name} of a packed bank cannot be replaced: make another bank")
+        if name in self._FIELDS:
+            raise AttributeError(f"{name} of a packed bank cannot be replaced: make another bank")
+        super().__setattr__(name, value)
 
     def __reduce__(self):
-        return PackedBank, (self.codes, self.scales, self.head_dim, self.kind)
+        added = {name: value for name, value in self.__dict__.items() if name not in self._FIELDS}
+        return type(self), (self.codes, self.scales, self.head_dim, self.kind), added
 
     @staticmethod
     def row_bytes(head_dim: int, kind: str = "mx8") -> tuple:

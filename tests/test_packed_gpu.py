@@ -355,12 +355,14 @@ def test_a_bank_keeps_its_arrays():
         with pytest.raises(AttributeError, match="cannot be replaced"):
             setattr(packed, name, other)
     assert packed.head_dim == 128 and packed.num_slots == 16 and packed.kind == "mx8" and packed.codes.shape == (16, 128)
+    packed.name = "notes"  # a caller's own field goes along
     rows = torch.randn((16, 128), device=DEV)
     sdm_bank_pack(packed, rows)
     for copied in (copy.deepcopy(packed), pickle.loads(pickle.dumps(packed))):
         assert copied._head[:2] == (copied.codes.data_ptr(), copied.scales.data_ptr())
         assert copied.codes.data_ptr() != packed.codes.data_ptr() and copied._head[2:] == packed._head[2:]
         assert torch.equal(copied.codes, packed.codes) and torch.equal(copied.scales, packed.scales)
+        assert type(copied) is PackedBank and copied.name == "notes"
         idx, w = torch.arange(16, device=DEV)[:, None], torch.ones((16, 1), device=DEV)
         before = sdm_gather_packed(packed, idx, w, chunk=1)[0]
         sdm_bank_pack(copied, rows * 2)  # and leaves the first one as it is
