@@ -26,7 +26,7 @@
 extern "C" {
 #endif
 
-#define SDM_ABI_VERSION 4 /* 2: adds sdm_gather_compact and the gather plan; 3: sdm_round_bf16; 4: sdm_memory.h */
+#define SDM_ABI_VERSION 5 /* 2: adds sdm_gather_compact and the gather plan; 3: sdm_round_bf16; 4: sdm_memory.h; 5: sdm_train.h */
 #define SDM_MAX_WIDTH 256 /* largest W, R and gather width */
 #define SDM_MAX_ROW_BYTES (1LL << 30) /* largest bank row, head_dim x element size, in bytes */
 

@@ -19,6 +19,14 @@ banks in 8 or 4 bits:
     packed = PackedBank.empty(num_slots, head_dim, "mx8"); sdm_bank_pack(packed, rows, slots=slots)
     out0, out1 = sdm_gather_packed(packed, idx0, w0, chunk=64, idx1=..., w1=...)
     dw0, dw1 = sdm_gather_weight_grad(packed_or_bank, idx0, dout0, chunk=64, idx1=..., dout1=...)
+
+and, declared in ``include/sdm_train.h``, what trains a router and a bank:
+
+    loss, counts, mean, coef = sdm_route_balance(logits, idx, chunk=4096, per_chunk=True, scale=0.01)
+    sdm_route_balance_backward(logits, counts, coef, chunk=4096, per_chunk=True, dlogits=dlogits, accumulate=True)
+    x = sdm_lookup(table, tokens, scale=32.0, dropout=0.1, rng=rng)
+    dtable = sdm_lookup_grad(tokens, dx, len(table), scale=32.0, dropout=0.1, rng=rng)
+    dbank = sdm_gather_bank_grad(idx0, w0, dout0, len(bank), chunk=64, idx1=..., w1=..., dout1=...)
 """
 
 from ._binding import (  # noqa: F401
@@ -49,4 +57,11 @@ from ._memory import (  # noqa: F401
     sdm_gather_weight_grad,
     sdm_route,
     sdm_route_backward,
+)
+from ._train import (  # noqa: F401
+    sdm_gather_bank_grad,
+    sdm_lookup,
+    sdm_lookup_grad,
+    sdm_route_balance,
+    sdm_route_balance_backward,
 )

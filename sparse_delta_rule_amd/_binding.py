@@ -87,6 +87,20 @@ def library() -> ctypes.CDLL:
     for fn in (lib.sdm_packed_row_bytes, lib.sdm_packed_scale_bytes):
         fn.argtypes = [i32, i64]
         fn.restype = i64
+    lib.sdm_route_balance.argtypes = [P, i32, i64, i64, i32, i32, i64, i64, P, i32, f32, i64, i64, P, i32, P, P, P, P, P,
+                                      i64, P]
+    lib.sdm_route_balance_backward.argtypes = [P, i32, i64, i64, i32, i64, i64, P, i32, P, P, P, i32, P, P]
+    lib.sdm_lookup.argtypes = [P, P, i32, i64, i64, i64, P, i32, f32, f32, P, P, i32, P]
+    lib.sdm_lookup_grad.argtypes = [i64, P, i32, P, i32, f32, f32, P, P, i32, i64, i64, i32, P, i64, P]
+    lib.sdm_gather_bank_grad.argtypes = [i64, i64, i64, P, i32, i32, P, P, P, i32, P, P, P, i32, P, i32, i64, i64, i32, P,
+                                         i64, P]
+    for fn in (lib.sdm_route_balance, lib.sdm_route_balance_backward, lib.sdm_lookup, lib.sdm_lookup_grad,
+               lib.sdm_gather_bank_grad):
+        fn.restype = ctypes.c_int
+    lib.sdm_route_balance_workspace.argtypes = [i64, i64, i64, i32]
+    lib.sdm_bank_grad_workspace.argtypes = [i64, i64, i64]
+    for fn in (lib.sdm_route_balance_workspace, lib.sdm_bank_grad_workspace):
+        fn.restype = i64
     _lib = lib
     return lib
 

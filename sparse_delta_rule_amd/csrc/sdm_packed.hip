@@ -4,6 +4,7 @@
 #include "../../include/sdm_memory.h"
 #include "sdm_kernels.h"
 #include "sdm_memory.h"
+#include "sdm_rows.h"
 
 namespace sdm {
 
@@ -20,24 +21,6 @@ constexpr int kXor1 = 0xb1, kXor2 = 0x4e;               // quad_perm [1,0,3,2] a
 constexpr int kHalfMirror = 0x141, kMirror = 0x140;     // lane i of 8, of 16 <- lane 7 - i, 15 - i
 
 // ------------------------------------------------------------------ pack
-
-// Eight consecutive columns of a row as float32, VB bytes a load; columns at or
-// past `left` are 0.
-template <typename E, int VB> __device__ __forceinline__ void load_octet(const E* p, int left, float (&x)[8]) {
-    constexpr int VEC = VB / int(sizeof(E));
-    if (left >= 8) {
-        typename RawVec<VB>::T raw[8 / VEC];
-#pragma unroll
-        for (int i = 0; i < 8 / VEC; ++i) raw[i] = reinterpret_cast<const typename RawVec<VB>::T*>(p)[i];
-        E e[8];
-        __builtin_memcpy(e, raw, sizeof e);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = widen(e[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = i < left ? widen(p[i]) : 0.0f;
-    }
-}
 
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 constexpr uint32_t kInfBits = 0x7f800000u;
@@ -135,36 +118,6 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(PackParams p) {
 }
 
 // ------------------------------------------------------------------ gather
-
-// N consecutive columns of a packed row (16, or 4): their codes, and their values as float32.
-template <bool MX4, int N> struct Codes {
-    static constexpr int kBytes = MX4 ? N / 2 : N;
-    using Raw = typename RawVec<kBytes>::T;
-    static __device__ __forceinline__ void values(const Raw& v, float s, float (&x)[N]) {
-        uint32_t w[kBytes < 4 ? 1 : kBytes / 4] = {};
-        __builtin_memcpy(w, &v, kBytes);
-        if constexpr (MX4) {
-#pragma unroll
-            for (int i = 0; i < (N + 7) / 8; ++i) {
-                const F32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], s, 0);
-                const F32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], s, 1);
-                x[8 * i] = a.x, x[8 * i + 1] = a.y, x[8 * i + 2] = b.x, x[8 * i + 3] = b.y;
-                if constexpr (N >= 8) {
-                    const F32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], s, 2);
-                    const F32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], s, 3);
-                    x[8 * i + 4] = c.x, x[8 * i + 5] = c.y, x[8 * i + 6] = d.x, x[8 * i + 7] = d.y;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < N / 4; ++i) {
-                const F32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[i], s, false);
-                const F32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[i], s, true);
-                x[4 * i] = a.x, x[4 * i + 1] = a.y, x[4 * i + 2] = b.x, x[4 * i + 3] = b.y;
-            }
-        }
-    }
-};
 
 __device__ __forceinline__ bool is_live(const MemoryGatherParams& p, int64_t t) {
     const int64_t c = t / p.chunk;

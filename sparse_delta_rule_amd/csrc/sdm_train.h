@@ -1,0 +1,108 @@
+// Internal declarations of what trains a router and a bank: launch parameter blocks,
+// the layouts of the workspaces, and the launchers that the C ABI calls.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace sdm {
+
+// ------------------------------------------------------------------ balance
+// A piece is a run of tokens of one sequence, which one workgroup reads: at most 255, so
+// that a key's count in it fits 16 bits (255 * SDM_MAX_WIDTH < 2^16).
+constexpr int kMaxPiece = 255;
+
+struct BalanceParams {
+    const void* logits;
+    const int32_t* chunk_valid;
+    uint32_t tokens, chunk, valid;
+    int keys, k, score;
+    int per_chunk, piece;
+    uint32_t sequence;  // tokens of a sequence
+    uint32_t sequences, pieces;  // pieces of each sequence
+    double scale;
+    uint32_t streams;
+    int64_t stream_slots;
+    const void* idx;
+    int idx64;
+    int32_t* counts;
+    float* mean;
+    float* coef;
+    float* loss;
+    // workspace
+    uint32_t* done;       // [1] workgroups of the second pass that have ended
+    uint32_t* live;       // [sequences * pieces]
+    uint32_t* live_all;   // [sequences]
+    double* loss_part;    // [sequences * key blocks]
+    float* part;          // [sequences * pieces, keys] sums of shares
+    uint32_t* part_count; // [sequences * pieces, (keys + 1) / 2] counts, two of 16 bits a word
+    // backward
+    const float* dloss;
+    void* dlogits;
+    int accumulate;
+};
+// Splits the tokens into pieces and, where `workspace` is given, places its arrays; returns the
+// workspace's bytes.
+int64_t balance_layout(BalanceParams* p, void* workspace);
+hipError_t launch_balance(const BalanceParams& p, bool bf16, hipStream_t stream);
+hipError_t launch_balance_backward(const BalanceParams& p, bool bf16, hipStream_t stream);
+
+// ------------------------------------------------------------------ lookup
+// The random bits of a lookup's columns; see sdm_lookup.
+struct Dropout {
+    const uint64_t* rng;
+    uint32_t threshold;  // 0: none
+};
+
+struct LookupParams {
+    const void* bank;
+    const uint8_t* scales;
+    int64_t num_slots, n;
+    int hd;
+    int64_t row_bytes;
+    int scale_bytes;
+    const void* idx;
+    int idx64;
+    float factor;
+    Dropout dropout;
+    void* out;
+};
+int64_t lookup_groups(const LookupParams& p);  // workgroups of the launch along its first axis
+hipError_t launch_lookup(const LookupParams& p, int bank_dtype, bool out_bf16, hipStream_t stream);
+
+// ------------------------------------------------------------------ gradient to a bank
+struct BankGradParams {
+    const void* idx[2];
+    const void* w[2];     // NULL: 1 (a lookup)
+    const void* dout[2];
+    uint32_t width[2];    // width[1] = 0: one operand
+    uint32_t tokens, chunk, valid;
+    const int32_t* chunk_valid;
+    int idx64, w_bf16;
+    float factor;
+    Dropout dropout;
+    void* dbank;
+    uint32_t num_slots;
+    int hd;
+    int add;
+    // workspace
+    uint32_t entries;
+    int passes;           // of 8 bits of a slot
+    uint32_t tiles;       // of kTile entries
+    int block, spill;     // entries of a lane group; how far it may go past their end
+    uint32_t blocks;
+    uint32_t* n;          // [1] entries that count
+    uint32_t* hist;       // [passes, tiles, 256]
+    uint32_t* total;      // [passes, 256]
+    uint32_t* keys[2];    // [entries] slots
+    uint32_t* ids[2];     // [entries] numbers of the entries
+    float* first;         // [blocks, octets * 8] sums of a run that began in an earlier block
+    float* last;          // [blocks, octets * 8] of one that goes on in the next
+};
+// From entries, num_slots and hd: the other sizes and, where `workspace` is given, the places of
+// its arrays; returns the workspace's bytes.
+int64_t bank_grad_layout(BankGradParams* p, void* workspace);
+int64_t bank_grad_groups(const BankGradParams& p, int bank_size);  // most workgroups of a launch along its first axis
+hipError_t launch_bank_grad(const BankGradParams& p, bool dout_bf16, bool bank_bf16, hipStream_t stream);
+
+}  // namespace sdm

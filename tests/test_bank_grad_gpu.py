@@ -1,0 +1,286 @@
+"""sdm_lookup_grad and sdm_gather_bank_grad against the plain implementation of
+tests/train_ref.py: bit for bit on small whole numbers, whose sums float32 holds exactly,
+and within what float32 sums allow on others."""
+
+import numpy as np
+import pytest
+import torch
+
+import train_ref as ref
+import sparse_delta_rule_amd as sdm
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda", 0)
+INF, NAN = float("inf"), float("nan")
+EPS = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}  # half a step, relative
+BOTH = [torch.float32, torch.bfloat16]
+
+
+def slots_like(kind, n, slots, seed):
+    g = torch.Generator().manual_seed(seed)
+    if kind == "even":
+        idx = torch.randint(0, slots, (n,), generator=g)
+    elif kind == "skewed":
+        idx = (torch.exp(torch.rand(n, generator=g, dtype=torch.float64) * np.log(slots)).long() - 1).clamp(0, slots - 1)
+    elif kind == "one":
+        idx = torch.full((n,), slots // 2)
+    elif kind == "runs":  # of every length up to some hundreds
+        idx = (torch.arange(n).double().sqrt() * 2).long() % slots
+    elif kind == "falling":
+        idx = (slots - 1 - torch.arange(n)) % slots
+    else:  # most of them none
+        idx = torch.where(torch.rand(n, generator=g) < 0.9, -1, torch.randint(0, slots, (n,), generator=g))
+    return idx
+
+
+def whole(shape, seed, most=3):
+    return torch.randint(-most, most + 1, shape, generator=torch.Generator().manual_seed(seed)).float()
+
+
+def lookup_case(n, slots, hd, kind, *, bank=torch.float32, out=torch.float32, index=torch.int64, add=False, p=0.0, scale=1.0,
+                exactly=True, seed=0):
+    idx = slots_like(kind, n, slots, seed + n)
+    dout = (whole((n, hd), seed) if exactly else torch.randn((n, hd), generator=torch.Generator().manual_seed(seed))).to(out)
+    rng = torch.tensor([seed * 77 + 1, (1 << 35) + n])
+    mask = ref.kept(n, hd, p, rng.tolist())
+    a = float(ref.factor(scale, p))
+    v = np.where(mask, dout.double().numpy(), 0)
+    want, size, count = ref.bank_grad(slots, idx.numpy(), lambda e: v[e], hd)
+    old = whole((slots, hd), 5, 100).to(bank)
+    dbank = old.clone().to(DEV) if add else None
+    got = sdm.sdm_lookup_grad(idx.to(index).to(DEV), dout.to(DEV), slots, scale=scale, dropout=p, rng=rng.to(DEV),
+                              bank_dtype=bank, dbank=dbank, accumulate=add)
+    assert got.dtype == bank and (got is dbank or not add)
+    check(got, want * a, size * abs(a), count, old.double().numpy() if add else None, exactly and a in (1.0, 2.0))
+
+
+def check(got, want, size, count, old, exactly):
+    total = want if old is None else want + old
+    dtype = got.dtype
+    got = got.double().cpu().numpy()
+    if exactly and dtype == torch.float32:
+        assert np.array_equal(got, total), np.argwhere(got != total)[:5]
+        return
+    # m terms: m additions of a sum at most `size`, the factor's product and the sum with what was there
+    off = (count[:, None] + 2) * 2.0 ** -24 * size * (1 + 1e-3) + 2 * 2.0 ** -24 * np.abs(total)
+    if exactly:
+        off *= 0
+    assert (np.abs(got - total) <= off + EPS[dtype] * (np.abs(total) + off) + 2.0 ** -140).all(), np.abs(got - total).max()
+    unnamed = count == 0
+    assert np.array_equal(got[unnamed], (np.zeros_like(total) if old is None else old)[unnamed])
+
+
+@pytest.mark.parametrize("kind", ["even", "skewed", "one", "runs", "falling", "none"])
+@pytest.mark.parametrize("n", [1, 2, 7, 8, 9, 63, 64, 65, 500, 4095, 4096, 4097, 9000])
+def test_lengths(n, kind):
+    lookup_case(n, 300, 24, kind)
+    lookup_case(n, 65537 if kind == "even" else 40, 3, kind, index=torch.int32, add=True)
+
+
+@pytest.mark.parametrize("add", [False, True], ids=["write", "add"])
+@pytest.mark.parametrize("out", BOTH, ids=["dout-f32", "dout-bf16"])
+@pytest.mark.parametrize("bank", BOTH, ids=["f32", "bf16"])
+@pytest.mark.parametrize("hd", [1, 2, 7, 8, 9, 40, 64, 100, 101, 128, 200, 256, 512, 513, 1024, 1032])
+def test_columns(hd, bank, out, add):
+    lookup_case(700, 50, hd, "skewed", bank=bank, out=out, add=add, index=torch.int32)
+    lookup_case(700, 50, hd, "runs", bank=bank, out=out, add=add, exactly=False, scale=0.7)
+
+
+@pytest.mark.parametrize("slots", [1, 2, 3, 255, 256, 257, 65535, 65536, 65537, (1 << 16) * 5, (1 << 24) - 1, 1 << 24, (1 << 24) + 1])
+def test_slots(slots):
+    """One to four passes of the sort, whose last digits are few or many."""
+    lookup_case(5000, slots, 2, "even")
+    lookup_case(5000, slots, 2, "skewed", add=True, index=torch.int32)
+
+
+@pytest.mark.parametrize("out", BOTH, ids=["dout-f32", "dout-bf16"])
+@pytest.mark.parametrize("hd", [5, 8, 64, 136])
+@pytest.mark.parametrize("p", [0.1, 0.5])
+def test_dropout(p, hd, out):
+    """The lookup's own mask: with p = 1/2 the factor is 2 and everything exact."""
+    lookup_case(400, 30, hd, "skewed", out=out, p=p, seed=3, exactly=p == 0.5)
+    lookup_case(400, 30, hd, "even", out=out, p=p, seed=4, exactly=p == 0.5, bank=torch.bfloat16, add=True)
+
+
+def test_dropped_columns_and_rows_outside_are_not_counted_whatever_they_hold():
+    rng = torch.tensor([3, 4])
+    mask = torch.from_numpy(ref.kept(50, 32, 0.5, rng.tolist()))
+    dout = torch.where(mask, 1.0, NAN)
+    idx = torch.arange(50) % 5
+    idx[7], dout[7] = -1, INF
+    idx[8], dout[8] = 5, NAN
+    got = sdm.sdm_lookup_grad(idx.to(DEV), dout.to(DEV), 5, dropout=0.5, rng=rng.to(DEV)).cpu()
+    want = torch.zeros((5, 32)).index_add_(0, idx.clamp(0, 4), torch.where(mask & (idx % 5 == idx)[:, None], 2.0, 0.0))
+    assert torch.equal(got, want)
+    bad = dout.clone()
+    bad[11] = NAN  # of slot 1
+    got = sdm.sdm_lookup_grad(idx.to(DEV), bad.to(DEV), 5, dropout=0.5, rng=rng.to(DEV)).cpu()
+    assert torch.isnan(got[1]).any() and torch.equal(got[[0, 2, 3, 4]], want[[0, 2, 3, 4]])
+
+
+@pytest.mark.parametrize("n", [0, 3])
+def test_nothing_to_add(n):
+    idx, dout = torch.full((n,), -1, device=DEV), torch.ones((n, 9), device=DEV)
+    got = sdm.sdm_lookup_grad(idx, dout, 70000)
+    assert got.shape == (70000, 9) and not got.any()
+    kept = torch.full((70000, 9), 4.0, device=DEV)
+    assert (sdm.sdm_lookup_grad(idx, dout, 70000, dbank=kept, accumulate=True) == 4).all()
+
+
+def test_a_lookup_and_its_gradient_are_adjoint():
+    """<lookup(B), D> = <B, lookup_grad(D)> for B and D of small whole numbers, through the same mask."""
+    B, D = whole((60, 48), 1), whole((4, 70, 48), 2)
+    idx = slots_like("skewed", 280, 60, 3).view(4, 70)
+    rng = torch.tensor([9, 10], device=DEV)
+    y = sdm.sdm_lookup(B.to(DEV), idx.to(DEV), scale=4.0, dropout=0.5, rng=rng)
+    d = sdm.sdm_lookup_grad(idx.to(DEV), D.to(DEV), 60, scale=4.0, dropout=0.5, rng=rng)
+    assert y.shape == (4, 70, 48) and (y.double().cpu() * D).sum().item() == (d.double().cpu() * B).sum().item() != 0
+
+
+def gather_case(tokens, chunk, W0, W1, slots, hd, kind, *, valid=None, cv=None, bank=torch.float32, w=torch.float32,
+                index=torch.int64, add=False, exactly=True, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    alive = ref.live(tokens, chunk, valid, None if cv is None else cv.numpy())
+    want, size, count = 0, 0, 0
+    args = []
+    for o, W in enumerate((W0, W1)):
+        if W == 0:
+            continue
+        idx = slots_like(kind, tokens * W, slots, seed + o).view(tokens, W)
+        weights = (whole((tokens, W), seed + 2 + o) if exactly else torch.randn((tokens, W), generator=g)).to(w)
+        dout = whole((tokens, hd), seed + 4 + o) if exactly else torch.randn((tokens, hd), generator=g)
+        idx[~alive], weights[~alive], dout[~alive] = 1 << 20, NAN, NAN  # padding: not read
+        flat, flat_w = np.where(alive[:, None], idx.numpy(), -1).ravel(), weights.double().numpy().ravel()
+        r, s, c = ref.bank_grad(slots, flat, lambda e: flat_w[e][:, None] * dout.double().numpy()[e // W], hd)
+        want, size, count = want + r, size + s, count + c
+        args.append((idx.to(index).to(DEV), weights.to(DEV), dout.to(DEV)))
+    second = dict(idx1=args[1][0], w1=args[1][1], dout1=args[1][2]) if W1 else {}
+    old = whole((slots, hd), 5, 100).to(bank)
+    dbank = old.clone().to(DEV) if add else None
+    got = sdm.sdm_gather_bank_grad(*args[0], slots, chunk=chunk, valid=valid, chunk_valid=None if cv is None else cv.to(DEV),
+                                   bank_dtype=bank, dbank=dbank, accumulate=add, **second)
+    check(got, want, size, count, old.double().numpy() if add else None, exactly)
+
+
+@pytest.mark.parametrize("kind", ["even", "skewed", "one", "runs"])
+@pytest.mark.parametrize("W0,W1", [(1, 0), (3, 0), (1, 1), (8, 5), (64, 64), (256, 1)])
+def test_gather_widths(W0, W1, kind):
+    gather_case(60, 12, W0, W1, 500, 40, kind, valid=7)
+    gather_case(60, 60, W0, W1, 500, 128, kind, index=torch.int32, w=torch.bfloat16, add=True)
+
+
+@pytest.mark.parametrize("bank", BOTH, ids=["f32", "bf16"])
+@pytest.mark.parametrize("w", BOTH, ids=["w-f32", "w-bf16"])
+@pytest.mark.parametrize("hd", [1, 7, 64, 100, 128, 520])
+def test_gather_types(hd, w, bank):
+    cv = torch.tensor([0, 10, 3, 9, 1], dtype=torch.int32)
+    gather_case(50, 10, 16, 9, 77, hd, "even", cv=cv, bank=bank, w=w)
+    gather_case(50, 10, 16, 9, 77, hd, "skewed", cv=cv, bank=bank, w=w, add=True, exactly=False, index=torch.int32)
+
+
+def test_gather_of_nothing_but_padding():
+    gather_case(40, 8, 5, 2, 30, 16, "even", valid=0)
+    gather_case(40, 8, 5, 2, 30, 16, "even", valid=0, add=True)
+
+
+def test_a_gather_and_its_gradient_are_adjoint():
+    B, D0, D1 = whole((90, 64), 1), whole((32, 64), 2), whole((32, 64), 3)
+    idx, w = torch.randint(0, 90, (32, 12), device=DEV), whole((32, 12), 4).to(DEV)
+    cv = torch.tensor([8, 0, 5, 2], dtype=torch.int32, device=DEV)
+    out0, _, out1 = sdm.sdm_gather(B.to(DEV), idx, w, chunk=8, chunk_valid=cv, idx1=idx, w1=2 * w, with_stash=False)
+    d = sdm.sdm_gather_bank_grad(idx, w, D0.to(DEV), 90, chunk=8, chunk_valid=cv, idx1=idx, w1=2 * w, dout1=D1.to(DEV))
+    lhs = (out0.double().cpu() * D0).sum() + (out1.double().cpu() * D1).sum()
+    assert lhs.item() == (d.double().cpu() * B).sum().item() != 0
+
+
+def test_the_gradient_by_differences():
+    """Of sum (out - target)^2 / 2 in float64 through the gather's definition."""
+    g = torch.Generator().manual_seed(1)
+    B, w, y = torch.randn((20, 8), generator=g), torch.randn((16, 4), generator=g), torch.randn((16, 8), generator=g)
+    idx = torch.randint(0, 20, (16, 4), generator=g)
+
+    def loss(bank):
+        return ((((bank[idx].double() * w.double()[..., None]).sum(1)) - y) ** 2).sum().item() / 2
+
+    out, _, _ = sdm.sdm_gather(B.to(DEV), idx.to(DEV), w.to(DEV), chunk=16, with_stash=False)
+    d = sdm.sdm_gather_bank_grad(idx.to(DEV), w.to(DEV), out - y.to(DEV), 20, chunk=16).cpu()
+    B = B.double()
+    for s, c in ((0, 0), (7, 3), (19, 7)):
+        up, down = B.clone(), B.clone()
+        up[s, c] += 1e-4
+        down[s, c] -= 1e-4
+        # a quadratic: its central difference is exact but for roundings, 2^-52 of a loss of some hundreds over 1e-4
+        assert d[s, c].item() == pytest.approx((loss(up) - loss(down)) / 2e-4, abs=1e-4)
+
+
+@pytest.mark.parametrize("off", [1, 2, 4])
+def test_any_alignment(off):
+    n, hd, slots = 200, 64, 20
+    idx = slots_like("skewed", n, slots, 1)
+    for out in BOTH:
+        for bank in BOTH:
+            flat = whole((n * hd + off,), 2).to(out).to(DEV)
+            dbank = torch.full((slots * hd + off + 1,), 9.0, dtype=bank, device=DEV)
+            got = sdm.sdm_lookup_grad(idx.to(DEV), flat[off:].view(n, hd), slots, dbank=dbank[off:-1].view(slots, hd))
+            want = torch.zeros((slots, hd)).index_add_(0, idx, flat[off:].view(n, hd).float().cpu())
+            assert torch.equal(got.float().cpu(), want.to(bank).float())
+            assert (dbank[:off] == 9).all() and dbank[-1].item() == 9
+
+
+@pytest.mark.parametrize("kind", ["skewed", "one"])
+def test_the_same_inputs_give_the_same_bits(kind):
+    n, slots, hd = 100000, 1000, 72
+    idx = slots_like(kind, n, slots, 1).to(DEV)
+    dout = torch.randn((n, hd), device=DEV)
+    first = sdm.sdm_lookup_grad(idx, dout, slots)
+    size = sdm.library().sdm_bank_grad_workspace(n, slots, hd)
+    for fill in (0, 0xff, 0x7f):
+        ws = torch.full((size,), fill, dtype=torch.uint8, device=DEV)
+        assert torch.equal(sdm.sdm_lookup_grad(idx, dout, slots, workspace=ws), first)
+    count = torch.bincount(idx, minlength=slots).cpu().numpy()
+    want, size = np.zeros((slots, hd)), np.zeros((slots, hd))
+    d = dout.double().cpu().numpy()
+    np.add.at(want, idx.cpu().numpy(), d)
+    np.add.at(size, idx.cpu().numpy(), np.abs(d))
+    check(first, want, size, count, None, False)
+    with pytest.raises(sdm.SdmError, match="bytes"):
+        sdm.sdm_lookup_grad(idx, dout, slots, workspace=ws[:1024])
+
+
+@pytest.mark.slow
+def test_a_bank_past_32_bit_offsets():
+    slots, hd = (1 << 25) + 5, 136  # 4.56e9 values
+    idx = torch.tensor([slots - 1, 0, slots - 1, 1 << 24, slots - 2])
+    dout = torch.arange(1, 6, dtype=torch.float32)[:, None].expand(5, hd).contiguous()
+    got = sdm.sdm_lookup_grad(idx.to(DEV), dout.to(DEV), slots, bank_dtype=torch.bfloat16)
+    assert got[[slots - 1, 0, 1 << 24, slots - 2]][:, 135].tolist() == [4, 2, 4, 5]
+    assert (got != 0).any(1).sum().item() == 4
+
+
+@pytest.mark.slow
+def test_many_entries():
+    """Several hundred tiles of the sort, both kinds of slots, and a run over thousands of blocks."""
+    g = torch.Generator(device=DEV).manual_seed(1)
+    T, W, slots = 40000, 64, 1 << 20
+    idx = torch.randint(0, slots, (T, W), generator=g, device=DEV)
+    idx[::3] = 12345
+    w = torch.randint(0, 3, (T, W), generator=g, device=DEV).float()
+    dout = torch.randint(-2, 3, (T, 16), generator=g, device=DEV).float()
+    got = sdm.sdm_gather_bank_grad(idx, w, dout, slots, chunk=40)
+    want = torch.zeros((slots, 16), dtype=torch.float64, device=DEV)
+    want.index_add_(0, idx.flatten(), (w[..., None] * dout[:, None]).view(-1, 16).double())
+    assert torch.equal(got.double(), want)
+
+
+def test_refusals():
+    idx, dout = torch.zeros(3, dtype=torch.int64, device=DEV), torch.ones((3, 8), device=DEV)
+    with pytest.raises(ValueError, match="dbank to add to"):
+        sdm.sdm_lookup_grad(idx, dout, 4, accumulate=True)
+    with pytest.raises(ValueError, match="dbank must be"):
+        sdm.sdm_lookup_grad(idx, dout, 4, dbank=torch.empty((5, 8), device=DEV))
+    with pytest.raises(TypeError, match="bank_dtype"):
+        sdm.sdm_lookup_grad(idx, dout, 4, bank_dtype=torch.float16)
+    with pytest.raises(sdm.SdmError, match="empty bank"):
+        sdm.sdm_lookup_grad(idx, dout, 0)
+    with pytest.raises(ValueError, match="w0 must be"):
+        sdm.sdm_gather_bank_grad(idx[:, None], torch.ones((3, 2), device=DEV), dout, 4, chunk=3)
