@@ -71,6 +71,16 @@ int64_t lookup_groups(const LookupParams& p);  // workgroups of the launch along
 hipError_t launch_lookup(const LookupParams& p, int bank_dtype, bool out_bf16, hipStream_t stream);
 
 // ------------------------------------------------------------------ gradient to a bank
+// n / d of n < 2^31 by a product: mul = ceil(2^shift / d), shift = 31 + ceil(log2 d), is
+// less than 2^32 and near enough for every such n (Granlund and Montgomery, 1994).
+struct Divisor {
+    uint32_t mul, shift;
+};
+
+struct Record {
+    uint32_t slot, entry;
+};
+
 struct BankGradParams {
     const void* idx[2];
     const void* w[2];     // NULL: 1 (a lookup)
@@ -85,19 +95,22 @@ struct BankGradParams {
     uint32_t num_slots;
     int hd;
     int add;
-    // workspace
+    // from the sizes
     uint32_t entries;
-    int passes;           // of 8 bits of a slot
-    uint32_t tiles;       // of kTile entries
+    uint32_t first_entries;  // of operand 0
+    Divisor by_width[2], by_chunk;
+    int passes, bits;     // of the sort, and of a slot in a pass
+    int items;            // entries of a thread of the sort; 0: one workgroup sorts them all
+    uint32_t tiles;       // of 256 * items entries
     int block, spill;     // entries of a lane group; how far it may go past their end
     uint32_t blocks;
+    // workspace
     uint32_t* n;          // [1] entries that count
-    uint32_t* hist;       // [passes, tiles, 256]
-    uint32_t* total;      // [passes, 256]
-    uint32_t* keys[2];    // [entries] slots
-    uint32_t* ids[2];     // [entries] numbers of the entries
-    float* first;         // [blocks, octets * 8] sums of a run that began in an earlier block
-    float* last;          // [blocks, octets * 8] of one that goes on in the next
+    uint32_t* hist;       // [passes, tiles, 2^bits]
+    uint32_t* total;      // [passes, 2^bits]
+    Record* records[2];   // [entries]
+    float* first;         // [blocks, columns rounded up to 8] sums of a run that began in an earlier block
+    float* last;          // [blocks, columns rounded up to 8] of one that goes on in the next
 };
 // From entries, num_slots and hd: the other sizes and, where `workspace` is given, the places of
 // its arrays; returns the workspace's bytes.
