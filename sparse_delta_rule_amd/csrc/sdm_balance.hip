@@ -6,6 +6,8 @@
 // Then p_i = e_i / sum e, and parts of a row with offsets of their own are put together
 // as parts of a softmax are: the part's sum times exp(its o - the largest o).
 
+#include <type_traits>
+
 #include "sdm_route_device.h"
 #include "sdm_train.h"
 
@@ -36,6 +38,31 @@ __device__ __forceinline__ Piece this_piece(const BalanceParams& p, uint32_t num
     r.end = begin + min(at + uint32_t(p.piece), p.sequence);
     return r;
 }
+
+// VPT keys a lane of THREADS, as they are in memory: loaded ahead of their use.
+template <typename E, int THREADS, int VPT, bool VEC> struct RawRow {
+    using Row = RowKeys<E, THREADS, VPT, VEC>;
+    static constexpr int kN = Row::kN;
+    using T = typename std::conditional<VEC, uint4, E>::type;
+    T raw[VPT / kN];
+
+    __device__ __forceinline__ void load(const E* row, int keys, int tid) {
+#pragma unroll
+        for (int i = 0; i < VPT / kN; ++i)
+            raw[i] = *reinterpret_cast<const T*>(row + min(Row::key_of(i * kN, tid), keys - kN));
+    }
+    // Clean logits; -inf past the row's end.
+    __device__ __forceinline__ void values(int keys, int tid, float (&c)[VPT]) const {
+#pragma unroll
+        for (int i = 0; i < VPT / kN; ++i) {
+            E e[kN];
+            __builtin_memcpy(e, &raw[i], sizeof e);
+            const bool in = Row::key_of(i * kN, tid) < keys;
+#pragma unroll
+            for (int j = 0; j < kN; ++j) c[i * kN + j] = in ? clean(widen(e[j])) : -INFINITY;
+        }
+    }
+};
 
 // The terms of one lane's keys, c[i] -> e_i, given the largest of the part's logits; returns the offset.
 template <int N> __device__ __forceinline__ float terms(int score, float largest, float (&c)[N]) {
@@ -92,24 +119,28 @@ __global__ __launch_bounds__(kSmallThreads) void balance_small_kernel(BalancePar
     ieee_mode_off();
     const int tid = threadIdx.x, lane = tid % LANES, row = tid / LANES;
     const Piece r = this_piece(p, blockIdx.x);
+    const E* logits = static_cast<const E*>(p.logits);
+    // Two rows ahead, the first of them before everything else.
+    RawRow<E, LANES, VPT, VEC> next[2];
+    auto load = [&](uint32_t t, RawRow<E, LANES, VPT, VEC>& to) {
+        to.load(logits + int64_t(min(t, r.end - 1)) * p.keys, p.keys, lane);
+    };
+    load(r.first + row, next[0]);
+    load(r.first + row + kRows, next[1]);
     if (blockIdx.x == 0 && tid == 0) *p.done = 0;
     for (int i = tid; i < (p.keys + 1) / 2; i += kSmallThreads) words[i] = 0;
     const int live = __syncthreads_count(r.first + tid < r.end && is_live(p, r.first + tid));
     if (tid == 0) p.live[blockIdx.x] = uint32_t(live);
     count_choices(p, r, 0, p.keys, words);
-    const E* logits = static_cast<const E*>(p.logits);
     float acc[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) acc[i] = 0.0f;
-    float next[VPT];
-    auto load = [&](uint32_t t) { Row::load(logits + int64_t(min(t, r.end - 1)) * p.keys, p.keys, lane, next); };
-    load(r.first + row);
     for (uint32_t t0 = r.first; t0 < r.end; t0 += kRows) {  // the same rounds in every wavefront
         const uint32_t t = t0 + row;
         float c[VPT];
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) c[i] = next[i];
-        load(t + kRows);
+        next[0].values(p.keys, lane, c);
+        next[0] = next[1];
+        load(t + 2 * kRows, next[1]);
         const float largest = lanes_reduce<LANES>(max_of(c, -INFINITY), [](float a, float b) { return max32(a, b); });
         terms(p.score, largest, c);
         const float sum = lanes_reduce<LANES>(sum_of(c), [](float a, float b) { return a + b; });
@@ -138,11 +169,15 @@ template <typename E, int VPT, bool VEC>
 __global__ __launch_bounds__(kBigThreads) void balance_big_kernel(BalanceParams p) {
     using Row = RowKeys<E, kBigThreads, VPT, VEC>;
     constexpr int kWaves = kBigThreads / 64;
+    constexpr bool kAhead = VPT * sizeof(E) <= 64;  // the next row is loaded while one is taken
     __shared__ float offset[2][kWaves], total[2][kWaves];
     __shared__ uint32_t words[kCountKeys / 2];
     ieee_mode_off();
     const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
     const Piece r = this_piece(p, blockIdx.x);
+    const E* logits = static_cast<const E*>(p.logits);
+    RawRow<E, kBigThreads, VPT, VEC> next;
+    if (kAhead) next.load(logits + int64_t(r.first) * p.keys, p.keys, tid);
     if (blockIdx.x == 0 && tid == 0) *p.done = 0;
     const int live = __syncthreads_count(r.first + tid < r.end && is_live(p, r.first + tid));
     if (tid == 0) p.live[blockIdx.x] = uint32_t(live);
@@ -156,15 +191,21 @@ __global__ __launch_bounds__(kBigThreads) void balance_big_kernel(BalanceParams 
         for (int i = tid; i < min(kCountKeys / 2, stride - base / 2); i += kBigThreads) to[i] = words[i];
         __syncthreads();
     }
-    const E* logits = static_cast<const E*>(p.logits);
     float acc[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) acc[i] = 0.0f;
     int buffer = 0;
     for (uint32_t t = r.first; t < r.end; ++t) {
-        if (!is_live(p, t)) continue;  // of the whole workgroup
         float c[VPT];
-        Row::load(logits + int64_t(t) * p.keys, p.keys, tid, c);
+        if (kAhead) {
+            next.values(p.keys, tid, c);
+            next.load(logits + int64_t(min(t + 1, r.end - 1)) * p.keys, p.keys, tid);
+        }
+        if (!is_live(p, t)) continue;  // of the whole workgroup
+        if (!kAhead) {
+            next.load(logits + int64_t(t) * p.keys, p.keys, tid);
+            next.values(p.keys, tid, c);
+        }
         const float largest = lanes_reduce<64>(max_of(c, -INFINITY), [](float a, float b) { return max32(a, b); });
         const float o = terms(p.score, largest, c);
         const float sum = lanes_reduce<64>(sum_of(c), [](float a, float b) { return a + b; });
@@ -189,8 +230,8 @@ __global__ __launch_bounds__(kBigThreads) void balance_big_kernel(BalanceParams 
 
 // ------------------------------------------------------------------ second pass: sequences
 
-constexpr int kJoinThreads = 512;
-constexpr int kJoinKeys = 64;  // keys of an item, a lane each
+constexpr int kJoinThreads = 1024;
+constexpr int kJoinKeys = 64;  // keys of an item
 
 template <typename T> __device__ __forceinline__ T wave_sum(T v) {
     for (int n = 1; n < 64; n *= 2) v += __shfl_xor(v, n);
@@ -206,48 +247,70 @@ template <typename T> __device__ __forceinline__ T join_sum(T v, T* lds) {
     return v;
 }
 
-// An item is 64 keys of a sequence: the pieces' sums and counts in order, in float64. The
-// workgroup that ends last puts the items' parts of the loss together.
+// An item is 64 keys of a sequence: the pieces' sums and counts in order, in float64. 16 lanes take
+// a piece's keys, four each, so that a workgroup reads 64 pieces at a time. The workgroup that ends
+// last puts the items' parts of the loss together.
 __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceParams p) {
-    constexpr int kWaves = kJoinThreads / 64;
-    __shared__ double sums[kWaves][kJoinKeys];
-    __shared__ int32_t counts[kWaves][kJoinKeys];
+    constexpr int kRows = kJoinThreads / 16, kWaves = kJoinThreads / 64;
+    __shared__ double sums[kRows][kJoinKeys];
+    __shared__ int32_t counts[kRows][kJoinKeys];
     __shared__ double scratch[kWaves];
     __shared__ uint32_t ticket;
-    const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+    const int tid = threadIdx.x, row = tid / 16, k0 = tid % 16 * 4;
     const uint32_t blocks = uint32_t(p.keys + kJoinKeys - 1) / kJoinKeys;
     const uint64_t items = uint64_t(p.sequences) * blocks;
     const int stride = (p.keys + 1) / 2;
+    const bool vec = p.keys % 4 == 0;  // the pieces' rows are 16-byte vectors of sums, and 8-byte ones of counts
     for (uint64_t item = blockIdx.x; item < items; item += gridDim.x) {
         const uint32_t g = uint32_t(item / blocks), b = uint32_t(item % blocks);
         const uint64_t first = uint64_t(g) * p.pieces;
-        uint64_t n = 0;
+        const int key = int(b) * kJoinKeys + k0;
+        double n = 0;
         for (uint32_t i = tid; i < p.pieces; i += kJoinThreads) n += p.live[first + i];
-        const uint32_t live = uint32_t(join_sum(double(n), scratch));
-        const int key = int(b) * kJoinKeys + lane;
-        double sum = 0;
-        int32_t count = 0;
+        double sum[4] = {};
+        int32_t count[4] = {};
         if (key < p.keys) {
-#pragma unroll 4
-            for (uint32_t i = wave; i < p.pieces; i += kWaves) {
-                sum += double(p.part[(first + i) * p.keys + key]);
-                count += int32_t(p.part_count[(first + i) * stride + key / 2] >> (key & 1) * 16 & 0xffffu);
+#pragma unroll 8
+            for (uint32_t i = row; i < p.pieces; i += kRows) {
+                const float* part = p.part + (first + i) * p.keys + key;
+                const uint32_t* words = p.part_count + (first + i) * stride + key / 2;
+                float4 v = {};
+                uint2 c = {};
+                if (vec) {
+                    v = *reinterpret_cast<const float4*>(part);
+                    c = *reinterpret_cast<const uint2*>(words);
+                } else {
+                    v.x = part[0];
+                    if (key + 1 < p.keys) v.y = part[1];
+                    if (key + 2 < p.keys) v.z = part[2];
+                    if (key + 3 < p.keys) v.w = part[3];
+                    c.x = words[0];
+                    if (key + 2 < p.keys) c.y = words[1];
+                }
+                sum[0] += v.x, sum[1] += v.y, sum[2] += v.z, sum[3] += v.w;
+                count[0] += c.x & 0xffff, count[1] += c.x >> 16, count[2] += c.y & 0xffff, count[3] += c.y >> 16;
             }
         }
-        sums[wave][lane] = sum;
-        counts[wave][lane] = count;
-        __syncthreads();
-        if (wave == 0) {
-            for (int w = 1; w < kWaves; ++w) {
-                sum += sums[w][lane];
-                count += counts[w][lane];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            sums[row][k0 + j] = sum[j];
+            counts[row][k0 + j] = count[j];
+        }
+        const uint32_t live = uint32_t(join_sum(n, scratch));  // and a barrier
+        if (tid < kJoinKeys) {
+            const int key = int(b) * kJoinKeys + tid, rows = int(min(p.pieces, uint32_t(kRows)));
+            double s = 0;
+            int32_t c = 0;
+            for (int r = 0; r < rows; ++r) {
+                s += sums[r][tid];
+                c += counts[r][tid];
             }
             if (key < p.keys) {
-                p.counts[int64_t(g) * p.keys + key] = count;
-                p.mean[int64_t(g) * p.keys + key] = live > 0 ? float(sum / live) : 0.0f;
+                p.counts[int64_t(g) * p.keys + key] = c;
+                p.mean[int64_t(g) * p.keys + key] = live > 0 ? float(s / live) : 0.0f;
             }
-            const double part = wave_sum(double(count) * sum);
-            if (lane == 0) {
+            const double part = wave_sum(double(c) * s);
+            if (tid == 0) {
                 p.loss_part[item] = part;
                 if (b == 0) p.live_all[g] = live;
             }
@@ -261,9 +324,9 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceParam
     __syncthreads();
     if (ticket != gridDim.x - 1) return;
     __threadfence();
-    uint64_t with = 0;
+    double with = 0;
     for (uint32_t g = tid; g < p.sequences; g += kJoinThreads) with += p.live_all[g] > 0;
-    const double sequences = join_sum(double(with), scratch);
+    const double sequences = join_sum(with, scratch);
     auto coef = [&](uint32_t g) {
         const double n = p.live_all[g];
         return n > 0 ? p.scale * p.keys / (double(p.k) * n * n * sequences) : 0.0;
@@ -350,13 +413,21 @@ __global__ __launch_bounds__(kSmallThreads) void balance_backward_small_kernel(B
     const Piece r = this_piece(p, blockIdx.x);
     const E* logits = static_cast<const E*>(p.logits);
     E* dlogits = static_cast<E*>(p.dlogits);
+    RawRow<E, LANES, VPT, VEC> next[2];  // two rows ahead
+    auto load = [&](uint32_t t, RawRow<E, LANES, VPT, VEC>& to) {
+        to.load(logits + int64_t(min(t, r.end - 1)) * p.keys, p.keys, lane);
+    };
+    load(r.first + row, next[0]);
+    load(r.first + row + kRows, next[1]);
     int32_t count[VPT];
     load_counts<Row>(p, r.sequence, lane, count);
     const float f = row_factor(p, r.sequence);
     for (uint32_t t = r.first + row; t < r.end; t += kRows) {
         const bool live = is_live(p, t);
         float x[VPT], e[VPT], g[VPT];
-        Row::load(logits + int64_t(t) * p.keys, p.keys, lane, x);
+        next[0].values(p.keys, lane, x);
+        next[0] = next[1];
+        load(t + 2 * kRows, next[1]);
         const float largest = lanes_reduce<LANES>(max_of(x, -INFINITY), [](float a, float b) { return max32(a, b); });
         int32_t top = INT32_MIN;
 #pragma unroll
@@ -391,6 +462,9 @@ __global__ __launch_bounds__(kBigThreads) void balance_backward_big_kernel(Balan
     const Piece r = this_piece(p, blockIdx.x);
     const E* logits = static_cast<const E*>(p.logits);
     E* dlogits = static_cast<E*>(p.dlogits);
+    constexpr bool kAhead = VPT * sizeof(E) <= 64;  // the next row is loaded while one is taken
+    RawRow<E, kBigThreads, VPT, VEC> next;
+    if (kAhead) next.load(logits + int64_t(r.first) * p.keys, p.keys, tid);
     int32_t count[VPT];
     load_counts<Row>(p, r.sequence, tid, count);
     const float f = row_factor(p, r.sequence);
@@ -398,6 +472,10 @@ __global__ __launch_bounds__(kBigThreads) void balance_backward_big_kernel(Balan
     for (uint32_t t = r.first; t < r.end; ++t) {
         E* out = dlogits + int64_t(t) * p.keys;
         float x[VPT], e[VPT], g[VPT];
+        if (kAhead) {
+            next.values(p.keys, tid, x);
+            next.load(logits + int64_t(min(t + 1, r.end - 1)) * p.keys, p.keys, tid);
+        }
         if (!is_live(p, t)) {  // of the whole workgroup
             if (!p.accumulate) {
 #pragma unroll
@@ -406,7 +484,10 @@ __global__ __launch_bounds__(kBigThreads) void balance_backward_big_kernel(Balan
             }
             continue;
         }
-        Row::load(logits + int64_t(t) * p.keys, p.keys, tid, x);
+        if (!kAhead) {
+            next.load(logits + int64_t(t) * p.keys, p.keys, tid);
+            next.values(p.keys, tid, x);
+        }
         const float largest = lanes_reduce<64>(max_of(x, -INFINITY), [](float a, float b) { return max32(a, b); });
         int32_t mine = INT32_MIN;
 #pragma unroll
@@ -455,7 +536,7 @@ __global__ __launch_bounds__(kBigThreads) void balance_backward_big_kernel(Balan
 
 // ------------------------------------------------------------------ launches
 
-constexpr int64_t kPieces = 512;  // pieces wanted of a call with many tokens
+constexpr int64_t kPieces = 512, kBigPieces = 256;  // pieces wanted of a call with many tokens
 
 template <typename E, int LANES, int VPT> void run_small(const BalanceParams& p, bool vec, bool backward, hipStream_t s) {
     const dim3 grid{unsigned(p.sequences * p.pieces)}, block{kSmallThreads};
@@ -489,7 +570,8 @@ template <typename E> void run_rows(const BalanceParams& p, bool backward, hipSt
 int64_t balance_layout(BalanceParams* p, void* workspace) {
     p->sequence = p->per_chunk ? p->chunk : p->tokens;
     p->sequences = p->per_chunk ? p->tokens / p->chunk : 1;
-    int64_t piece = (int64_t(p->tokens) + kPieces - 1) / kPieces;
+    const int64_t wanted = p->keys > kSmallKeys ? kBigPieces : kPieces;
+    int64_t piece = (int64_t(p->tokens) + wanted - 1) / wanted;
     if (piece > kMaxPiece) piece = kMaxPiece;
     if (piece > p->sequence) piece = p->sequence;
     if (piece < 1) piece = 1;

@@ -21,31 +21,31 @@ __device__ __forceinline__ uint32_t divide(uint32_t n, const Divisor& d) {
     return uint32_t(uint64_t(n) * d.mul >> d.shift);
 }
 
-// Where an entry's token is: its operand and number.
-struct Place {
-    uint32_t op, token, at;  // at: the entry's number in its operand
-};
-template <bool LOOKUP> __device__ __forceinline__ Place place_of(const BankGradParams& p, uint32_t e) {
-    if (LOOKUP) return {0, e, e};
-    const uint32_t op = e >= p.first_entries, at = op ? e - p.first_entries : e;
-    const Divisor d = op ? p.by_width[1] : p.by_width[0];
-    return {op, divide(at, d), at};
-}
-
 constexpr uint32_t kNone = 0xffffffffu;
-// An entry's slot, or kNone where it does not count. All of its loads are made whatever the others
-// bring, so that those of many entries are in flight together.
-template <bool LOOKUP> __device__ __forceinline__ uint32_t slot_of(const BankGradParams& p, uint32_t e) {
-    const Place r = place_of<LOOKUP>(p, e);
-    const int64_t s = slot_at(r.op ? p.idx[1] : p.idx[0], r.at, p.idx64 ? 8 : 4);
+struct Entry {
+    Record r;  // slot kNone: does not count
+    float w;
+};
+
+// Entry e of the call. All of its loads are made whatever the others bring, so that those of many
+// entries are in flight together.
+template <bool LOOKUP> __device__ __forceinline__ Entry entry_of(const BankGradParams& p, uint32_t e) {
+    const bool second = !LOOKUP && e >= p.first_entries;
+    const uint32_t at = second ? e - p.first_entries : e;
+    const int64_t s = slot_at(second ? p.idx[1] : p.idx[0], at, p.idx64 ? 8 : 4);
     bool counts = uint64_t(s) < uint64_t(p.num_slots);
+    uint32_t token = e;
+    float w = 1.0f;
     if (!LOOKUP) {
-        const uint32_t c = divide(r.token, p.by_chunk);
+        const Divisor by_width = second ? p.by_width[1] : p.by_width[0];
+        token = divide(at, by_width);
+        const uint32_t c = divide(token, p.by_chunk);
         int32_t limit = int32_t(p.valid);
         if (p.chunk_valid != nullptr) limit = p.chunk_valid[c];
-        counts &= int32_t(r.token - c * p.chunk) < limit;
+        counts &= int32_t(token - c * p.chunk) < limit;
+        w = value_at(second ? p.w[1] : p.w[0], at, p.w_bf16 ? 2 : 4);
     }
-    return counts ? uint32_t(s) : kNone;
+    return {{counts ? uint32_t(s) : kNone, token | (second ? kSecond : 0)}, w};
 }
 
 // ------------------------------------------------------------------ sort
@@ -74,12 +74,11 @@ __device__ __forceinline__ uint32_t lanes_below(uint64_t lanes) {
 // Each of a wavefront's ITEMS entries (64 neighbours at a time): how many of its earlier ones have
 // the same digit. count: the wavefront's own, of each digit, 0 before and its sum after.
 template <int ITEMS>
-__device__ __forceinline__ void rank_items(const uint32_t (&slot)[ITEMS], int pass, int bits, uint32_t* count,
-                                           uint32_t (&rank)[ITEMS]) {
+__device__ __forceinline__ void rank_items(const Entry (&e)[ITEMS], int pass, int bits, uint32_t* count, uint32_t (&rank)[ITEMS]) {
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-        const bool has = slot[i] != kNone;
-        const uint32_t digit = digit_of(slot[i], pass, bits);
+        const bool has = e[i].r.slot != kNone;
+        const uint32_t digit = digit_of(e[i].r.slot, pass, bits);
         const uint64_t same = lanes_with(digit, has, bits);
         const uint32_t below = lanes_below(same);
         rank[i] = 0;
@@ -115,27 +114,25 @@ template <int THREADS> __device__ __forceinline__ uint32_t sum_below(uint32_t v,
 // Few entries: one workgroup sorts them in LDS, all passes in one launch.
 constexpr int kOneThreads = 1024;
 constexpr int kOneWaves = kOneThreads / 64;
-constexpr int kOneItems = 8;
-constexpr uint32_t kOneEntries = kOneThreads * kOneItems;
 
 template <bool LOOKUP, int ITEMS> __global__ __launch_bounds__(kOneThreads) void sort_one_kernel(BankGradParams p) {
-    __shared__ Record records[kOneThreads * ITEMS];
+    constexpr uint32_t kMost = kOneThreads * ITEMS;
+    __shared__ Record records[kMost];
+    __shared__ float weights[LOOKUP ? 1 : kMost];
     __shared__ uint32_t count[kOneWaves][kMaxDigits];
     __shared__ uint32_t scratch[kOneWaves];
     const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, digits = 1 << p.bits;
-    uint32_t slot[ITEMS], entry[ITEMS], rank[ITEMS], n = p.entries;
+    uint32_t rank[ITEMS], n = p.entries;
+    Entry e[ITEMS];
     const uint32_t first = wave * (64 * ITEMS) + lane;
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-        entry[i] = first + i * 64;
-        slot[i] = slot_of<LOOKUP>(p, min(entry[i], n - 1));
-    }
+    for (int i = 0; i < ITEMS; ++i) e[i] = entry_of<LOOKUP>(p, min(first + i * 64, n - 1));
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) slot[i] = entry[i] < n ? slot[i] : kNone;
+    for (int i = 0; i < ITEMS; ++i) e[i].r.slot = first + i * 64 < n ? e[i].r.slot : kNone;
     for (int pass = 0; pass < p.passes; ++pass) {
-        for (int i = tid; i < kOneWaves * digits; i += kOneThreads) count[i / digits][i % digits] = 0;
+        for (int i = tid; i < kOneWaves << p.bits; i += kOneThreads) count[i >> p.bits][i & (digits - 1)] = 0;
         __syncthreads();
-        rank_items<ITEMS>(slot, pass, p.bits, count[wave], rank);
+        rank_items<ITEMS>(e, pass, p.bits, count[wave], rank);
         __syncthreads();
         uint32_t all = 0;
         if (tid < digits)
@@ -150,127 +147,152 @@ template <bool LOOKUP, int ITEMS> __global__ __launch_bounds__(kOneThreads) void
         }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i)
-            if (slot[i] != kNone) records[count[wave][digit_of(slot[i], pass, p.bits)] + rank[i]] = Record{slot[i], entry[i]};
+        for (int i = 0; i < ITEMS; ++i) {
+            if (e[i].r.slot == kNone) continue;
+            const uint32_t to = count[wave][digit_of(e[i].r.slot, pass, p.bits)] + rank[i];
+            records[to] = e[i].r;
+            if (!LOOKUP) weights[to] = e[i].w;
+        }
         __syncthreads();
         if (pass == p.passes - 1) break;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
-            const Record r = records[min(first + i * 64, uint32_t(kOneThreads * ITEMS - 1))];
-            slot[i] = first + i * 64 < n ? r.slot : kNone;
-            entry[i] = r.entry;
+            const uint32_t from = min(first + i * 64, kMost - 1);
+            e[i] = {records[from], LOOKUP ? 1.0f : weights[from]};
+            e[i].r.slot = first + i * 64 < n ? e[i].r.slot : kNone;
         }
     }
-    Record* to = p.records[(p.passes - 1) & 1];
-    for (uint32_t i = tid; i < n; i += kOneThreads) to[i] = records[i];
+    const int to = (p.passes - 1) & 1;
+    for (uint32_t i = tid; i < n; i += kOneThreads) {
+        p.records[to][i] = records[i];
+        if (!LOOKUP) p.weights[to][i] = weights[i];
+    }
     if (tid == 0) *p.n = n;
 }
 
 constexpr int kWaves = kThreads / 64;
 
-// The slots of a thread's entries of a tile, `stride` apart; kNone past the end.
-template <bool FIRST, bool LOOKUP, int ITEMS>
-__device__ __forceinline__ void load_slots(const BankGradParams& p, int pass, uint32_t first, uint32_t stride, uint32_t n,
-                                           uint32_t (&slot)[ITEMS], uint32_t (&entry)[ITEMS]) {
+// A thread's entries of a tile, `stride` apart; slot kNone past the end. WEIGHTS: with their weights.
+template <bool FIRST, bool LOOKUP, bool WEIGHTS, int ITEMS>
+__device__ __forceinline__ void load_entries(const BankGradParams& p, int pass, uint32_t first, uint32_t stride, uint32_t n,
+                                             Entry (&e)[ITEMS]) {
     if (n == 0) {
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) slot[i] = kNone, entry[i] = 0;
+        for (int i = 0; i < ITEMS; ++i) e[i] = {{kNone, 0}, 0.0f};
         return;
     }
+    const int from = (pass - 1) & 1;
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-        entry[i] = min(first + i * stride, n - 1);
-        if (FIRST) {
-            slot[i] = slot_of<LOOKUP>(p, entry[i]);
-        } else {
-            const Record r = p.records[(pass - 1) & 1][entry[i]];
-            slot[i] = r.slot;
-            entry[i] = r.entry;
-        }
+        const uint32_t at = min(first + i * stride, n - 1);
+        if (FIRST) e[i] = entry_of<LOOKUP>(p, at);
+        else e[i] = {p.records[from][at], WEIGHTS ? p.weights[from][at] : 1.0f};
     }
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) slot[i] = first + i * stride < n ? slot[i] : kNone;
+    for (int i = 0; i < ITEMS; ++i) e[i].r.slot = first + i * stride < n ? e[i].r.slot : kNone;
 }
 
-__device__ __forceinline__ uint32_t* hist_of(const BankGradParams& p, int pass, uint32_t tile) {
-    return p.hist + (int64_t(pass) * p.tiles + tile) * (1 << p.bits);
+// The count of a tile's entries that have a digit: tiles side by side where they are scanned, digits
+// where every workgroup adds the tiles up.
+template <bool SUMS> __device__ __forceinline__ uint32_t* hist_of(const BankGradParams& p, int pass, uint32_t tile, int digit) {
+    if (SUMS) return p.hist + ((int64_t(pass) * p.tiles + tile) << p.bits) + digit;
+    return p.hist + ((int64_t(pass) << p.bits) + digit) * p.stride + tile;
 }
 
 // How many entries of each tile have each digit.
-template <bool FIRST, bool LOOKUP, int ITEMS>
+template <bool FIRST, bool LOOKUP, int ITEMS, bool SUMS>
 __global__ __launch_bounds__(kThreads) void sort_count_kernel(BankGradParams p, int pass) {
     __shared__ uint32_t count[kMaxDigits];
     const int digits = 1 << p.bits;
     for (int d = threadIdx.x; d < digits; d += kThreads) count[d] = 0;
     __syncthreads();
     const uint32_t n = FIRST ? p.entries : *p.n;
-    uint32_t slot[ITEMS], entry[ITEMS];
-    load_slots<FIRST, LOOKUP, ITEMS>(p, pass, blockIdx.x * uint32_t(kThreads * ITEMS) + threadIdx.x, kThreads, n, slot, entry);
+    Entry e[ITEMS];
+    load_entries<FIRST, LOOKUP, false, ITEMS>(p, pass, blockIdx.x * uint32_t(kThreads * ITEMS) + threadIdx.x, kThreads, n, e);
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i)
-        if (slot[i] != kNone) atomicAdd(&count[digit_of(slot[i], pass, p.bits)], 1u);
+        if (e[i].r.slot != kNone) atomicAdd(&count[digit_of(e[i].r.slot, pass, p.bits)], 1u);
     __syncthreads();
-    uint32_t* hist = hist_of(p, pass, blockIdx.x);
-    for (int d = threadIdx.x; d < digits; d += kThreads) hist[d] = count[d];
+    for (int d = threadIdx.x; d < digits; d += kThreads) *hist_of<SUMS>(p, pass, blockIdx.x, d) = count[d];
 }
 
-// For each digit, the entries of lower tiles that have it, in place, and of all of them.
-constexpr int kScanDigits = 32, kScanParts = 32;
-__global__ __launch_bounds__(kScanDigits * kScanParts) void sort_scan_kernel(BankGradParams p, int pass) {
-    __shared__ uint32_t sums[kScanParts][kScanDigits];
-    const int d = threadIdx.x % kScanDigits, part = threadIdx.x / kScanDigits;
-    const int digits = 1 << p.bits, digit = min(int(blockIdx.x) * kScanDigits + d, digits - 1);
-    uint32_t* hist = hist_of(p, pass, 0) + digit;
-    const int64_t each = (int64_t(p.tiles) + kScanParts - 1) / kScanParts;
-    const int64_t begin = min(part * each, int64_t(p.tiles)), end = min(begin + each, int64_t(p.tiles));
-    uint32_t sum = 0;
-#pragma unroll 8
-    for (int64_t i = begin; i < end; ++i) sum += hist[i * digits];
-    sums[part][d] = sum;
-    __syncthreads();
-    if (int(blockIdx.x) * kScanDigits + d >= digits) return;
-    uint32_t before = 0, all = 0;
-    for (int i = 0; i < kScanParts; ++i) {
-        before += i < part ? sums[i][d] : 0;
-        all += sums[i][d];
+// For each digit, the entries of lower tiles that have it, in place, and of all of them: a
+// workgroup a digit, kScanTiles tiles at a time.
+constexpr uint32_t kScanEach = 4, kScanTiles = kThreads * kScanEach;
+__global__ __launch_bounds__(kThreads) void sort_scan_kernel(BankGradParams p, int pass) {
+    __shared__ uint32_t scratch[2][kWaves];
+    const int digits = 1 << p.bits;
+    uint32_t* hist = p.hist + (int64_t(pass) * digits + blockIdx.x) * p.stride;
+    uint32_t before = 0;
+    int buffer = 0;
+    for (uint32_t i0 = 0; i0 < p.tiles; i0 += kScanTiles, buffer ^= 1) {
+        const uint32_t i = i0 + threadIdx.x * kScanEach;  // p.stride is a multiple of kScanEach
+        uint4 v = {};
+        if (i < p.tiles) v = *reinterpret_cast<const uint4*>(hist + i);
+        v.y = i + 1 < p.tiles ? v.y : 0;
+        v.z = i + 2 < p.tiles ? v.z : 0;
+        v.w = i + 3 < p.tiles ? v.w : 0;
+        uint32_t all;
+        uint32_t at = before + sum_below<kThreads>(v.x + v.y + v.z + v.w, scratch[buffer], &all);
+        if (i < p.tiles) *reinterpret_cast<uint4*>(hist + i) = make_uint4(at, at + v.x, at + v.x + v.y, at + v.x + v.y + v.z);
+        before += all;
     }
-#pragma unroll 8
-    for (int64_t i = begin; i < end; ++i) {
-        const uint32_t v = hist[i * digits];
-        hist[i * digits] = before;
-        before += v;
-    }
-    if (part == 0) p.total[pass * digits + digit] = all;
+    if (threadIdx.x == 0) p.total[pass * digits + blockIdx.x] = before;
 }
 
 // Puts each entry of a tile in its place of the order by this pass's digit. A wavefront takes
-// 64 neighbours at a time; the lanes of the same digit find one another by ballots.
-template <bool FIRST, bool LOOKUP, int ITEMS>
+// 64 neighbours at a time; the lanes of the same digit find one another by ballots. The tile's
+// entries are put in order in LDS first, so that those of a digit leave as one run of memory.
+// SUMS: the tiles are few, and a workgroup adds up the lower ones' counts by itself.
+template <bool FIRST, bool LOOKUP, int ITEMS, bool SUMS>
 __global__ __launch_bounds__(kThreads) void sort_place_kernel(BankGradParams p, int pass) {
+    constexpr uint32_t kTile = kThreads * ITEMS;
+    __shared__ Record records[kTile];
+    __shared__ float weights[LOOKUP ? 1 : kTile];
     __shared__ uint32_t count[kWaves][kMaxDigits];
-    __shared__ uint32_t scratch[kWaves];
+    __shared__ uint32_t go[kMaxDigits];  // where a digit's entries of this tile go, less where they are in `records`
+    __shared__ uint32_t scratch[2][kWaves];
     const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, digits = 1 << p.bits;
     const uint32_t n = FIRST ? p.entries : *p.n;
-    uint32_t slot[ITEMS], entry[ITEMS], rank[ITEMS];
-    load_slots<FIRST, LOOKUP, ITEMS>(p, pass, blockIdx.x * uint32_t(kThreads * ITEMS) + wave * (64 * ITEMS) + lane, 64, n, slot,
-                                     entry);
-    // Where each digit's entries of this tile begin: a thread takes digits 2 tid and 2 tid + 1.
-    uint32_t total[2], before[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int d = 2 * tid + j;
-        total[j] = d < digits ? p.total[pass * digits + d] : 0;
-        before[j] = d < digits ? hist_of(p, pass, blockIdx.x)[d] : 0;
-        for (int w = 0; w < kWaves; ++w) count[w][d] = 0;
+    if (!FIRST && blockIdx.x * kTile >= n) return;
+    Entry e[ITEMS];
+    uint32_t rank[ITEMS];
+    load_entries<FIRST, LOOKUP, !LOOKUP, ITEMS>(p, pass, blockIdx.x * kTile + wave * (64 * ITEMS) + lane, 64, n, e);
+    // A thread takes digits 2 tid and 2 tid + 1: those of all tiles, and of the lower ones.
+    uint32_t total[2] = {}, before[2] = {};
+    if (2 * tid < digits) {
+        if (SUMS) {
+#pragma unroll 16
+            for (uint32_t i = 0; i < p.tiles; ++i) {
+                const uint2 v = *reinterpret_cast<const uint2*>(hist_of<SUMS>(p, pass, i, 2 * tid));
+                total[0] += v.x;
+                total[1] += v.y;
+                before[0] += i < blockIdx.x ? v.x : 0;
+                before[1] += i < blockIdx.x ? v.y : 0;
+            }
+        } else {
+            const uint2 a = *reinterpret_cast<const uint2*>(p.total + pass * digits + 2 * tid);
+            total[0] = a.x, total[1] = a.y;
+            before[0] = *hist_of<SUMS>(p, pass, blockIdx.x, 2 * tid);
+            before[1] = *hist_of<SUMS>(p, pass, blockIdx.x, 2 * tid + 1);
+        }
     }
-    uint32_t all;
-    const uint32_t below = sum_below<kThreads>(total[0] + total[1], scratch, &all);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        for (int w = 0; w < kWaves; ++w) count[w][2 * tid + j] = 0;
+    uint32_t all, here;
+    const uint32_t below = sum_below<kThreads>(total[0] + total[1], scratch[0], &all);
     if (FIRST && blockIdx.x == 0 && tid == 0) *p.n = all;
-    rank_items<ITEMS>(slot, pass, p.bits, count[wave], rank);
+    rank_items<ITEMS>(e, pass, p.bits, count[wave], rank);
     __syncthreads();
+    uint32_t mine[2] = {};
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        for (int w = 0; w < kWaves; ++w) mine[j] += count[w][2 * tid + j];
+    uint32_t base = sum_below<kThreads>(mine[0] + mine[1], scratch[1], &here);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        uint32_t base = below + (j == 1 ? total[0] : 0) + before[j];
+        go[2 * tid + j] = below + (j == 1 ? total[0] : 0) + before[j] - base;
         for (int w = 0; w < kWaves; ++w) {
             const uint32_t v = count[w][2 * tid + j];
             count[w][2 * tid + j] = base;
@@ -278,166 +300,422 @@ __global__ __launch_bounds__(kThreads) void sort_place_kernel(BankGradParams p, 
         }
     }
     __syncthreads();
-    Record* to = p.records[pass & 1];
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i)
-        if (slot[i] != kNone) to[count[wave][digit_of(slot[i], pass, p.bits)] + rank[i]] = Record{slot[i], entry[i]};
+    for (int i = 0; i < ITEMS; ++i) {
+        if (e[i].r.slot == kNone) continue;
+        const uint32_t to = count[wave][digit_of(e[i].r.slot, pass, p.bits)] + rank[i];
+        records[to] = e[i].r;
+        if (!LOOKUP) weights[to] = e[i].w;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        const uint32_t from = i * kThreads + tid;
+        if (from >= here) break;
+        const Record r = records[from];
+        const uint32_t to = go[digit_of(r.slot, pass, p.bits)] + from;
+        p.records[pass & 1][to] = r;
+        if (!LOOKUP) p.weights[pass & 1][to] = weights[from];
+    }
 }
 
 // ------------------------------------------------------------------ sums
 
-// The sorted entries are cut into blocks, a lane group each; a workgroup takes neighbours. A run
-// of equal slots that ends within `spill` entries past a block's end is taken by that block to
-// its end, and the next begins behind it; of a longer one each block makes a partial sum, which
-// join_kernel adds up. cont: block b's first run began in an earlier block and is not that
-// block's alone. `at`: the slot of a sorted entry.
+// The sorted entries are cut into blocks, a lane group each. A run of equal slots that ends within
+// `spill` entries past the end of the block it begins in, or the next one's, is that block's to its
+// end, and the next begins behind it. Of a longer run each block makes a partial sum, which
+// join_kernel adds up. cont: the block of sorted entries that begins at `begin` continues such a
+// long run. at(i): the slot of sorted entry i.
 template <typename F> __device__ __forceinline__ bool cont(const BankGradParams& p, F at, uint32_t n, uint64_t begin) {
     return begin > 0 && begin + p.spill < n && at(begin - 1) == at(begin + p.spill);
 }
 
-// N neighbouring columns of a row.
-template <typename E, int VB, int N> __device__ __forceinline__ void load_columns(const E* p, int left, float (&x)[N]) {
-    constexpr int VEC = VB / int(sizeof(E));
-    if (left >= N) {
-        typename RawVec<VB>::T raw[N / VEC];
+__device__ __forceinline__ bool bit_at(uint64_t bits, int i) {
+    return (i & 32 ? uint32_t(bits >> 32) : uint32_t(bits)) >> (i & 31) & 1;
+}
+
+// N neighbouring columns of a row of hd, from column c. VEC: rows are whole vectors of N; else a
+// column at a time, those past the row's end 0.
+template <typename D, int N, bool VEC> __device__ __forceinline__ void load_columns(const D* row, int c, int hd, float (&x)[N]) {
+    if constexpr (VEC) {
+        constexpr int VB = N * int(sizeof(D)) < 16 ? N * int(sizeof(D)) : 16, M = VB / int(sizeof(D));
 #pragma unroll
-        for (int i = 0; i < N / VEC; ++i) raw[i] = reinterpret_cast<const typename RawVec<VB>::T*>(p)[i];
-        E e[N];
-        __builtin_memcpy(e, raw, sizeof e);
+        for (int i = 0; i < N; i += M) {
+            const typename RawVec<VB>::T raw = *reinterpret_cast<const typename RawVec<VB>::T*>(row + c + i);
+            D e[M];
+            __builtin_memcpy(e, &raw, VB);
 #pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = widen(e[i]);
+            for (int j = 0; j < M; ++j) x[i + j] = widen(e[j]);
+        }
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = i < left ? widen(p[i]) : 0.0f;
+        for (int i = 0; i < N; ++i) x[i] = c + i < hd ? widen(row[c + i]) : 0.0f;
     }
 }
-template <typename E, int VB, int N> __device__ __forceinline__ void store_columns(E* p, int left, const float (&x)[N]) {
-    constexpr int VEC = VB / int(sizeof(E));
-    if (left >= N) {
+// The row's new values: the sums times `factor`, and (ADD) what was there.
+template <typename E, int N, bool VEC, bool ADD>
+__device__ __forceinline__ void store_columns(E* row, int c, int hd, float factor, const float (&x)[N]) {
+    float v[N];
 #pragma unroll
-        for (int i = 0; i < N; i += VEC) {
-            float v[VEC];
+    for (int i = 0; i < N; ++i) v[i] = x[i] * factor;
+    if (ADD) {
+        float old[N];
+        load_columns<E, N, VEC>(row, c, hd, old);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) v[j] = x[i + j];
-            store_stream(reinterpret_cast<typename RawVec<VB>::T*>(p + i), Pack<E, VB>::of(v));
+        for (int i = 0; i < N; ++i) v[i] += old[i];
+    }
+    if constexpr (VEC) {
+        constexpr int VB = N * int(sizeof(E)) < 16 ? N * int(sizeof(E)) : 16, M = VB / int(sizeof(E));
+#pragma unroll
+        for (int i = 0; i < N; i += M) {
+            float part[M];
+#pragma unroll
+            for (int j = 0; j < M; ++j) part[j] = v[i + j];
+            store_stream(reinterpret_cast<typename RawVec<VB>::T*>(row + c + i), Pack<E, VB>::of(part));
         }
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (i < left) p[i] = narrow<E>(x[i]);
+            if (c + i < hd) row[c + i] = narrow<E>(v[i]);
     }
 }
 
-template <typename E, int VB, int N>
-__device__ __forceinline__ void finish(const BankGradParams& p, uint32_t slot, int c0, const float (&acc)[N]) {
-    E* row = static_cast<E*>(p.dbank) + int64_t(slot) * p.hd + c0;
-    float v[N];
-#pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = acc[j] * p.factor;
-    if (p.add) {
-        float old[N];
-        load_columns<E, VB, N>(row, p.hd - c0, old);
-#pragma unroll
-        for (int j = 0; j < N; ++j) v[j] += old[j];
-    }
-    store_columns<E, VB, N>(row, p.hd - c0, v);
-}
-
-constexpr int kMaxBlock = 64;
-constexpr int kMaxSpill = 16;
-constexpr int kMinLanes = 8;
-constexpr int kFlight = 8;  // rows whose loads are in flight together
-
+// What the sums need of an entry, put into LDS.
 struct Term {
-    uint32_t slot, token, op;
+    const void* row;  // of dout
+    uint32_t token;
     float w;
 };
 
-template <typename D, int DVB, typename E, int VB, bool WEIGHTS, bool DROP>
-__global__ __launch_bounds__(kThreads) void sum_kernel(BankGradParams p, int lanes, int slices) {
-    constexpr int N = 16 / int(sizeof(D));  // columns of a lane
-    constexpr int EVB = VB == 16 ? (N * int(sizeof(E)) < 16 ? N * int(sizeof(E)) : 16) : VB;
-    extern __shared__ Term lds[];
-    const int groups = kThreads / lanes, lane = int(threadIdx.x) % lanes, group = int(threadIdx.x) / lanes;
-    const int c0 = (int(blockIdx.x % slices) * lanes + lane) * N;
-    const int columns = (p.hd + 7) / 8 * 8;
-    const uint64_t range = uint64_t(groups) * p.block, start = blockIdx.x / slices * range;
-    const Record* records = p.records[(p.passes - 1) & 1];
-    const uint32_t n = *p.n;
-    if (start >= n) return;
-    // terms[i]: entry start - 1 + i, so that the one before the range is there
-    const Term* terms = lds;
-    const int there = int(min(range + p.spill + 2, n - start + 1));
-    for (int i = threadIdx.x; i < there; i += kThreads) {
-        const Record r = records[start + i > 0 ? start + i - 1 : 0];
-        const Place e = place_of<!WEIGHTS>(p, r.entry);
-        Term t = {r.slot, e.token, e.op, 1.0f};
-        if (WEIGHTS) t.w = value_at(e.op ? p.w[1] : p.w[0], e.at, p.w_bf16 ? 2 : 4);
-        lds[i] = t;
+constexpr int kFlight = 8;  // rows whose loads are in flight together
+
+// What the two kinds of sums share. A lane has V vectors of N columns of a row's slice, `lanes`
+// vectors apart; the lanes of a group read a vector of all of them in one run of memory.
+template <typename D, typename E, bool VEC, bool WEIGHTS, bool DROP> struct Sums {
+    static constexpr int N = 16 / int(sizeof(D));
+    static constexpr int V = 1;
+
+    const BankGradParams& p;
+    const Record* records;
+    const float* weights;
+    uint32_t n;
+    int c[V];  // the lane's columns
+    PhiloxKey key;
+
+    __device__ __forceinline__ Sums(const BankGradParams& p, int lanes, int lane, uint32_t slice) : p(p) {
+        const int last = (p.passes - 1) & 1;
+        records = p.records[last];
+        weights = p.weights[last];
+        n = *p.n;
+#pragma unroll
+        for (int v = 0; v < V; ++v) c[v] = ((int(slice) * V + v) * lanes + lane) * N;
+        key = {};
+        if (DROP) key = philox_key(p.dropout);
     }
-    __syncthreads();
-    const uint32_t b = uint32_t(blockIdx.x / slices) * groups + group;
-    const uint64_t begin = uint64_t(b) * p.block;
-    if (begin >= n || c0 >= p.hd) return;
-    auto slot_of_sorted = [&](uint64_t i) { return terms[int(i + 1 - start)].slot; };
-    const bool from_before = cont(p, slot_of_sorted, n, begin), goes_on = cont(p, slot_of_sorted, n, begin + p.block);
-    int at = int(begin + 1 - start), end = min(at + p.block, there);
-    const uint32_t last = terms[end - 1].slot;
-    if (begin > 0 && !from_before)
-        for (const uint32_t before = terms[at - 1].slot; at < end && terms[at].slot == before;) ++at;
-    if (!goes_on)
-        while (end < there && terms[end].slot == last) ++end;
-    PhiloxKey key = {};
-    if (DROP) key = philox_key(p.dropout);
-    float acc[N] = {};
-    bool open = from_before;  // the run being added up began in an earlier block
-    while (at < end) {
-        const int count = min(end - at, kFlight);
-        float x[kFlight][N];
+    __device__ __forceinline__ Term term(uint64_t i) const {
+        const uint32_t token = records[i].token;
+        const void* dout = WEIGHTS && (token & kSecond) ? p.dout[1] : p.dout[0];
+        return {static_cast<const D*>(dout) + int64_t(token & ~kSecond) * p.hd, token, WEIGHTS ? weights[i] : 1.0f};
+    }
+    __device__ __forceinline__ void load(const Term& t, float (&x)[V][N]) const {
 #pragma unroll
-        for (int u = 0; u < kFlight; ++u) {
-            const Term& t = terms[at + min(u, count - 1)];
-            const D* row = static_cast<const D*>(t.op ? p.dout[1] : p.dout[0]) + int64_t(t.token) * p.hd;
-            load_columns<D, DVB, N>(row + c0, p.hd - c0, x[u]);
+        for (int v = 0; v < V; ++v) {
+            // A vector past the row's end reads the row's last.
+            const int from = VEC ? min(c[v], p.hd - N) : c[v];
+            load_columns<D, N, VEC>(static_cast<const D*>(t.row), from, p.hd, x[v]);
         }
+    }
+    __device__ __forceinline__ void add(const Term& t, const float (&x)[V][N], float (&acc)[V][N]) const {
 #pragma unroll
-        for (int u = 0; u < kFlight; ++u) {
-            if (u >= count) break;
-            const Term t = terms[at + u];
-            const uint32_t kept = DROP ? kept_columns(key, uint32_t(c0) / 8, t.token, p.dropout.threshold) >> (c0 & 7) : 0xff;
+        for (int v = 0; v < V; ++v) {
+            const uint32_t kept =
+                DROP ? kept_columns(key, uint32_t(c[v]) / 8, t.token, p.dropout.threshold) >> (c[v] & 7) : 0xff;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                if (WEIGHTS) acc[j] = fmaf(t.w, x[u][j], acc[j]);
-                else acc[j] += kept >> j & 1 ? x[u][j] : 0.0f;
-            }
-            const bool is_last = at + u + 1 == end;
-            if (is_last || terms[at + u + 1].slot != t.slot) {
-                if (open || (is_last && goes_on)) {
-                    float* to = (open ? p.first : p.last) + int64_t(b) * columns + c0;
-#pragma unroll
-                    for (int j = 0; j < N; j += 4)
-                        *reinterpret_cast<float4*>(to + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
-                } else {
-                    finish<E, EVB, N>(p, t.slot, c0, acc);
-                }
-                open = false;
-#pragma unroll
-                for (int j = 0; j < N; ++j) acc[j] = 0.0f;
+                if (WEIGHTS) acc[v][j] = fmaf(t.w, x[v][j], acc[v][j]);
+                else if (DROP) acc[v][j] += kept >> j & 1 ? x[v][j] : 0.0f;
+                else acc[v][j] += x[v][j];
             }
         }
-        at += count;
+    }
+    __device__ __forceinline__ void clear(float (&acc)[V][N]) const {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int j = 0; j < N; ++j) acc[v][j] = 0.0f;
+    }
+    template <bool ADD> __device__ __forceinline__ void finish(uint32_t slot, const float (&acc)[V][N]) const {
+        E* row = static_cast<E*>(p.dbank) + int64_t(slot) * p.hd;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (c[v] < p.hd) store_columns<E, N, VEC, ADD>(row, c[v], p.hd, WEIGHTS ? 1.0f : p.factor, acc[v]);
+    }
+};
+
+// The grid of the sums, workgroups in eights, one on each XCD: `sums` eights for the blocks of entries,
+// then `rows` eights for the bank's rows. (Taken in turn, the blocks' workgroups, most of which end
+// at once, left the rows' to half of the compute units.)
+struct SumGrid {
+    int lanes, slices, shift;  // lanes of a group; groups that share a row's columns; log2 of p.block
+    uint32_t ranges;           // workgroups of a slice, for the blocks
+    uint32_t group_rows;       // rows of a lane group
+    uint32_t row_ranges;       // workgroups of a slice, for the rows
+    uint32_t sums, rows;
+};
+
+// ------------------------------------------------------------------ whole banks: sums of rows
+
+constexpr int kMinLanes = 4;
+constexpr int kMaxRows = 2048;       // of a workgroup
+constexpr uint32_t kStaged = 1024;   // entries of a workgroup that fit LDS
+constexpr uint32_t kScanned = 4096;  // entries that are looked at one by one for where the rows begin
+
+// The first of the sorted entries whose slot is at least `slot`: a wavefront looks at 64 places at once.
+__device__ __forceinline__ uint32_t lower_bound(const Record* records, uint32_t n, uint64_t slot) {
+    uint32_t lo = 0, len = n;
+    while (len > 0) {
+        const uint32_t step = (len + 63) / 64, q = (threadIdx.x % 64 + 1) * step - 1;
+        const uint32_t less = uint32_t(__popcll(__ballot(q < len && records[lo + min(q, len - 1)].slot < slot)));
+        lo += less * step;
+        len = min(step - 1, len - less * step);
+    }
+    return lo;
+}
+
+// A workgroup takes neighbouring rows of the bank and writes each: the sum of its entries, or 0. So
+// the bank is written once and in order. Rows of long runs are left to the blocks' sums.
+template <typename S>
+__device__ __forceinline__ void sum_rows(const S& s, const SumGrid& g, uint32_t range, uint32_t* lds) {
+    constexpr int N = S::N, V = S::V;
+    const BankGradParams& p = s.p;
+    const int tid = threadIdx.x, groups = kThreads / g.lanes, group = tid / g.lanes;
+    const uint64_t first = uint64_t(range) * groups * g.group_rows;
+    const uint32_t rows = uint32_t(min(uint64_t(groups) * g.group_rows, uint64_t(p.num_slots) - first));
+    Term* terms = reinterpret_cast<Term*>(lds);        // [kStaged]
+    uint32_t* starts = lds + kStaged * sizeof(Term) / 4;  // [rows + 1] where a row's entries begin, from the first row's
+    uint32_t* bounds = starts + groups * g.group_rows + 1;  // [2]
+    if (tid < 128) {
+        const uint32_t at = lower_bound(s.records, s.n, first + (tid < 64 ? 0 : rows));
+        if (tid % 64 == 0) bounds[tid / 64] = at;
+    }
+    __syncthreads();
+    const uint32_t lo = bounds[0], count = bounds[1] - lo;
+    if (count <= kScanned) {
+        for (uint32_t r = tid; r <= rows; r += kThreads) starts[r] = count;
+        __syncthreads();
+        for (uint32_t i = tid; i < count; i += kThreads) {
+            const int row = int(s.records[lo + i].slot - uint32_t(first));
+            const int before = i > 0 ? int(s.records[lo + i - 1].slot - uint32_t(first)) : -1;
+            for (int k = before + 1; k <= row; ++k) starts[k] = i;
+            if (i < kStaged) terms[i] = s.term(lo + i);
+        }
+    } else {
+        for (uint32_t r = tid; r <= rows; r += kThreads) {
+            uint32_t a = 0, b = count;
+            while (a < b) {
+                const uint32_t m = a + (b - a) / 2;
+                if (s.records[lo + m].slot < first + r) a = m + 1;
+                else b = m;
+            }
+            starts[r] = a;
+        }
+    }
+    __syncthreads();
+    if (s.c[0] >= p.hd) return;
+    const bool staged = count <= kStaged;
+    auto is_long = [&](uint32_t r) {
+        const uint32_t a = lo + starts[r], b = lo + starts[r + 1];
+        return b - a > uint32_t(p.spill) && (((a >> g.shift) + 1) << g.shift) + uint32_t(p.spill) < b;
+    };
+    const uint32_t r0 = min(group * g.group_rows, rows), r1 = min(r0 + g.group_rows, rows);
+    float acc[V][N];
+    s.clear(acc);
+    for (uint32_t r = r0; r < r1; ++r)
+        if (starts[r] == starts[r + 1]) s.template finish<false>(uint32_t(first) + r, acc);
+    for (uint32_t r = r0; r < r1;) {
+        if (is_long(r)) {
+            ++r;
+            continue;
+        }
+        uint32_t to = r + 1;  // rows r .. to have no long run
+        while (to < r1 && !is_long(to)) ++to;
+        uint32_t at = starts[r];
+        const uint32_t end = starts[to];
+        while (r < to && starts[r + 1] == at) ++r;
+        uint32_t row_end = starts[min(r + 1, to)];
+        while (at < end) {
+            const uint32_t some = min(end - at, uint32_t(kFlight));
+            float x[kFlight][V][N];
+            Term t[kFlight];
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u) {
+                const uint32_t i = at + min(uint32_t(u), some - 1);
+                if (staged) t[u] = terms[i];
+                else t[u] = s.term(lo + i);
+            }
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u) s.load(t[u], x[u]);
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u) {
+                if (u >= int(some)) break;
+                s.add(t[u], x[u], acc);
+                if (at + u + 1 == row_end) {
+                    s.template finish<false>(uint32_t(first) + r, acc);
+                    s.clear(acc);
+                    do {
+                        ++r;
+                        row_end = starts[min(r + 1, to)];
+                    } while (r < to && row_end == at + u + 1);
+                }
+            }
+            at += some;
+        }
+        r = to;
     }
 }
 
-// Runs over several blocks. A workgroup looks at kJoinBlocks blocks; the partial sums of each
-// run that begins in one of them are added by its lane groups in turn, and theirs in order.
+// No entries: nothing but zeros, a workgroup for each kZeroBytes.
+constexpr int64_t kZeroBytes = 65536;
+__global__ __launch_bounds__(kThreads) void zero_kernel(char* to, int64_t bytes) {
+    const int64_t begin = int64_t(blockIdx.x) * kZeroBytes, end = min(begin + kZeroBytes, bytes);
+    if (reinterpret_cast<uintptr_t>(to) % 16 == 0) {
+        for (int64_t i = begin + threadIdx.x * 16; i + 16 <= end; i += kThreads * 16)
+            store_stream(reinterpret_cast<uint4*>(to + i), uint4{});
+        for (int64_t i = end - end % 16 + threadIdx.x * 2; i < end; i += kThreads * 2) *reinterpret_cast<uint16_t*>(to + i) = 0;
+    } else {
+        for (int64_t i = begin + threadIdx.x * 2; i < end; i += kThreads * 2) *reinterpret_cast<uint16_t*>(to + i) = 0;
+    }
+}
+
+// ------------------------------------------------------------------ sums of blocks
+
+constexpr int kMaxBlock = 32;
+constexpr int kMaxSpill = 16;
+
+// The words of LDS between the entries of a block and the next's: the groups' reads then fall on
+// different banks.
+__device__ __host__ __forceinline__ int lds_place(int i, int shift) { return i + (i >> shift); }
+
+// What the entries of a range of blocks add to their rows. ALL: every run (SDM_GRAD_ADD); else the
+// long ones alone.
+template <bool ALL, typename S>
+__device__ __forceinline__ void sum_blocks(const S& s, const SumGrid& g, uint32_t range_number, uint32_t* lds) {
+    constexpr int N = S::N, V = S::V;
+    const BankGradParams& p = s.p;
+    const int groups = kThreads / g.lanes, group = int(threadIdx.x) / g.lanes;
+    const int columns = (p.hd + 7) / 8 * 8;
+    const uint64_t range = uint64_t(groups) * p.block, start = range_number * range;
+    const uint32_t n = s.n;
+    if (start >= n) return;
+    if (!ALL) {
+        auto at = [&](uint64_t i) { return s.records[i].slot; };
+        const bool some = int(threadIdx.x) <= groups && cont(p, at, n, start + uint64_t(threadIdx.x) * p.block);
+        if (!__syncthreads_or(some)) return;
+    }
+    // In LDS entry start - 1 + i has number i, so that the one before the range is there.
+    const int most = int(range) + p.spill + 2;
+    auto place = [&](int i) { return lds_place(i, g.shift); };
+    Term* terms = reinterpret_cast<Term*>(lds);
+    uint32_t* slots = lds + (place(most) + 1) * int(sizeof(Term) / 4);
+    const int there = int(min(uint64_t(most), n - start + 1));
+    for (int i = threadIdx.x; i < there; i += kThreads) {
+        const uint64_t from = start + i > 0 ? start + i - 1 : 0;
+        slots[place(i)] = s.records[from].slot;
+        terms[place(i)] = s.term(from);
+    }
+    __syncthreads();
+    const uint32_t b = range_number * groups + group;
+    const uint64_t begin = uint64_t(b) * p.block;
+    if (begin >= n || s.c[0] >= p.hd) return;
+    auto slot_of_sorted = [&](uint64_t i) { return slots[place(int(i + 1 - start))]; };
+    const bool from_before = cont(p, slot_of_sorted, n, begin), goes_on = cont(p, slot_of_sorted, n, begin + p.block);
+    int at = int(begin + 1 - start), end = min(at + p.block, there);
+    const uint32_t last = slots[place(end - 1)];
+    if (begin > 0 && !from_before)
+        for (const uint32_t earlier = slots[place(at - 1)]; at < end && slots[place(at)] == earlier;) ++at;
+    if (!goes_on)
+        while (end < there && slots[place(end)] == last) ++end;
+    auto add_up = [&](int at, int end, bool open) {  // open: the first run began in an earlier block
+        float acc[V][N];
+        s.clear(acc);
+        uint32_t slot = at < end ? slots[place(at)] : 0;
+        while (at < end) {
+            const int some = min(end - at, kFlight);
+            float x[kFlight][V][N];
+            Term t[kFlight];
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u) t[u] = terms[place(at + min(u, some - 1))];
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u) s.load(t[u], x[u]);
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u) {
+                if (u >= some) break;
+                s.add(t[u], x[u], acc);
+                const bool is_last = at + u + 1 == end;
+                const uint32_t next = is_last ? kNone : slots[place(at + u + 1)];
+                if (next != slot) {
+                    if (open || (is_last && goes_on)) {
+                        float* to = (open ? p.first : p.last) + int64_t(b) * columns;
+#pragma unroll
+                        for (int v = 0; v < V; ++v)
+#pragma unroll
+                            for (int j = 0; j < N; j += 4)
+                                if (s.c[v] < p.hd)
+                                    *reinterpret_cast<float4*>(to + s.c[v] + j) =
+                                        make_float4(acc[v][j], acc[v][j + 1], acc[v][j + 2], acc[v][j + 3]);
+                    } else {
+                        s.template finish<ALL>(slot, acc);
+                    }
+                    open = false;
+                    slot = next;
+                    s.clear(acc);
+                }
+            }
+            at += some;
+        }
+    };
+    if (ALL) {
+        add_up(at, end, from_before);
+        return;
+    }
+    // The block's first run, or its last, or both, should they be long.
+    int head = at, tail = end;
+    if (from_before)
+        for (const uint32_t first = slots[place(at)]; head < end && slots[place(head)] == first;) ++head;
+    if (goes_on)
+        while (tail > head && slots[place(tail - 1)] == last) --tail;
+    if (from_before) add_up(at, head, true);
+    if (tail < end) add_up(tail, end, false);
+}
+
+// All of a gradient's sums but the long runs' totals. The slices of a row's columns lie on XCDs of
+// their own (workgroup i runs on XCD i mod 8), so that what an XCD's L2 cache holds of dout is that
+// slice alone.
+template <typename D, typename E, bool VEC, bool WEIGHTS, bool DROP, bool ADD>
+__global__ __launch_bounds__(kThreads) void sum_kernel(BankGradParams p, SumGrid g) {
+    extern __shared__ uint4 lds16[];
+    uint32_t* lds = reinterpret_cast<uint32_t*>(lds16);
+    const bool blocks = ADD || blockIdx.x < 8 * g.sums;
+    const uint32_t number = blockIdx.x - (blocks ? 0 : 8 * g.sums), range = number / g.slices;
+    if (range >= (blocks ? g.ranges : g.row_ranges)) return;
+    const Sums<D, E, VEC, WEIGHTS, DROP> s(p, g.lanes, int(threadIdx.x) % g.lanes, number % g.slices);
+    if (blocks) sum_blocks<ADD>(s, g, range, lds);
+    else sum_rows(s, g, range, lds);
+}
+
+// ------------------------------------------------------------------ sums of blocks' sums
+
+// Runs over several blocks. A workgroup looks at 64 blocks. Of the runs that begin there each lane
+// group adds up some of the short ones; a long one's blocks are shared by all lane groups, whose
+// sums are added in order.
 constexpr int kJoinThreads = 1024;
 constexpr int kJoinBlocks = 64;
 
-template <typename E, int VB> __global__ __launch_bounds__(kJoinThreads) void join_kernel(BankGradParams p, int lanes) {
+constexpr uint32_t kShort = 16;  // blocks of a run that one lane group adds up
+
+template <typename E, bool VEC, bool ADD> __global__ __launch_bounds__(kJoinThreads) void join_kernel(BankGradParams p, int lanes) {
     constexpr int N = 4;
-    constexpr int EVB = VB == 16 ? N * int(sizeof(E)) : VB;
-    __shared__ uint64_t begins;
+    __shared__ uint64_t masks[2];
     __shared__ float sums[kJoinThreads][N];
     const int tid = threadIdx.x, groups = kJoinThreads / lanes, lane = tid % lanes, group = tid / lanes;
     const int c0 = (int(blockIdx.y) * lanes + lane) * N;
@@ -448,34 +726,68 @@ template <typename E, int VB> __global__ __launch_bounds__(kJoinThreads) void jo
     if (uint64_t(b0) * p.block >= n) return;
     auto at = [&](uint64_t i) { return records[i].slot; };
     if (tid < 64) {
-        const uint64_t begin = uint64_t(b0 + tid) * p.block;
-        bool is = cont(p, at, n, begin + p.block);
-        if (is && begin > 0) is = at(begin - 1) != at(begin + p.block - 1);
-        const uint64_t found = __ballot(is);
-        if (tid == 0) begins = found;
+        // Bit i of the first: a run of several blocks begins in block b0 + i; of the second: block
+        // b0 + 1 + i is in the middle of one.
+        const uint64_t begin = uint64_t(b0 + tid) * p.block, end = begin + p.block;
+        const bool goes_on = cont(p, at, n, end), further = goes_on && cont(p, at, n, end + p.block);
+        const bool begins = goes_on && (begin == 0 || at(begin - 1) != at(end - 1));
+        const bool through = further && at(end) == at(end + p.block - 1);
+        const uint64_t b = __ballot(begins), m = __ballot(through);
+        if (tid == 0) {
+            masks[0] = b;
+            masks[1] = m;
+        }
     }
     __syncthreads();
+    const uint64_t begins = masks[0], middles = masks[1];
+    auto add = [&](float (&acc)[N], uint32_t b, uint32_t from, uint32_t more, uint32_t stride) {
+#pragma unroll 8
+        for (uint32_t c = from; c < more; c += stride) {
+            float x[N];
+            load_columns<float, N, true>(p.first + (int64_t(b) + 1 + c) * columns, c0, p.hd, x);
+#pragma unroll
+            for (int j = 0; j < N; ++j) acc[j] += x[j];
+        }
+    };
+    auto finish = [&](uint32_t slot, const float (&acc)[N]) {
+        E* row = static_cast<E*>(p.dbank) + int64_t(slot) * p.hd;
+        store_columns<E, N, VEC, ADD>(row, c0, p.hd, p.factor, acc);
+    };
+    // The run's blocks after its first, as far as the masks tell: the middle ones, and its last.
+    auto known = [&](int i) {
+        uint32_t more = 1;
+        while (i < 64 && bit_at(middles, i)) ++i, ++more;
+        return more;
+    };
+    int turn = 0;
+    for (uint64_t left = begins; left != 0; left &= left - 1, ++turn) {
+        if (turn % groups != group) continue;
+        const int i = __ffsll(static_cast<unsigned long long>(left)) - 1;
+        const uint32_t b = b0 + uint32_t(i), more = known(i);
+        if (more > kShort || i + more > 64 || c0 >= p.hd) continue;
+        float acc[N];
+        load_columns<float, N, true>(p.last + b * columns, c0, p.hd, acc);
+        add(acc, b, 0, more, 1);
+        finish(at(uint64_t(b) * p.block + p.block - 1), acc);
+    }
     for (uint64_t left = begins; left != 0; left &= left - 1) {
-        const uint32_t b = b0 + uint32_t(__ffsll(static_cast<unsigned long long>(left))) - 1;
-        const uint32_t slot = at(uint64_t(b) * p.block + p.block - 1);
-        // The blocks after b whose first run is this one.
-        uint32_t more = 0, found;
-        do {
-            const uint64_t begin = (uint64_t(b) + 1 + more + tid) * p.block;
-            const bool is = cont(p, at, n, begin) && at(begin) == slot;
-            found = uint32_t(__syncthreads_count(is));
-            more += found;
-        } while (found == kJoinThreads);
+        const int i = __ffsll(static_cast<unsigned long long>(left)) - 1;
+        uint32_t more = known(i);
+        if (more <= kShort && i + more <= 64) continue;  // of the whole workgroup
+        const uint32_t b = b0 + uint32_t(i), slot = at(uint64_t(b) * p.block + p.block - 1);
+        if (i + more > 64) {  // perhaps further than the masks
+            uint32_t found;
+            do {
+                const uint64_t begin = (uint64_t(b) + 1 + more + tid) * p.block;
+                const bool is = cont(p, at, n, begin) && at(begin) == slot;
+                found = uint32_t(__syncthreads_count(is));
+                more += found;
+            } while (found == kJoinThreads);
+        }
         float acc[N] = {};
         if (c0 < p.hd) {
-            if (group == 0) load_columns<float, 16, N>(p.last + b * columns + c0, N, acc);
-#pragma unroll 8
-            for (uint32_t c = group; c < more; c += groups) {
-                float x[N];
-                load_columns<float, 16, N>(p.first + (int64_t(b) + 1 + c) * columns + c0, N, x);
-#pragma unroll
-                for (int j = 0; j < N; ++j) acc[j] += x[j];
-            }
+            if (group == 0) load_columns<float, N, true>(p.last + b * columns, c0, p.hd, acc);
+            add(acc, b, group, more, groups);
         }
         *reinterpret_cast<float4*>(sums[tid]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
         __syncthreads();
@@ -484,111 +796,114 @@ template <typename E, int VB> __global__ __launch_bounds__(kJoinThreads) void jo
 #pragma unroll
                 for (int j = 0; j < N; ++j) acc[j] += sums[g * lanes + lane][j];
             }
-            finish<E, EVB, N>(p, slot, c0, acc);
+            finish(slot, acc);
         }
         __syncthreads();
     }
 }
 
-// ------------------------------------------------------------------ rows that no entry names
-
-constexpr int kZeroBytes = 65536;  // of a workgroup's rows
-constexpr int kZeroRows = 1024;    // at most
-
-__device__ __forceinline__ uint32_t lower_bound(const Record* records, uint32_t n, uint64_t slot) {
-    uint32_t lo = 0, hi = n;
-    while (lo < hi) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        if (records[mid].slot < slot) lo = mid + 1;
-        else hi = mid;
-    }
-    return lo;
-}
-
-template <int VB> __global__ __launch_bounds__(kThreads) void zero_kernel(BankGradParams p, int rows, int64_t row_bytes) {
-    __shared__ uint8_t named[kZeroRows];
-    __shared__ uint32_t bounds[2];
-    const Record* records = p.records[(p.passes - 1) & 1];
-    const uint32_t n = p.entries > 0 ? *p.n : 0;
-    const int64_t first = int64_t(blockIdx.x) * rows;
-    const int count = int(min(int64_t(rows), int64_t(p.num_slots) - first));
-    for (int i = threadIdx.x; i < count; i += kThreads) named[i] = 0;
-    if (threadIdx.x < 2) bounds[threadIdx.x] = lower_bound(records, n, uint64_t(first) + (threadIdx.x == 0 ? 0 : count));
-    __syncthreads();
-    for (uint32_t i = bounds[0] + threadIdx.x; i < bounds[1]; i += kThreads) named[records[i].slot - uint32_t(first)] = 1;
-    __syncthreads();
-    const int per_row = int(row_bytes / VB);
-    char* base = static_cast<char*>(p.dbank) + first * row_bytes;
-    using T = typename RawVec<VB>::T;
-    for (int64_t v = threadIdx.x; v < int64_t(count) * per_row; v += kThreads)
-        if (!named[v / per_row]) store_stream(reinterpret_cast<T*>(base) + v, T{});
-}
-
 // ------------------------------------------------------------------ launches
 
-template <typename D, int DVB, typename E, int VB> void run_sums(const BankGradParams& p, hipStream_t stream) {
-    constexpr int N = 16 / int(sizeof(D));
-    const int vecs = (p.hd + N - 1) / N;
-    int lanes = kMinLanes;
-    while (lanes < 64 && lanes < vecs) lanes *= 2;
-    const int groups = kThreads / lanes, slices = (vecs + lanes - 1) / lanes;
-    const dim3 grid{unsigned((p.blocks + groups - 1) / groups * slices)}, block{kThreads};
-    const size_t lds = size_t(groups * p.block + p.spill + 2) * sizeof(Term);
-    if (p.w[0] != nullptr) {
-        if constexpr (sizeof(D) == 4)
-            hipLaunchKernelGGL((sum_kernel<D, DVB, E, VB, true, false>), grid, block, lds, stream, p, lanes, slices);
-    } else if (p.dropout.threshold != 0) {
-        hipLaunchKernelGGL((sum_kernel<D, DVB, E, VB, false, true>), grid, block, lds, stream, p, lanes, slices);
-    } else {
-        hipLaunchKernelGGL((sum_kernel<D, DVB, E, VB, false, false>), grid, block, lds, stream, p, lanes, slices);
+int log2_of(int v) {
+    int s = 0;
+    while ((1 << s) < v) ++s;
+    return s;
+}
+
+SumGrid sum_grid(const BankGradParams& p, int dout_size, int bank_size) {
+    const int n = 16 / dout_size, vecs = (p.hd + n - 1) / n;
+    SumGrid g{};
+    // A gather reads each token's dout once for every entry: slices of the columns, so that what the
+    // entries read of them nearly fits an XCD's 4 MB of L2, but of whole 128-byte lines of dbank.
+    g.slices = 1;
+    const int64_t bytes = (p.width[1] != 0 ? 2 : 1) * int64_t(p.tokens) * p.hd * dout_size;
+    if (p.width[0] + p.width[1] >= 8)
+        while (g.slices < 8 && bytes / g.slices > (3 << 20) && p.hd * bank_size / g.slices >= 256) g.slices *= 2;
+    if (vecs > 64 * g.slices) g.slices = (vecs + 63) / 64;
+    g.lanes = kMinLanes;
+    while (g.lanes * g.slices < vecs) g.lanes *= 2;
+    const int groups = kThreads / g.lanes;
+    g.shift = log2_of(p.block);
+    g.ranges = (p.blocks + groups - 1) / groups;
+    g.sums = uint32_t((int64_t(g.ranges) * g.slices + 7) / 8);
+    if (!p.add) {
+        // Rows of a lane group: 32 KB of the bank a workgroup. (1563 tiles of 64 KB are one and a half
+        // rounds of the compute units: 32768 tokens of 50000 x 1024, 123 against 89 us for the call; with
+        // 16 KB, 101 us.)
+        g.group_rows = 1;
+        while (g.group_rows < 32 && 2 * g.group_rows * groups <= kMaxRows &&
+               int64_t(g.group_rows) * kThreads * n * bank_size < 32768)
+            g.group_rows *= 2;
+        const int64_t rows = int64_t(groups) * g.group_rows;
+        g.row_ranges = uint32_t((p.num_slots + rows - 1) / rows);
+        g.rows = uint32_t((int64_t(g.row_ranges) * g.slices + 7) / 8);
     }
-    int join_lanes = kMinLanes;
-    while (join_lanes < 64 && join_lanes < (p.hd + 3) / 4) join_lanes *= 2;
-    const dim3 join{unsigned((p.blocks + kJoinBlocks - 1) / kJoinBlocks), unsigned(((p.hd + 3) / 4 + join_lanes - 1) / join_lanes)};
-    if (p.blocks > 1) hipLaunchKernelGGL((join_kernel<E, VB>), join, dim3(kJoinThreads), 0, stream, p, join_lanes);
+    return g;
 }
 
-template <typename D, int DVB> void run_bank(const BankGradParams& p, bool bank_bf16, bool vec, hipStream_t stream) {
-    if (bank_bf16 && vec) run_sums<D, DVB, uint16_t, 16>(p, stream);
-    else if (bank_bf16) run_sums<D, DVB, uint16_t, 2>(p, stream);
-    else if (vec) run_sums<D, DVB, float, 16>(p, stream);
-    else run_sums<D, DVB, float, 4>(p, stream);
+template <typename D, typename E, bool VEC, bool WEIGHTS, bool DROP>
+void run_sum(const BankGradParams& p, const SumGrid& g, hipStream_t stream) {
+    const int groups = kThreads / g.lanes, most = groups * p.block + p.spill + 2;
+    size_t lds = size_t(lds_place(most, g.shift) + 1) * (sizeof(Term) + 4);
+    const size_t for_rows = kStaged * sizeof(Term) + size_t(groups * g.group_rows + 3) * 4;
+    if (!p.add && for_rows > lds) lds = for_rows;
+    const dim3 grid{8 * (g.sums + g.rows)}, block{kThreads};
+    if (p.add) hipLaunchKernelGGL((sum_kernel<D, E, VEC, WEIGHTS, DROP, true>), grid, block, lds, stream, p, g);
+    else hipLaunchKernelGGL((sum_kernel<D, E, VEC, WEIGHTS, DROP, false>), grid, block, lds, stream, p, g);
 }
 
-int64_t zero_rows(int64_t row_bytes) {
-    const int64_t rows = kZeroBytes / row_bytes;
-    return rows < 1 ? 1 : rows > kZeroRows ? kZeroRows : rows;
-}
-template <int VB> void run_zero(const BankGradParams& p, int64_t row_bytes, hipStream_t stream) {
-    const int64_t rows = zero_rows(row_bytes);
-    hipLaunchKernelGGL(zero_kernel<VB>, dim3(unsigned((p.num_slots + rows - 1) / rows)), dim3(kThreads), 0, stream, p,
-                       int(rows), row_bytes);
+template <typename D, typename E, bool VEC> void run_sums(const BankGradParams& p, hipStream_t stream) {
+    const SumGrid g = sum_grid(p, int(sizeof(D)), int(sizeof(E)));
+    if (p.w[0] != nullptr) {
+        if constexpr (sizeof(D) == 4) run_sum<D, E, VEC, true, false>(p, g, stream);
+    } else if (p.dropout.threshold != 0) {
+        run_sum<D, E, VEC, false, true>(p, g, stream);
+    } else {
+        run_sum<D, E, VEC, false, false>(p, g, stream);
+    }
+    if (p.blocks <= 1) return;
+    int lanes = kMinLanes;
+    while (lanes < 64 && lanes < (p.hd + 3) / 4) lanes *= 2;
+    const dim3 join{unsigned((p.blocks + kJoinBlocks - 1) / kJoinBlocks), unsigned(((p.hd + 3) / 4 + lanes - 1) / lanes)};
+    if (p.add) hipLaunchKernelGGL((join_kernel<E, VEC, true>), join, dim3(kJoinThreads), 0, stream, p, lanes);
+    else hipLaunchKernelGGL((join_kernel<E, VEC, false>), join, dim3(kJoinThreads), 0, stream, p, lanes);
 }
 
+template <typename D, typename E> void run_types(const BankGradParams& p, hipStream_t stream) {
+    // Whole vectors of 16 / sizeof(D) columns in every row of dout and of dbank.
+    constexpr int kN = 16 / int(sizeof(D)), kBank = kN * int(sizeof(E)) < 16 ? kN * int(sizeof(E)) : 16;
+    const uintptr_t dout = reinterpret_cast<uintptr_t>(p.dout[0]) | (p.width[1] != 0 ? reinterpret_cast<uintptr_t>(p.dout[1]) : 0);
+    if (p.hd % kN == 0 && dout % 16 == 0 && reinterpret_cast<uintptr_t>(p.dbank) % kBank == 0) run_sums<D, E, true>(p, stream);
+    else run_sums<D, E, false>(p, stream);
+}
+
+// Up to this many entries one workgroup sorts them all.
+constexpr int64_t kOneEntries = 4 * kOneThreads;
 template <bool LOOKUP> void run_sort_one(const BankGradParams& p, hipStream_t stream) {
     const dim3 grid{1}, block{kOneThreads};
     if (p.entries <= kOneThreads) hipLaunchKernelGGL((sort_one_kernel<LOOKUP, 1>), grid, block, 0, stream, p);
     else if (p.entries <= 2 * kOneThreads) hipLaunchKernelGGL((sort_one_kernel<LOOKUP, 2>), grid, block, 0, stream, p);
-    else if (p.entries <= 4 * kOneThreads) hipLaunchKernelGGL((sort_one_kernel<LOOKUP, 4>), grid, block, 0, stream, p);
-    else hipLaunchKernelGGL((sort_one_kernel<LOOKUP, kOneItems>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((sort_one_kernel<LOOKUP, 4>), grid, block, 0, stream, p);
 }
 
-template <bool LOOKUP, int ITEMS> void run_sort_many(const BankGradParams& p, hipStream_t stream) {
+// Up to this many tiles every workgroup that places entries adds their counts up by itself.
+constexpr uint32_t kSumTiles = 64;
+
+template <bool FIRST, bool LOOKUP, int ITEMS, bool SUMS> void run_pass(const BankGradParams& p, int pass, hipStream_t stream) {
     const dim3 tiles{p.tiles}, block{kThreads};
-    const dim3 scans{unsigned(((1 << p.bits) + kScanDigits - 1) / kScanDigits)};
-    for (int pass = 0; pass < p.passes; ++pass) {
-        if (pass == 0) hipLaunchKernelGGL((sort_count_kernel<true, LOOKUP, ITEMS>), tiles, block, 0, stream, p, pass);
-        else hipLaunchKernelGGL((sort_count_kernel<false, LOOKUP, ITEMS>), tiles, block, 0, stream, p, pass);
-        hipLaunchKernelGGL(sort_scan_kernel, scans, dim3(kScanDigits * kScanParts), 0, stream, p, pass);
-        if (pass == 0) hipLaunchKernelGGL((sort_place_kernel<true, LOOKUP, ITEMS>), tiles, block, 0, stream, p, pass);
-        else hipLaunchKernelGGL((sort_place_kernel<false, LOOKUP, ITEMS>), tiles, block, 0, stream, p, pass);
-    }
+    hipLaunchKernelGGL((sort_count_kernel<FIRST, LOOKUP, ITEMS, SUMS>), tiles, block, 0, stream, p, pass);
+    if (!SUMS) hipLaunchKernelGGL(sort_scan_kernel, dim3(1u << p.bits), block, 0, stream, p, pass);
+    hipLaunchKernelGGL((sort_place_kernel<FIRST, LOOKUP, ITEMS, SUMS>), tiles, block, 0, stream, p, pass);
+}
+template <bool LOOKUP, int ITEMS, bool SUMS> void run_sort_many(const BankGradParams& p, hipStream_t stream) {
+    run_pass<true, LOOKUP, ITEMS, SUMS>(p, 0, stream);
+    for (int pass = 1; pass < p.passes; ++pass) run_pass<false, LOOKUP, ITEMS, SUMS>(p, pass, stream);
 }
 
 template <bool LOOKUP> void run_sort(const BankGradParams& p, hipStream_t stream) {
     if (p.items == 0) run_sort_one<LOOKUP>(p, stream);
-    else if (p.items == 4) run_sort_many<LOOKUP, 4>(p, stream);
-    else run_sort_many<LOOKUP, 16>(p, stream);
+    else if (p.items == 4) run_sort_many<LOOKUP, 4, true>(p, stream);
+    else run_sort_many<LOOKUP, 8, false>(p, stream);
 }
 
 Divisor divisor(uint32_t d) {
@@ -603,15 +918,15 @@ Divisor divisor(uint32_t d) {
 
 int64_t bank_grad_layout(BankGradParams* p, void* workspace) {
     const int64_t entries = p->entries, octets = (int64_t(p->hd) + 7) / 8;
-    int bits = 1;
+    int bits = 1;  // at least: a thread of the sort takes pairs of digits
     while (bits < 31 && (uint64_t(p->num_slots - 1) >> bits) != 0) ++bits;
     p->passes = (bits + kMaxBits - 1) / kMaxBits;
     p->bits = (bits + p->passes - 1) / p->passes;
-    p->items = entries <= kOneEntries ? 0 : entries <= 262144 ? 4 : 16;
+    p->items = entries <= kOneEntries ? 0 : entries <= int64_t(kSumTiles) * kThreads * 4 ? 4 : 8;
     p->tiles = p->items > 0 ? uint32_t((entries + kThreads * p->items - 1) / (kThreads * p->items)) : 0;
     // Entries of a lane group: enough groups for four wavefronts on each SIMD of 256 CUs.
     const int64_t threads = entries * (octets < kMinLanes ? kMinLanes : octets);
-    int block = 8;
+    int block = 16;
     while (block < kMaxBlock && threads / block > 4096 * 64) block *= 2;
     p->block = block;
     p->spill = block / 2 < kMaxSpill ? block / 2 : kMaxSpill;
@@ -626,16 +941,18 @@ int64_t bank_grad_layout(BankGradParams* p, void* workspace) {
     const int64_t digits = int64_t(1) << p->bits;
     p->n = reinterpret_cast<uint32_t*>(place(4));
     p->total = reinterpret_cast<uint32_t*>(place(4 * p->passes * digits));
-    p->hist = reinterpret_cast<uint32_t*>(place(4 * p->passes * p->tiles * digits));
+    p->stride = (p->tiles + kScanEach - 1) / kScanEach * kScanEach;
+    p->hist = reinterpret_cast<uint32_t*>(place(4 * p->passes * p->stride * digits));
     for (int i = 0; i < 2; ++i) p->records[i] = reinterpret_cast<Record*>(place(8 * entries));
+    for (int i = 0; i < 2; ++i) p->weights[i] = reinterpret_cast<float*>(place(4 * entries));
     p->first = reinterpret_cast<float*>(place(32 * octets * p->blocks));
     p->last = reinterpret_cast<float*>(place(32 * octets * p->blocks));
     return used;
 }
 
-int64_t bank_grad_groups(const BankGradParams& p, int bank_size) {
-    const int64_t rows = zero_rows(int64_t(p.hd) * bank_size);
-    return p.add ? 0 : (p.num_slots + rows - 1) / rows;  // those over entries are at most 2^31 / 64
+int64_t bank_grad_groups(const BankGradParams& p, int dout_size, int bank_size) {
+    const SumGrid g = sum_grid(p, dout_size, bank_size);
+    return 8 * (int64_t(g.sums) + g.rows);
 }
 
 hipError_t launch_bank_grad(const BankGradParams& call, bool dout_bf16, bool bank_bf16, hipStream_t stream) {
@@ -644,23 +961,19 @@ hipError_t launch_bank_grad(const BankGradParams& call, bool dout_bf16, bool ban
     p.by_width[0] = divisor(p.width[0]);
     p.by_width[1] = divisor(p.width[1]);
     p.by_chunk = divisor(p.chunk);
-    const int64_t row_bytes = int64_t(p.hd) * (bank_bf16 ? 2 : 4);
-    const bool bank_vec = (reinterpret_cast<uintptr_t>(p.dbank) | uintptr_t(row_bytes)) % 16 == 0;
-    const uintptr_t at = reinterpret_cast<uintptr_t>(p.dout[0]) | (p.width[1] != 0 ? reinterpret_cast<uintptr_t>(p.dout[1]) : 0) |
-                         uintptr_t(p.hd) * (dout_bf16 ? 2 : 4);
-    if (p.entries > 0 && p.w[0] == nullptr) run_sort<true>(p, stream);
-    else if (p.entries > 0) run_sort<false>(p, stream);
-    if (!p.add) {
-        if (bank_vec) run_zero<16>(p, row_bytes, stream);
-        else if (bank_bf16) run_zero<2>(p, row_bytes, stream);
-        else run_zero<4>(p, row_bytes, stream);
+    if (p.entries == 0) {
+        const int64_t bytes = int64_t(p.num_slots) * p.hd * (bank_bf16 ? 2 : 4);
+        if (!p.add)
+            hipLaunchKernelGGL(zero_kernel, dim3(unsigned((bytes + kZeroBytes - 1) / kZeroBytes)), dim3(kThreads), 0, stream,
+                               static_cast<char*>(p.dbank), bytes);
+        return hipGetLastError();
     }
-    if (p.entries > 0) {
-        if (dout_bf16 && at % 16 == 0) run_bank<uint16_t, 16>(p, bank_bf16, bank_vec, stream);
-        else if (dout_bf16) run_bank<uint16_t, 2>(p, bank_bf16, bank_vec, stream);
-        else if (at % 16 == 0) run_bank<float, 16>(p, bank_bf16, bank_vec, stream);
-        else run_bank<float, 4>(p, bank_bf16, bank_vec, stream);
-    }
+    if (p.w[0] == nullptr) run_sort<true>(p, stream);
+    else run_sort<false>(p, stream);
+    if (dout_bf16 && bank_bf16) run_types<uint16_t, uint16_t>(p, stream);
+    else if (dout_bf16) run_types<uint16_t, float>(p, stream);
+    else if (bank_bf16) run_types<float, uint16_t>(p, stream);
+    else run_types<float, float>(p, stream);
     return hipGetLastError();
 }
 

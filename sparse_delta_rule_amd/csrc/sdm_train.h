@@ -77,9 +77,11 @@ struct Divisor {
     uint32_t mul, shift;
 };
 
+// An entry as it is sorted: its slot, and its token with its operand in the top bit.
 struct Record {
-    uint32_t slot, entry;
+    uint32_t slot, token;
 };
+constexpr uint32_t kSecond = 0x80000000u;  // operand 1
 
 struct BankGradParams {
     const void* idx[2];
@@ -106,16 +108,19 @@ struct BankGradParams {
     uint32_t blocks;
     // workspace
     uint32_t* n;          // [1] entries that count
-    uint32_t* hist;       // [passes, tiles, 2^bits]
+    int64_t stride;       // of the counts of a digit
+    uint32_t* hist;       // [passes, tiles, 2^bits], or [passes, 2^bits, stride] where they are scanned
     uint32_t* total;      // [passes, 2^bits]
     Record* records[2];   // [entries]
+    float* weights[2];    // [entries] (a gather)
     float* first;         // [blocks, columns rounded up to 8] sums of a run that began in an earlier block
     float* last;          // [blocks, columns rounded up to 8] of one that goes on in the next
 };
 // From entries, num_slots and hd: the other sizes and, where `workspace` is given, the places of
 // its arrays; returns the workspace's bytes.
 int64_t bank_grad_layout(BankGradParams* p, void* workspace);
-int64_t bank_grad_groups(const BankGradParams& p, int bank_size);  // most workgroups of a launch along its first axis
+// Workgroups of the largest launch; the sizes are set.
+int64_t bank_grad_groups(const BankGradParams& p, int dout_size, int bank_size);
 hipError_t launch_bank_grad(const BankGradParams& p, bool dout_bf16, bool bank_bf16, hipStream_t stream);
 
 }  // namespace sdm

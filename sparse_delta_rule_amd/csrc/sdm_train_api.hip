@@ -305,7 +305,8 @@ int sdm_lookup_grad(int64_t n, const void* idx, int idx_dtype, const void* dout,
     p.dropout.rng = rng;
     p.dbank = dbank;
     p.add = mode == SDM_GRAD_ADD;
-    if (bank_grad_groups(p, bs) > kMaxGroups) return fail(SDM_E_SHAPE, "%s: the bank exceeds the grid", fn);
+    if (bank_grad_groups(p, ds, bs) > kMaxGroups)
+        return fail(SDM_E_SHAPE, "%s: the bank or the entries exceed the grid", fn);
     return launched(fn, launch_bank_grad(p, dout_dtype == SDM_BF16, bank_dtype == SDM_BF16,
                                          static_cast<hipStream_t>(hip_stream)));
 }
@@ -380,7 +381,8 @@ int sdm_gather_bank_grad(int64_t tokens, int64_t chunk, int64_t valid, const int
     p.factor = 1.0f;
     p.dbank = dbank;
     p.add = mode == SDM_GRAD_ADD;
-    if (bank_grad_groups(p, bs) > kMaxGroups) return fail(SDM_E_SHAPE, "%s: the bank exceeds the grid", fn);
+    if (bank_grad_groups(p, 4, bs) > kMaxGroups)
+        return fail(SDM_E_SHAPE, "%s: the bank or the entries exceed the grid", fn);
     return launched(fn, launch_bank_grad(p, false, bank_dtype == SDM_BF16, static_cast<hipStream_t>(hip_stream)));
 }
 

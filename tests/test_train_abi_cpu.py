@@ -209,7 +209,7 @@ GRAD = dict(n=300, idx=A, idx_dtype=I32, dout=A + 64 * MB, dout_dtype=BF16, scal
     (dict(workspace=A + 200 * MB), E_OVERLAP, "dbank and workspace"),
     (dict(workspace=A), E_OVERLAP, "workspace and idx"),
     (dict(rng=A + 200 * MB + 8), E_OVERLAP, "dbank and rng"),
-    (dict(num_slots=(1 << 31) - 1, head_dim=16384, dbank=A + (1 << 50)), E_SHAPE, "exceeds the grid"),
+    (dict(num_slots=(1 << 31) - 1, head_dim=16384, dbank=A + (1 << 50)), E_SHAPE, "exceed the grid"),
 ])
 def test_lookup_grad_rejects(kw, code, msg):
     rejects("sdm_lookup_grad", GRAD, kw, code, msg)
