@@ -94,9 +94,10 @@ int64_t sdm_route_balance_workspace(int64_t tokens, int64_t keys, int64_t chunk,
  *     sigmoid:  d_ti = p_ti (1 - s_ti) (f_i - sum_j f_j p_tj)
  * for a live token t of sequence g; 0 for the others, and for keys whose score is 0.
  *     dlogits = d,  or dlogits + d (accumulate)
- * Differences of counts are exact, and taken from the count of the row's largest key,
- * so that nothing cancels where one key is far above the rest. The rest is float32; the
- * sum is rounded once to the logits' type.
+ * Counts are taken relative to their mean, or in a row where one key has more than 4/5 of
+ * the share to that key's count (p sums to 1, so that a constant changes nothing): there
+ * nothing cancels, however far that key is above the rest. Differences below 2^24 are
+ * exact, the rest is float32; the sum is rounded once to the logits' type.
  *
  * Arguments: as sdm_route_balance, with
  *   counts, coef  [sequences, keys] and [sequences].

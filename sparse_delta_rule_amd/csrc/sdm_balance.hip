@@ -22,9 +22,19 @@ __device__ __forceinline__ uint32_t live_limit(const BalanceParams& p, uint32_t 
     return uint32_t(max(v, 0));
 }
 __device__ __forceinline__ bool is_live(const BalanceParams& p, uint32_t t) {
-    const uint32_t c = t / p.chunk;
+    const uint32_t c = divide(t, p.by_chunk);
     return t - c * p.chunk < live_limit(p, c);
 }
+
+struct Larger {
+    __device__ __forceinline__ float operator()(float a, float b) const { return max32(a, b); }
+};
+struct Plus {
+    __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+    __device__ __forceinline__ int32_t operator()(int32_t a, int32_t b) const { return int32_t(uint32_t(a) + uint32_t(b)); }
+};
+constexpr Larger larger{};
+constexpr Plus plus{};
 
 // The tokens of a workgroup's piece.
 struct Piece {
@@ -53,31 +63,76 @@ template <typename E, int THREADS, int VPT, bool VEC> struct RawRow {
     }
     // Clean logits; -inf past the row's end.
     __device__ __forceinline__ void values(int keys, int tid, float (&c)[VPT]) const {
+        constexpr uint32_t kMinusInf = sizeof(E) == 2 ? 0xff80ff80u : 0xff800000u;
 #pragma unroll
         for (int i = 0; i < VPT / kN; ++i) {
             E e[kN];
-            __builtin_memcpy(e, &raw[i], sizeof e);
-            const bool in = Row::key_of(i * kN, tid) < keys;
+            if constexpr (VEC) {
+                const uint32_t in = uint32_t((Row::key_of(i * kN, tid) - keys) >> 31);  // all ones where the row has the vector
+                uint4 v = raw[i];
+                v.x = (v.x & in) | (kMinusInf & ~in), v.y = (v.y & in) | (kMinusInf & ~in);
+                v.z = (v.z & in) | (kMinusInf & ~in), v.w = (v.w & in) | (kMinusInf & ~in);
+                opaque(v);  // four words chosen, not each key
+                __builtin_memcpy(e, &v, 16);
+            } else {
+                e[0] = raw[i];
+            }
 #pragma unroll
-            for (int j = 0; j < kN; ++j) c[i * kN + j] = in ? clean(widen(e[j])) : -INFINITY;
+            for (int j = 0; j < kN; ++j) c[i * kN + j] = clean(VEC || Row::key_of(i, tid) < keys ? widen(e[j]) : -INFINITY);
         }
     }
 };
 
-// The terms of one lane's keys, c[i] -> e_i, given the largest of the part's logits; returns the offset.
-template <int N> __device__ __forceinline__ float terms(int score, float largest, float (&c)[N]) {
+// f over the LANES (16, 32 or 64) neighbouring lanes of a row, without LDS: gfx950 swaps rows of 16
+// and halves of 32 lanes between two registers.
+template <int LANES, typename T, typename F> __device__ __forceinline__ T reduce(T v, F f) {
+    v = lanes_reduce<16>(v, f);
+    auto both = [&](auto pair) {
+        const uint32_t a = pair[0], b = pair[1];
+        T x, y;
+        __builtin_memcpy(&x, &a, 4);
+        __builtin_memcpy(&y, &b, 4);
+        v = f(x, y);
+    };
+    auto bits = [&] {
+        uint32_t u;
+        __builtin_memcpy(&u, &v, 4);
+        return u;
+    };
+    if constexpr (LANES >= 32) both(__builtin_amdgcn_permlane16_swap(bits(), bits(), false, false));
+    if constexpr (LANES >= 64) both(__builtin_amdgcn_permlane32_swap(bits(), bits(), false, false));
+    return v;
+}
+
+// The terms of one lane's keys, c[i] -> e_i, given the largest of the part's logits; returns the
+// offset. scale: what every e_i is to be multiplied by to be relative to that offset: an exponential
+// by one fused operation, 2^(x L - q) with q = o L rounded, has what q's rounding puts into all of
+// them, 2^(o L - q), taken out there. rest (may be NULL): 1 - s_i of a sigmoid, for positive x the
+// exponential's own share, so that it is as precise as s_i is for negative x.
+template <int N>
+__device__ __forceinline__ float terms(int score, float largest, float (&c)[N], float* rest, float& scale) {
+    constexpr float kL = 1.44269504f;
+    scale = 1.0f;
     if (score == SDM_SOFTMAX) {
         const float o = max32(largest, -FLT_MAX);
+        if (__ballot(!(fabsf(o) < 65536.0f)) == 0) {
+            const float q = o * kL;
 #pragma unroll
-        for (int i = 0; i < N; ++i) c[i] = exp32(c[i] - o);
+            for (int i = 0; i < N; ++i) c[i] = __builtin_amdgcn_exp2f(fmaf(c[i], kL, -q));
+            scale = __builtin_amdgcn_exp2f(-fmaf(o, kL, -q));
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) c[i] = exp32(c[i] - o);
+        }
         return o;
     }
     const bool deep = largest <= kDeep;
     const float o = deep ? max32(largest, -FLT_MAX) : 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const float e = exp32(deep ? c[i] - o : -c[i]);
-        c[i] = deep ? e : __builtin_amdgcn_rcpf(1.0f + e);
+        const float e = exp32(deep ? c[i] - o : -c[i]), s = __builtin_amdgcn_rcpf(1.0f + e);
+        if (rest != nullptr) rest[i] = deep ? 1.0f : c[i] > 0 ? e * s : 1.0f - s;
+        c[i] = deep ? e : s;
     }
     return o;
 }
@@ -93,10 +148,10 @@ template <int N> __device__ __forceinline__ float sum_of(const float (&x)[N]) {
 __device__ __forceinline__ void count_choices(const BalanceParams& p, const Piece& r, int base, int most, uint32_t* words) {
     const uint32_t entries = (r.end - r.first) * uint32_t(p.k);
     for (uint32_t e = threadIdx.x; e < entries; e += blockDim.x) {
-        const uint32_t t = r.first + e / uint32_t(p.k);
+        const uint32_t t = r.first + divide(e, p.by_k);
         const int64_t o = int64_t(r.first) * p.k + e;
         const int64_t slot = p.idx64 ? static_cast<const int64_t*>(p.idx)[o] : int64_t(static_cast<const int32_t*>(p.idx)[o]);
-        const int64_t key = slot - int64_t(t % p.streams) * p.stream_slots;
+        const int64_t key = p.stream_slots == 0 ? slot : slot - int64_t(t % p.streams) * p.stream_slots;
         if (key < base || key >= int64_t(base) + most || !is_live(p, t)) continue;
         atomicAdd(words + (uint32_t(key) - uint32_t(base)) / 2, key & 1 ? 0x10000u : 1u);
     }
@@ -141,9 +196,10 @@ __global__ __launch_bounds__(kSmallThreads) void balance_small_kernel(BalancePar
         next[0].values(p.keys, lane, c);
         next[0] = next[1];
         load(t + 2 * kRows, next[1]);
-        const float largest = lanes_reduce<LANES>(max_of(c, -INFINITY), [](float a, float b) { return max32(a, b); });
-        terms(p.score, largest, c);
-        const float sum = lanes_reduce<LANES>(sum_of(c), [](float a, float b) { return a + b; });
+        const float largest = reduce<LANES>(max_of(c, -INFINITY), larger);
+        float scale;  // of all of the row's terms
+        terms(p.score, largest, c, nullptr, scale);
+        const float sum = reduce<LANES>(sum_of(c), plus);
         const float f = sum > 0 && t < r.end && is_live(p, t) ? 1.0f / sum : 0.0f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) acc[i] = fmaf(c[i], f, acc[i]);
@@ -160,15 +216,14 @@ __global__ __launch_bounds__(kSmallThreads) void balance_small_kernel(BalancePar
     for (int i = tid; i < stride; i += kSmallThreads) p.part_count[int64_t(blockIdx.x) * stride + i] = words[i];
 }
 
-constexpr int kBigThreads = 1024;
 constexpr int kCountKeys = 16384;  // keys counted in LDS at a time
 
 // Longer rows: the workgroup takes one row after another, its sums in registers. A wavefront's
 // terms have an offset of their own, so a row needs one barrier.
-template <typename E, int VPT, bool VEC>
-__global__ __launch_bounds__(kBigThreads) void balance_big_kernel(BalanceParams p) {
-    using Row = RowKeys<E, kBigThreads, VPT, VEC>;
-    constexpr int kWaves = kBigThreads / 64;
+template <typename E, int THREADS, int VPT, bool VEC>
+__global__ __launch_bounds__(THREADS) void balance_big_kernel(BalanceParams p) {
+    using Row = RowKeys<E, THREADS, VPT, VEC>;
+    constexpr int kWaves = THREADS / 64;
     constexpr bool kAhead = VPT * sizeof(E) <= 64;  // the next row is loaded while one is taken
     __shared__ float offset[2][kWaves], total[2][kWaves];
     __shared__ uint32_t words[kCountKeys / 2];
@@ -176,19 +231,19 @@ __global__ __launch_bounds__(kBigThreads) void balance_big_kernel(BalanceParams 
     const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
     const Piece r = this_piece(p, blockIdx.x);
     const E* logits = static_cast<const E*>(p.logits);
-    RawRow<E, kBigThreads, VPT, VEC> next;
+    RawRow<E, THREADS, VPT, VEC> next;
     if (kAhead) next.load(logits + int64_t(r.first) * p.keys, p.keys, tid);
     if (blockIdx.x == 0 && tid == 0) *p.done = 0;
     const int live = __syncthreads_count(r.first + tid < r.end && is_live(p, r.first + tid));
     if (tid == 0) p.live[blockIdx.x] = uint32_t(live);
     const int stride = (p.keys + 1) / 2;
     for (int base = 0; base < p.keys; base += kCountKeys) {
-        for (int i = tid; i < kCountKeys / 2; i += kBigThreads) words[i] = 0;
+        for (int i = tid; i < kCountKeys / 2; i += THREADS) words[i] = 0;
         __syncthreads();
         count_choices(p, r, base, kCountKeys, words);
         __syncthreads();
         uint32_t* to = p.part_count + int64_t(blockIdx.x) * stride + base / 2;
-        for (int i = tid; i < min(kCountKeys / 2, stride - base / 2); i += kBigThreads) to[i] = words[i];
+        for (int i = tid; i < min(kCountKeys / 2, stride - base / 2); i += THREADS) to[i] = words[i];
         __syncthreads();
     }
     float acc[VPT];
@@ -206,18 +261,20 @@ __global__ __launch_bounds__(kBigThreads) void balance_big_kernel(BalanceParams 
             next.load(logits + int64_t(t) * p.keys, p.keys, tid);
             next.values(p.keys, tid, c);
         }
-        const float largest = lanes_reduce<64>(max_of(c, -INFINITY), [](float a, float b) { return max32(a, b); });
-        const float o = terms(p.score, largest, c);
-        const float sum = lanes_reduce<64>(sum_of(c), [](float a, float b) { return a + b; });
+        const float largest = reduce<64>(max_of(c, -INFINITY), larger);
+        float scale;
+        const float o = terms(p.score, largest, c, nullptr, scale);
+        const float sum = reduce<64>(sum_of(c), plus) * scale;
         if (lane == 0) {
             offset[buffer][wave] = o;
             total[buffer][wave] = sum;
         }
         __syncthreads();
-        float most = -FLT_MAX, z = 0;
-        for (int w = 0; w < kWaves; ++w) most = max32(most, offset[buffer][w]);
-        for (int w = 0; w < kWaves; ++w) z = fmaf(total[buffer][w], exp32(offset[buffer][w] - most), z);
-        const float f = z > 0 ? exp32(o - most) / z : 0.0f;
+        // A lane for each wavefront's part, in every 16 lanes.
+        const int w = lane % 16 % kWaves;
+        const float part = offset[buffer][w], most = lanes_reduce<16>(part, larger);
+        const float z = lanes_reduce<16>(lane % 16 < kWaves ? total[buffer][w] * exp32(part - most) : 0.0f, plus);
+        const float f = z > 0 ? scale * exp32(o - most) / z : 0.0f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) acc[i] = fmaf(c[i], f, acc[i]);
         buffer ^= 1;
@@ -252,11 +309,11 @@ template <typename T> __device__ __forceinline__ T join_sum(T v, T* lds) {
 // last puts the items' parts of the loss together.
 __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceParams p) {
     constexpr int kRows = kJoinThreads / 16, kWaves = kJoinThreads / 64;
-    __shared__ double sums[kRows][kJoinKeys];
-    __shared__ int32_t counts[kRows][kJoinKeys];
+    __shared__ double sums[kWaves][kJoinKeys];
+    __shared__ int32_t counts[kWaves][kJoinKeys];
     __shared__ double scratch[kWaves];
     __shared__ uint32_t ticket;
-    const int tid = threadIdx.x, row = tid / 16, k0 = tid % 16 * 4;
+    const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, row = tid / 16, k0 = tid % 16 * 4;
     const uint32_t blocks = uint32_t(p.keys + kJoinKeys - 1) / kJoinKeys;
     const uint64_t items = uint64_t(p.sequences) * blocks;
     const int stride = (p.keys + 1) / 2;
@@ -270,7 +327,7 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceParam
         double sum[4] = {};
         int32_t count[4] = {};
         if (key < p.keys) {
-#pragma unroll 8
+#pragma unroll 4
             for (uint32_t i = row; i < p.pieces; i += kRows) {
                 const float* part = p.part + (first + i) * p.keys + key;
                 const uint32_t* words = p.part_count + (first + i) * stride + key / 2;
@@ -293,37 +350,44 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceParam
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            sums[row][k0 + j] = sum[j];
-            counts[row][k0 + j] = count[j];
+            sum[j] += __shfl_xor(sum[j], 16);
+            sum[j] += __shfl_xor(sum[j], 32);
+            count[j] += __shfl_xor(count[j], 16);
+            count[j] += __shfl_xor(count[j], 32);
+        }
+        if (lane < 16) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                sums[wave][k0 + j] = sum[j];
+                counts[wave][k0 + j] = count[j];
+            }
         }
         const uint32_t live = uint32_t(join_sum(n, scratch));  // and a barrier
-        if (tid < kJoinKeys) {
-            const int key = int(b) * kJoinKeys + tid, rows = int(min(p.pieces, uint32_t(kRows)));
+        if (wave == 0) {
+            const int mine = int(b) * kJoinKeys + lane;
             double s = 0;
             int32_t c = 0;
-            for (int r = 0; r < rows; ++r) {
-                s += sums[r][tid];
-                c += counts[r][tid];
+            for (int w = 0; w < kWaves; ++w) {
+                s += sums[w][lane];
+                c += counts[w][lane];
             }
-            if (key < p.keys) {
-                p.counts[int64_t(g) * p.keys + key] = c;
-                p.mean[int64_t(g) * p.keys + key] = live > 0 ? float(s / live) : 0.0f;
+            if (mine < p.keys) {
+                p.counts[int64_t(g) * p.keys + mine] = c;
+                p.mean[int64_t(g) * p.keys + mine] = live > 0 ? float(s / live) : 0.0f;
             }
             const double part = wave_sum(double(c) * s);
-            if (tid == 0) {
+            if (lane == 0) {
                 p.loss_part[item] = part;
                 if (b == 0) p.live_all[g] = live;
             }
         }
         __syncthreads();
     }
-    if (tid == 0) {
-        __threadfence();
-        ticket = __hip_atomic_fetch_add(p.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-    }
+    // Thread 0's own stores are what the last workgroup reads: its release, and the other thread 0's
+    // acquire and the barrier behind it, are all that this needs.
+    if (tid == 0) ticket = __hip_atomic_fetch_add(p.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
     __syncthreads();
     if (ticket != gridDim.x - 1) return;
-    __threadfence();
     double with = 0;
     for (uint32_t g = tid; g < p.sequences; g += kJoinThreads) with += p.live_all[g] > 0;
     const double sequences = join_sum(with, scratch);
@@ -350,23 +414,13 @@ __global__ __launch_bounds__(256) void balance_nothing_kernel(BalanceParams p) {
 }
 
 // ------------------------------------------------------------------ backward
+//
+// With p_i = e_i / z a row's gradient is p_i (f_i - sum_j f_j p_j), and as the p_i sum to 1 it stays
+// the same when a constant is taken from all f_i. The counts are taken relative to their mean, which
+// keeps them small where a route is balanced; in a row where one key has nearly all of the share,
+// relative to that key's count, so that its own gradient, a sum over the others, loses nothing.
 
-// The difference of two counts as float32 (a difference past 2^31 cannot be: a sequence has
-// fewer choices).
-__device__ __forceinline__ float apart(int32_t a, int32_t b) { return float(int32_t(uint32_t(a) - uint32_t(b))); }
-
-// A lane's VPT gradients: p_i ((c_i - top) - d), and for a sigmoid times 1 - s_i, times f.
-template <int N>
-__device__ __forceinline__ void gradients(int score, const float (&x)[N], const float (&e)[N], const int32_t (&count)[N],
-                                          int32_t top, float share, float d, float f, float (&out)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const float s = e[i] * share;
-        float v = s * (apart(count[i], top) - d) * f;
-        if (score == SDM_SIGMOID) v *= __builtin_amdgcn_rcpf(1.0f + exp32(x[i]));
-        out[i] = s > 0 ? v : 0.0f;  // also where f is not finite
-    }
-}
+constexpr float kMostShare = 0.8f;
 
 template <typename E, typename Row, int VPT, bool VEC>
 __device__ __forceinline__ void store_row(E* out, int keys, int tid, const float (&g)[VPT], bool add) {
@@ -397,11 +451,74 @@ __device__ __forceinline__ float row_factor(const BalanceParams& p, uint32_t seq
     return p.coef[sequence] * (p.dloss != nullptr ? *p.dloss : 1.0f);
 }
 
+// A lane's counts; returns their sum.
 template <typename Row, int VPT>
-__device__ __forceinline__ void load_counts(const BalanceParams& p, uint32_t sequence, int tid, int32_t (&count)[VPT]) {
+__device__ __forceinline__ int32_t load_counts(const BalanceParams& p, uint32_t sequence, int tid, int32_t (&count)[VPT]) {
     const int32_t* counts = p.counts + int64_t(sequence) * p.keys;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) count[i] = counts[min(Row::key_of(i, tid), p.keys - 1)];
+    uint32_t sum = 0;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) sum += Row::key_of(i, tid) < p.keys ? uint32_t(count[i]) : 0;
+    return int32_t(sum);
+}
+// The differences to `from`, exact below 2^24.
+template <int N> __device__ __forceinline__ void apart(const int32_t (&count)[N], int32_t from, float (&c)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) c[i] = float(int32_t(uint32_t(count[i]) - uint32_t(from)));
+}
+
+// sum_i e_i (c_i - top) of one lane.
+template <int N> __device__ __forceinline__ float dot_of(const float (&e)[N], const float (&c)[N], float top) {
+    float d = 0;
+    if (top == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) d = fmaf(e[i], c[i], d);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) d = fmaf(e[i], c[i] - top, d);
+    }
+    return d;
+}
+
+// A lane's gradients, e[i] -> e_i share ((c_i - top) - d) f, and for a sigmoid times 1 - s_i.
+template <int N>
+__device__ __forceinline__ void gradients(int score, const float (&rest)[N], const float (&c)[N], float top, float share, float d,
+                                          float f, float (&e)[N]) {
+    const float k = share * f;
+    if (__ballot(!(fabsf(k) < INFINITY && fabsf(d) < INFINITY)) != 0) {  // a key of score 0 has the gradient 0 all the same
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float s = e[i] * share, v = s * ((c[i] - top) - d) * f * (score == SDM_SIGMOID ? rest[i] : 1.0f);
+            e[i] = s > 0 ? v : 0.0f;
+        }
+        return;
+    }
+    if (top == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) e[i] *= k * (c[i] - d);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) e[i] *= k * ((c[i] - top) - d);
+    }
+    if (score == SDM_SIGMOID) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) e[i] *= rest[i];
+    }
+}
+
+// The largest term that a part with this largest logit and offset has (relative to that offset).
+__device__ __forceinline__ float largest_term(int score, float largest, float o) {
+    if (score == SDM_SIGMOID && largest > kDeep) return __builtin_amdgcn_rcpf(1.0f + exp32(-largest));
+    return exp32(largest - o);  // 1, or 0 where no key has a score
+}
+// The count of one lane's keys that have the row's largest term.
+template <typename Row, int VPT>
+__device__ __forceinline__ float count_of_largest(const float (&e)[VPT], const float (&c)[VPT], float largest, int keys, int tid) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) top = e[i] == largest && Row::key_of(i, tid) < keys ? max32(top, c[i]) : top;
+    return top;
 }
 
 template <typename E, int LANES, int VPT, bool VEC>
@@ -419,117 +536,115 @@ __global__ __launch_bounds__(kSmallThreads) void balance_backward_small_kernel(B
     };
     load(r.first + row, next[0]);
     load(r.first + row + kRows, next[1]);
-    int32_t count[VPT];
-    load_counts<Row>(p, r.sequence, lane, count);
+    float c[VPT];
+    {
+        int32_t count[VPT];
+        const int32_t sum = reduce<LANES>(load_counts<Row>(p, r.sequence, lane, count), plus);
+        apart(count, sum / p.keys, c);
+    }
     const float f = row_factor(p, r.sequence);
-    for (uint32_t t = r.first + row; t < r.end; t += kRows) {
-        const bool live = is_live(p, t);
-        float x[VPT], e[VPT], g[VPT];
-        next[0].values(p.keys, lane, x);
+    for (uint32_t t0 = r.first; t0 < r.end; t0 += kRows) {  // the same rounds in every wavefront
+        const uint32_t t = t0 + row;
+        const bool there = t < r.end, live = there && is_live(p, t);
+        float e[VPT], rest[VPT], scale;
+        next[0].values(p.keys, lane, e);
         next[0] = next[1];
         load(t + 2 * kRows, next[1]);
-        const float largest = lanes_reduce<LANES>(max_of(x, -INFINITY), [](float a, float b) { return max32(a, b); });
-        int32_t top = INT32_MIN;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            e[i] = x[i];
-            top = x[i] == largest && Row::key_of(i, lane) < p.keys ? max(top, count[i]) : top;
-        }
-        top = lanes_reduce<LANES>(top, [](int32_t a, int32_t b) { return max(a, b); });
-        terms(p.score, largest, e);
-        float z = 0, d = 0;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            z += e[i];
-            d = fmaf(e[i], apart(count[i], top), d);
-        }
-        z = lanes_reduce<LANES>(z, [](float a, float b) { return a + b; });
-        d = lanes_reduce<LANES>(d, [](float a, float b) { return a + b; });
+        const float largest = reduce<LANES>(max_of(e, -INFINITY), larger);
+        const float o = terms(p.score, largest, e, rest, scale);
+        const float z = reduce<LANES>(sum_of(e), plus);
         const float share = z > 0 && live ? 1.0f / z : 0.0f;
-        gradients(p.score, x, e, count, top, share, d * share, f, g);
-        if (live || !p.accumulate) store_row<E, Row, VPT, VEC>(dlogits + int64_t(t) * p.keys, p.keys, lane, g, p.accumulate);
+        float top = 0;
+        if (__ballot(share * largest_term(p.score, largest, o) > kMostShare) != 0) {
+            const float most = reduce<LANES>(max_of(e, 0.0f), larger);
+            top = reduce<LANES>(count_of_largest<Row>(e, c, most, p.keys, lane), larger);
+        }
+        const float d = reduce<LANES>(dot_of(e, c, top), plus);
+        gradients(p.score, rest, c, top, share, d * share, f, e);
+        if (there && (live || !p.accumulate))
+            store_row<E, Row, VPT, VEC>(dlogits + int64_t(t) * p.keys, p.keys, lane, e, p.accumulate);
     }
 }
 
-template <typename E, int VPT, bool VEC>
-__global__ __launch_bounds__(kBigThreads) void balance_backward_big_kernel(BalanceParams p) {
-    using Row = RowKeys<E, kBigThreads, VPT, VEC>;
-    constexpr int kWaves = kBigThreads / 64;
-    __shared__ float largest_of[2][kWaves], offset[2][kWaves], total[2][kWaves], dot[2][kWaves];
-    __shared__ int32_t top_of[2][kWaves];
+template <typename E, int THREADS, int VPT, bool VEC>
+__global__ __launch_bounds__(THREADS) void balance_backward_big_kernel(BalanceParams p) {
+    using Row = RowKeys<E, THREADS, VPT, VEC>;
+    constexpr int kWaves = THREADS / 64;
+    constexpr bool kAhead = VPT * sizeof(E) <= 64;  // the next row is loaded while one is taken
+    __shared__ float offset[2][kWaves], total[2][kWaves], dot[2][kWaves], term[2][kWaves];
+    __shared__ float again[2][kWaves];
+    __shared__ int32_t sums[kWaves];
     ieee_mode_off();
     const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
     const Piece r = this_piece(p, blockIdx.x);
     const E* logits = static_cast<const E*>(p.logits);
     E* dlogits = static_cast<E*>(p.dlogits);
-    constexpr bool kAhead = VPT * sizeof(E) <= 64;  // the next row is loaded while one is taken
-    RawRow<E, kBigThreads, VPT, VEC> next;
+    RawRow<E, THREADS, VPT, VEC> next;
     if (kAhead) next.load(logits + int64_t(r.first) * p.keys, p.keys, tid);
-    int32_t count[VPT];
-    load_counts<Row>(p, r.sequence, tid, count);
+    float c[VPT];
+    {
+        int32_t count[VPT];
+        const int32_t mine = reduce<64>(load_counts<Row>(p, r.sequence, tid, count), plus);
+        if (lane == 0) sums[wave] = mine;
+        __syncthreads();
+        uint32_t sum = 0;
+        for (int w = 0; w < kWaves; ++w) sum += uint32_t(sums[w]);
+        apart(count, int32_t(sum) / p.keys, c);
+    }
     const float f = row_factor(p, r.sequence);
     int buffer = 0;
     for (uint32_t t = r.first; t < r.end; ++t) {
         E* out = dlogits + int64_t(t) * p.keys;
-        float x[VPT], e[VPT], g[VPT];
+        float e[VPT], rest[VPT], scale;
         if (kAhead) {
-            next.values(p.keys, tid, x);
+            next.values(p.keys, tid, e);
             next.load(logits + int64_t(min(t + 1, r.end - 1)) * p.keys, p.keys, tid);
         }
         if (!is_live(p, t)) {  // of the whole workgroup
             if (!p.accumulate) {
 #pragma unroll
-                for (int i = 0; i < VPT; ++i) g[i] = 0.0f;
-                store_row<E, Row, VPT, VEC>(out, p.keys, tid, g, false);
+                for (int i = 0; i < VPT; ++i) e[i] = 0.0f;
+                store_row<E, Row, VPT, VEC>(out, p.keys, tid, e, false);
             }
             continue;
         }
         if (!kAhead) {
             next.load(logits + int64_t(t) * p.keys, p.keys, tid);
-            next.values(p.keys, tid, x);
+            next.values(p.keys, tid, e);
         }
-        const float largest = lanes_reduce<64>(max_of(x, -INFINITY), [](float a, float b) { return max32(a, b); });
-        int32_t mine = INT32_MIN;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            e[i] = x[i];
-            mine = x[i] == largest && Row::key_of(i, tid) < p.keys ? max(mine, count[i]) : mine;
-        }
-        mine = lanes_reduce<64>(mine, [](int32_t a, int32_t b) { return max(a, b); });
-        const float o = terms(p.score, largest, e);
-        float z = 0, d = 0;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            z += e[i];
-            d = fmaf(e[i], apart(count[i], mine), d);
-        }
-        z = lanes_reduce<64>(z, [](float a, float b) { return a + b; });
-        d = lanes_reduce<64>(d, [](float a, float b) { return a + b; });
+        const float largest = reduce<64>(max_of(e, -INFINITY), larger);
+        const float o = terms(p.score, largest, e, rest, scale);
+        const float mine = reduce<64>(sum_of(e), plus) * scale, its_dot = reduce<64>(dot_of(e, c, 0.0f), plus) * scale;
         if (lane == 0) {
-            largest_of[buffer][wave] = largest;
             offset[buffer][wave] = o;
-            total[buffer][wave] = z;
-            dot[buffer][wave] = d;
-            top_of[buffer][wave] = mine;
+            total[buffer][wave] = mine;
+            dot[buffer][wave] = its_dot;
+            term[buffer][wave] = largest_term(p.score, largest, o);
         }
         __syncthreads();
-        float most = -FLT_MAX, highest = -INFINITY;
-        int32_t top = INT32_MIN;
-        for (int w = 0; w < kWaves; ++w) {
-            most = max32(most, offset[buffer][w]);
-            highest = max32(highest, largest_of[buffer][w]);
+        // A lane for each wavefront's part, in every 16 lanes.
+        const int w = lane % 16 % kWaves;
+        const float at = offset[buffer][w], most = lanes_reduce<16>(at, larger);
+        const float part = lane % 16 < kWaves ? exp32(at - most) : 0.0f;
+        const float z = lanes_reduce<16>(total[buffer][w] * part, plus);
+        float d = lanes_reduce<16>(dot[buffer][w] * part, plus), top = 0;
+        const float biggest = lanes_reduce<16>(term[buffer][w] * part, larger);
+        const float share = z > 0 ? 1.0f / z : 0.0f, own = scale * exp32(o - most);
+        if (biggest * share > kMostShare) {  // of the whole workgroup
+            // The key's count, then the sum relative to it.
+            const float here = reduce<64>(max_of(e, 0.0f), larger);
+            float its = reduce<64>(count_of_largest<Row>(e, c, here, p.keys, tid), larger);
+            if (!(term[buffer][wave] * exp32(o - most) == biggest)) its = -INFINITY;
+            if (lane == 0) again[0][wave] = its;
+            __syncthreads();
+            top = lanes_reduce<16>(again[0][w], larger);
+            its = reduce<64>(dot_of(e, c, top), plus) * own;
+            if (lane == 0) again[1][wave] = its;
+            __syncthreads();
+            d = lanes_reduce<16>(lane % 16 < kWaves ? again[1][w] : 0.0f, plus);
         }
-        for (int w = 0; w < kWaves; ++w) top = largest_of[buffer][w] == highest ? max(top, top_of[buffer][w]) : top;
-        z = 0;
-        d = 0;
-        for (int w = 0; w < kWaves; ++w) {
-            const float part = exp32(offset[buffer][w] - most), sum = total[buffer][w] * part;
-            z += sum;
-            d += fmaf(sum, apart(top_of[buffer][w], top), dot[buffer][w] * part);
-        }
-        const float share = z > 0 ? 1.0f / z : 0.0f;
-        gradients(p.score, x, e, count, top, share * exp32(o - most), d * share, f, g);
-        store_row<E, Row, VPT, VEC>(out, p.keys, tid, g, p.accumulate);
+        gradients(p.score, rest, c, top, share * own, d * share, f, e);
+        store_row<E, Row, VPT, VEC>(out, p.keys, tid, e, p.accumulate);
         buffer ^= 1;
     }
 }
@@ -545,12 +660,12 @@ template <typename E, int LANES, int VPT> void run_small(const BalanceParams& p,
     else if (vec) hipLaunchKernelGGL((balance_small_kernel<E, LANES, VPT, true>), grid, block, 0, s, p);
     else hipLaunchKernelGGL((balance_small_kernel<E, LANES, VPT, false>), grid, block, 0, s, p);
 }
-template <typename E, int VPT> void run_big(const BalanceParams& p, bool vec, bool backward, hipStream_t s) {
-    const dim3 grid{unsigned(p.sequences * p.pieces)}, block{kBigThreads};
-    if (vec && backward) hipLaunchKernelGGL((balance_backward_big_kernel<E, VPT, true>), grid, block, 0, s, p);
-    else if (backward) hipLaunchKernelGGL((balance_backward_big_kernel<E, VPT, false>), grid, block, 0, s, p);
-    else if (vec) hipLaunchKernelGGL((balance_big_kernel<E, VPT, true>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((balance_big_kernel<E, VPT, false>), grid, block, 0, s, p);
+template <typename E, int THREADS, int VPT> void run_big(const BalanceParams& p, bool vec, bool backward, hipStream_t s) {
+    const dim3 grid{unsigned(p.sequences * p.pieces)}, block{THREADS};
+    if (vec && backward) hipLaunchKernelGGL((balance_backward_big_kernel<E, THREADS, VPT, true>), grid, block, 0, s, p);
+    else if (backward) hipLaunchKernelGGL((balance_backward_big_kernel<E, THREADS, VPT, false>), grid, block, 0, s, p);
+    else if (vec) hipLaunchKernelGGL((balance_big_kernel<E, THREADS, VPT, true>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((balance_big_kernel<E, THREADS, VPT, false>), grid, block, 0, s, p);
 }
 template <typename E> void run_rows(const BalanceParams& p, bool backward, hipStream_t s) {
     const uintptr_t at = reinterpret_cast<uintptr_t>(p.logits) | (backward ? reinterpret_cast<uintptr_t>(p.dlogits) : 0);
@@ -559,10 +674,10 @@ template <typename E> void run_rows(const BalanceParams& p, bool backward, hipSt
     else if (p.keys <= 256) run_small<E, 32, 8>(p, vec, backward, s);
     else if (p.keys <= 512) run_small<E, 64, 8>(p, vec, backward, s);
     else if (p.keys <= 1024) run_small<E, 64, 16>(p, vec, backward, s);
-    else if (p.keys <= 8192) run_big<E, 8>(p, vec, backward, s);
-    else if (p.keys <= 16384) run_big<E, 16>(p, vec, backward, s);
-    else if (p.keys <= 32768) run_big<E, 32>(p, vec, backward, s);
-    else run_big<E, 64>(p, vec, backward, s);
+    else if (p.keys <= 8192) run_big<E, 1024, 8>(p, vec, backward, s);
+    else if (p.keys <= 16384) run_big<E, 1024, 16>(p, vec, backward, s);
+    else if (p.keys <= 32768) run_big<E, 1024, 32>(p, vec, backward, s);
+    else run_big<E, 1024, 64>(p, vec, backward, s);
 }
 
 }  // namespace
@@ -578,6 +693,7 @@ int64_t balance_layout(BalanceParams* p, void* workspace) {
     p->piece = int(piece);
     p->pieces = uint32_t((p->sequence + piece - 1) / piece);
     const int64_t pieces = int64_t(p->sequences) * p->pieces, blocks = (p->keys + kJoinKeys - 1) / kJoinKeys;
+    p->by_chunk = divisor(p->chunk);
     char* base = static_cast<char*>(workspace);
     int64_t used = 0;
     auto place = [&](int64_t bytes) {

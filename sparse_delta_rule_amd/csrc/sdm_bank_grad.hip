@@ -17,10 +17,6 @@ constexpr int kThreads = 256;
 
 // ------------------------------------------------------------------ entries
 
-__device__ __forceinline__ uint32_t divide(uint32_t n, const Divisor& d) {
-    return uint32_t(uint64_t(n) * d.mul >> d.shift);
-}
-
 constexpr uint32_t kNone = 0xffffffffu;
 struct Entry {
     Record r;  // slot kNone: does not count
@@ -904,14 +900,6 @@ template <bool LOOKUP> void run_sort(const BankGradParams& p, hipStream_t stream
     if (p.items == 0) run_sort_one<LOOKUP>(p, stream);
     else if (p.items == 4) run_sort_many<LOOKUP, 4, true>(p, stream);
     else run_sort_many<LOOKUP, 8, false>(p, stream);
-}
-
-Divisor divisor(uint32_t d) {
-    Divisor r{0, 31};
-    if (d == 0) return r;  // never divided by
-    while ((uint64_t(1) << (r.shift - 31)) < d) ++r.shift;
-    r.mul = uint32_t(((uint64_t(1) << r.shift) + d - 1) / d);
-    return r;
 }
 
 }  // namespace

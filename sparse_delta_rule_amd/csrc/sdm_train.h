@@ -7,6 +7,23 @@
 
 namespace sdm {
 
+// n / d of n < 2^31 by a product: mul = ceil(2^shift / d), shift = 31 + ceil(log2 d), is
+// less than 2^32 and near enough for every such n (Granlund and Montgomery, 1994).
+struct Divisor {
+    uint32_t mul, shift;
+};
+inline Divisor divisor(uint32_t d) {
+    Divisor r{0, 31};
+    if (d == 0) return r;  // never divided by
+    while ((uint64_t(1) << (r.shift - 31)) < d) ++r.shift;
+    r.mul = uint32_t(((uint64_t(1) << r.shift) + d - 1) / d);
+    return r;
+}
+__device__ __forceinline__ uint32_t divide(uint32_t n, const Divisor& d) {
+    return uint32_t(uint64_t(n) * d.mul >> d.shift);
+}
+
+
 // ------------------------------------------------------------------ balance
 // A piece is a run of tokens of one sequence, which one workgroup reads: at most 255, so
 // that a key's count in it fits 16 bits (255 * SDM_MAX_WIDTH < 2^16).
@@ -16,6 +33,7 @@ struct BalanceParams {
     const void* logits;
     const int32_t* chunk_valid;
     uint32_t tokens, chunk, valid;
+    Divisor by_chunk, by_k;
     int keys, k, score;
     int per_chunk, piece;
     uint32_t sequence;  // tokens of a sequence
@@ -71,12 +89,6 @@ int64_t lookup_groups(const LookupParams& p);  // workgroups of the launch along
 hipError_t launch_lookup(const LookupParams& p, int bank_dtype, bool out_bf16, hipStream_t stream);
 
 // ------------------------------------------------------------------ gradient to a bank
-// n / d of n < 2^31 by a product: mul = ceil(2^shift / d), shift = 31 + ceil(log2 d), is
-// less than 2^32 and near enough for every such n (Granlund and Montgomery, 1994).
-struct Divisor {
-    uint32_t mul, shift;
-};
-
 // An entry as it is sorted: its slot, and its token with its operand in the top bit.
 struct Record {
     uint32_t slot, token;

@@ -149,6 +149,7 @@ int sdm_route_balance(const void* logits, int logit_dtype, int64_t tokens, int64
         if (rc != SDM_OK) return rc;
     }
     p.k = k;
+    p.by_k = divisor(uint32_t(k));
     p.scale = scale;
     p.streams = uint32_t(streams < UINT32_MAX ? streams : UINT32_MAX);
     p.stream_slots = stream_slots;

@@ -75,24 +75,29 @@ def balance(logits, keys_of, *, score="softmax", chunk=None, valid=None, chunk_v
 
 def balance_backward(logits, counts, coef, *, dloss=1.0, score="softmax", chunk=None, valid=None, chunk_valid=None,
                      per_chunk=False):
-    """(dlogits, bound)."""
+    """(dlogits, bound). Counts are taken relative to their mean, or to that of a key with more than 4/5 of its row's
+    share: what float32 sums of their products with the shares may be off by is relative to those differences."""
     X = clean(logits)
     T, N = X.shape
     out, off = np.zeros_like(X), np.zeros_like(X)
     for g, run in enumerate(sequences(T, chunk or max(T, 1), valid, chunk_valid, per_chunk)):
         f = dloss * float(coef[g])
+        whole = counts[g].astype(np.float64)
         for t in run:
             x = X[t]
             p, rest, rel = shares(x, score)
             if not p.any():
                 continue
-            c = counts[g].astype(np.float64) - counts[g][x == x.max()].max()
-            d = c - (p * c).sum()
+            mean, top = np.trunc(whole.sum() / N), whole[x == x.max()].max()
+            d = (whole - top) - (p * (whole - top)).sum()
             out[t] = p * rest * d * f
             with np.errstate(invalid="ignore"):
                 more = rel + 12 * U + (np.minimum(np.where(x > -np.inf, np.abs(x), 0), 200) * 2 * U if score == "sigmoid" else 0)
-            sums = (p * np.abs(c) * (rel + 110 * U)).sum()
-            off[t] = np.abs(f) * p * rest * (np.abs(d) * more + sums + 4 * U * np.abs(c)) + np.abs(f) * np.abs(d) * 2.0 ** -120
+            for c, there in ((whole - mean, p.max() < 0.81), (whole - top, p.max() > 0.79)):
+                if there:
+                    sums = (p * np.abs(c) * (rel + 110 * U)).sum()
+                    size = np.abs(f) * p * rest * (np.abs(d) * more + sums + 4 * U * np.abs(c))
+                    off[t] = np.maximum(off[t], size + np.abs(f) * (np.abs(d) + np.abs(c).max()) * 2.0 ** -120)
     return out, off
 
 
