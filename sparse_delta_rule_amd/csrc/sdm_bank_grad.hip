@@ -44,6 +44,28 @@ template <bool LOOKUP> __device__ __forceinline__ Entry entry_of(const BankGradP
     return {{counts ? uint32_t(s) : kNone, token | (second ? kSecond : 0)}, w};
 }
 
+// ------------------------------------------------------------------ zeros
+
+// Part `part` of `parts` of the bank's bytes, kZeroBytes a workgroup: the sort's launches leave most
+// of the card idle.
+constexpr int64_t kZeroBytes = 65536;
+__device__ __host__ __forceinline__ int64_t zero_groups(int64_t bytes, int parts) {  // of a part
+    return ((bytes + kZeroBytes - 1) / kZeroBytes + parts - 1) / parts;
+}
+__device__ __forceinline__ void zero_part(const BankGradParams& p, int part, int parts, uint32_t group) {
+    const int64_t begin = (part * zero_groups(p.zero_bytes, parts) + group) * kZeroBytes, end = min(begin + kZeroBytes, p.zero_bytes);
+    char* to = static_cast<char*>(p.dbank);
+    const int threads = blockDim.x;
+    if (reinterpret_cast<uintptr_t>(to) % 16 == 0) {
+        for (int64_t i = begin + threadIdx.x * 16; i + 16 <= end; i += threads * 16)
+            store_stream(reinterpret_cast<uint4*>(to + i), uint4{});
+        for (int64_t i = end - end % 16 + threadIdx.x * 2; i < end; i += threads * 2) *reinterpret_cast<uint16_t*>(to + i) = 0;
+    } else {
+        for (int64_t i = begin + threadIdx.x * 2; i < end; i += threads * 2) *reinterpret_cast<uint16_t*>(to + i) = 0;
+    }
+}
+__global__ __launch_bounds__(kThreads) void zero_kernel(BankGradParams p) { zero_part(p, 0, 1, blockIdx.x); }
+
 // ------------------------------------------------------------------ sort
 
 constexpr int kMaxBits = 9;  // of a digit
@@ -70,7 +92,7 @@ __device__ __forceinline__ uint32_t lanes_below(uint64_t lanes) {
 // Each of a wavefront's ITEMS entries (64 neighbours at a time): how many of its earlier ones have
 // the same digit. count: the wavefront's own, of each digit, 0 before and its sum after.
 template <int ITEMS>
-__device__ __forceinline__ void rank_items(const Entry (&e)[ITEMS], int pass, int bits, uint32_t* count, uint32_t (&rank)[ITEMS]) {
+__device__ __forceinline__ void rank_items(const Entry (&e)[ITEMS], int pass, int bits, uint16_t* count, uint32_t (&rank)[ITEMS]) {
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
         const bool has = e[i].r.slot != kNone;
@@ -82,7 +104,7 @@ __device__ __forceinline__ void rank_items(const Entry (&e)[ITEMS], int pass, in
             const uint32_t before = count[digit];
             rank[i] = before + below;
             wave_lds_order();
-            if (below == 0) count[digit] = before + uint32_t(__popcll(same));
+            if (below == 0) count[digit] = uint16_t(before + uint32_t(__popcll(same)));
         }
         wave_lds_order();
     }
@@ -115,8 +137,9 @@ template <bool LOOKUP, int ITEMS> __global__ __launch_bounds__(kOneThreads) void
     constexpr uint32_t kMost = kOneThreads * ITEMS;
     __shared__ Record records[kMost];
     __shared__ float weights[LOOKUP ? 1 : kMost];
-    __shared__ uint32_t count[kOneWaves][kMaxDigits];
+    __shared__ uint16_t count[kOneWaves][kMaxDigits];  // of all entries, at most kMost
     __shared__ uint32_t scratch[kOneWaves];
+    if (blockIdx.x > 0) return zero_part(p, 0, 1, blockIdx.x - 1);
     const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, digits = 1 << p.bits;
     uint32_t rank[ITEMS], n = p.entries;
     Entry e[ITEMS];
@@ -137,7 +160,7 @@ template <bool LOOKUP, int ITEMS> __global__ __launch_bounds__(kOneThreads) void
         if (tid < digits) {
             for (int w = 0; w < kOneWaves; ++w) {
                 const uint32_t v = count[w][tid];
-                count[w][tid] = base;
+                count[w][tid] = uint16_t(base);
                 base += v;
             }
         }
@@ -168,22 +191,19 @@ template <bool LOOKUP, int ITEMS> __global__ __launch_bounds__(kOneThreads) void
 
 constexpr int kWaves = kThreads / 64;
 
-// A thread's entries of a tile, `stride` apart; slot kNone past the end. WEIGHTS: with their weights.
+// A thread's entries of a tile, `stride` apart: what is there, before it is known how many count.
 template <bool FIRST, bool LOOKUP, bool WEIGHTS, int ITEMS>
-__device__ __forceinline__ void load_entries(const BankGradParams& p, int pass, uint32_t first, uint32_t stride, uint32_t n,
-                                             Entry (&e)[ITEMS]) {
-    if (n == 0) {
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) e[i] = {{kNone, 0}, 0.0f};
-        return;
-    }
+__device__ __forceinline__ void load_entries(const BankGradParams& p, int pass, uint32_t first, uint32_t stride, Entry (&e)[ITEMS]) {
     const int from = (pass - 1) & 1;
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-        const uint32_t at = min(first + i * stride, n - 1);
+        const uint32_t at = min(first + i * stride, p.entries - 1);
         if (FIRST) e[i] = entry_of<LOOKUP>(p, at);
         else e[i] = {p.records[from][at], WEIGHTS ? p.weights[from][at] : 1.0f};
     }
+}
+// Slot kNone past the end.
+template <int ITEMS> __device__ __forceinline__ void cut_entries(uint32_t first, uint32_t stride, uint32_t n, Entry (&e)[ITEMS]) {
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) e[i].r.slot = first + i * stride < n ? e[i].r.slot : kNone;
 }
@@ -199,12 +219,14 @@ template <bool SUMS> __device__ __forceinline__ uint32_t* hist_of(const BankGrad
 template <bool FIRST, bool LOOKUP, int ITEMS, bool SUMS>
 __global__ __launch_bounds__(kThreads) void sort_count_kernel(BankGradParams p, int pass) {
     __shared__ uint32_t count[kMaxDigits];
+    if (blockIdx.x >= p.tiles) return zero_part(p, 2 * pass, 2 * p.passes, blockIdx.x - p.tiles);
     const int digits = 1 << p.bits;
+    const uint32_t n = FIRST ? p.entries : *p.n, first = blockIdx.x * uint32_t(kThreads * ITEMS) + threadIdx.x;
+    Entry e[ITEMS];
+    load_entries<FIRST, LOOKUP, false, ITEMS>(p, pass, first, kThreads, e);
     for (int d = threadIdx.x; d < digits; d += kThreads) count[d] = 0;
     __syncthreads();
-    const uint32_t n = FIRST ? p.entries : *p.n;
-    Entry e[ITEMS];
-    load_entries<FIRST, LOOKUP, false, ITEMS>(p, pass, blockIdx.x * uint32_t(kThreads * ITEMS) + threadIdx.x, kThreads, n, e);
+    cut_entries(first, kThreads, n, e);
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i)
         if (e[i].r.slot != kNone) atomicAdd(&count[digit_of(e[i].r.slot, pass, p.bits)], 1u);
@@ -245,15 +267,15 @@ __global__ __launch_bounds__(kThreads) void sort_place_kernel(BankGradParams p, 
     constexpr uint32_t kTile = kThreads * ITEMS;
     __shared__ Record records[kTile];
     __shared__ float weights[LOOKUP ? 1 : kTile];
-    __shared__ uint32_t count[kWaves][kMaxDigits];
+    __shared__ uint16_t count[kWaves][kMaxDigits];  // of the tile's entries
     __shared__ uint32_t go[kMaxDigits];  // where a digit's entries of this tile go, less where they are in `records`
     __shared__ uint32_t scratch[2][kWaves];
+    if (blockIdx.x >= p.tiles) return zero_part(p, 2 * pass + 1, 2 * p.passes, blockIdx.x - p.tiles);
     const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, digits = 1 << p.bits;
-    const uint32_t n = FIRST ? p.entries : *p.n;
-    if (!FIRST && blockIdx.x * kTile >= n) return;
+    const uint32_t n = FIRST ? p.entries : *p.n, first = blockIdx.x * kTile + wave * (64 * ITEMS) + lane;
     Entry e[ITEMS];
     uint32_t rank[ITEMS];
-    load_entries<FIRST, LOOKUP, !LOOKUP, ITEMS>(p, pass, blockIdx.x * kTile + wave * (64 * ITEMS) + lane, 64, n, e);
+    load_entries<FIRST, LOOKUP, !LOOKUP, ITEMS>(p, pass, first, 64, e);
     // A thread takes digits 2 tid and 2 tid + 1: those of all tiles, and of the lower ones.
     uint32_t total[2] = {}, before[2] = {};
     if (2 * tid < digits) {
@@ -276,6 +298,8 @@ __global__ __launch_bounds__(kThreads) void sort_place_kernel(BankGradParams p, 
 #pragma unroll
     for (int j = 0; j < 2; ++j)
         for (int w = 0; w < kWaves; ++w) count[w][2 * tid + j] = 0;
+    if (!FIRST && blockIdx.x * kTile >= n) return;  // of the whole workgroup
+    cut_entries(first, 64, n, e);
     uint32_t all, here;
     const uint32_t below = sum_below<kThreads>(total[0] + total[1], scratch[0], &all);
     if (FIRST && blockIdx.x == 0 && tid == 0) *p.n = all;
@@ -291,7 +315,7 @@ __global__ __launch_bounds__(kThreads) void sort_place_kernel(BankGradParams p, 
         go[2 * tid + j] = below + (j == 1 ? total[0] : 0) + before[j] - base;
         for (int w = 0; w < kWaves; ++w) {
             const uint32_t v = count[w][2 * tid + j];
-            count[w][2 * tid + j] = base;
+            count[w][2 * tid + j] = uint16_t(base);
             base += v;
         }
     }
@@ -570,19 +594,6 @@ __device__ __forceinline__ void sum_rows(const S& s, const SumGrid& g, uint32_t 
     }
 }
 
-// No entries: nothing but zeros, a workgroup for each kZeroBytes.
-constexpr int64_t kZeroBytes = 65536;
-__global__ __launch_bounds__(kThreads) void zero_kernel(char* to, int64_t bytes) {
-    const int64_t begin = int64_t(blockIdx.x) * kZeroBytes, end = min(begin + kZeroBytes, bytes);
-    if (reinterpret_cast<uintptr_t>(to) % 16 == 0) {
-        for (int64_t i = begin + threadIdx.x * 16; i + 16 <= end; i += kThreads * 16)
-            store_stream(reinterpret_cast<uint4*>(to + i), uint4{});
-        for (int64_t i = end - end % 16 + threadIdx.x * 2; i < end; i += kThreads * 2) *reinterpret_cast<uint16_t*>(to + i) = 0;
-    } else {
-        for (int64_t i = begin + threadIdx.x * 2; i < end; i += kThreads * 2) *reinterpret_cast<uint16_t*>(to + i) = 0;
-    }
-}
-
 // ------------------------------------------------------------------ sums of blocks
 
 constexpr int kMaxBlock = 32;
@@ -592,11 +603,15 @@ constexpr int kMaxSpill = 16;
 // different banks.
 __device__ __host__ __forceinline__ int lds_place(int i, int shift) { return i + (i >> shift); }
 
-// What the entries of a range of blocks add to their rows. ALL: every run (SDM_GRAD_ADD); else the
-// long ones alone.
-template <bool ALL, typename S>
+// How the sums are made: a row of the bank at a time, and the long runs by blocks; or all by blocks of
+// entries, stored to rows that are zero, or added to what is there.
+enum { kByRows, kStore, kAdd };
+
+// What the entries of a range of blocks add to their rows; by rows, the long runs' alone.
+template <int MODE, typename S>
 __device__ __forceinline__ void sum_blocks(const S& s, const SumGrid& g, uint32_t range_number, uint32_t* lds) {
     constexpr int N = S::N, V = S::V;
+    constexpr bool ALL = MODE != kByRows;
     const BankGradParams& p = s.p;
     const int groups = kThreads / g.lanes, group = int(threadIdx.x) / g.lanes;
     const int columns = (p.hd + 7) / 8 * 8;
@@ -660,7 +675,7 @@ __device__ __forceinline__ void sum_blocks(const S& s, const SumGrid& g, uint32_
                                     *reinterpret_cast<float4*>(to + s.c[v] + j) =
                                         make_float4(acc[v][j], acc[v][j + 1], acc[v][j + 2], acc[v][j + 3]);
                     } else {
-                        s.template finish<ALL>(slot, acc);
+                        s.template finish<MODE == kAdd>(slot, acc);
                     }
                     open = false;
                     slot = next;
@@ -687,15 +702,15 @@ __device__ __forceinline__ void sum_blocks(const S& s, const SumGrid& g, uint32_
 // All of a gradient's sums but the long runs' totals. The slices of a row's columns lie on XCDs of
 // their own (workgroup i runs on XCD i mod 8), so that what an XCD's L2 cache holds of dout is that
 // slice alone.
-template <typename D, typename E, bool VEC, bool WEIGHTS, bool DROP, bool ADD>
+template <typename D, typename E, bool VEC, bool WEIGHTS, bool DROP, int MODE>
 __global__ __launch_bounds__(kThreads) void sum_kernel(BankGradParams p, SumGrid g) {
     extern __shared__ uint4 lds16[];
     uint32_t* lds = reinterpret_cast<uint32_t*>(lds16);
-    const bool blocks = ADD || blockIdx.x < 8 * g.sums;
+    const bool blocks = MODE != kByRows || blockIdx.x < 8 * g.sums;
     const uint32_t number = blockIdx.x - (blocks ? 0 : 8 * g.sums), range = number / g.slices;
     if (range >= (blocks ? g.ranges : g.row_ranges)) return;
     const Sums<D, E, VEC, WEIGHTS, DROP> s(p, g.lanes, int(threadIdx.x) % g.lanes, number % g.slices);
-    if (blocks) sum_blocks<ADD>(s, g, range, lds);
+    if (blocks) sum_blocks<MODE>(s, g, range, lds);
     else sum_rows(s, g, range, lds);
 }
 
@@ -712,6 +727,7 @@ constexpr uint32_t kShort = 16;  // blocks of a run that one lane group adds up
 template <typename E, bool VEC, bool ADD> __global__ __launch_bounds__(kJoinThreads) void join_kernel(BankGradParams p, int lanes) {
     constexpr int N = 4;
     __shared__ uint64_t masks[2];
+    __shared__ uint32_t slots[64];  // of the blocks' last entries
     __shared__ float sums[kJoinThreads][N];
     const int tid = threadIdx.x, groups = kJoinThreads / lanes, lane = tid % lanes, group = tid / lanes;
     const int c0 = (int(blockIdx.y) * lanes + lane) * N;
@@ -723,12 +739,16 @@ template <typename E, bool VEC, bool ADD> __global__ __launch_bounds__(kJoinThre
     auto at = [&](uint64_t i) { return records[i].slot; };
     if (tid < 64) {
         // Bit i of the first: a run of several blocks begins in block b0 + i; of the second: block
-        // b0 + 1 + i is in the middle of one.
+        // b0 + 1 + i is in the middle of one. All of the slots that this takes are loaded at once.
         const uint64_t begin = uint64_t(b0 + tid) * p.block, end = begin + p.block;
-        const bool goes_on = cont(p, at, n, end), further = goes_on && cont(p, at, n, end + p.block);
-        const bool begins = goes_on && (begin == 0 || at(begin - 1) != at(end - 1));
-        const bool through = further && at(end) == at(end + p.block - 1);
-        const uint64_t b = __ballot(begins), m = __ballot(through);
+        auto any = [&](uint64_t i) { return records[min(i, uint64_t(p.entries - 1))].slot; };
+        const uint32_t earlier = any(begin > 0 ? begin - 1 : 0), last = any(end - 1), first = any(end), spill = any(end + p.spill);
+        const uint32_t next_last = any(end + p.block - 1), next_spill = any(end + p.block + p.spill);
+        const bool goes_on = end + p.spill < n && last == spill;
+        const bool further = goes_on && end + p.block + p.spill < n && next_last == next_spill;
+        const bool is_new = goes_on && (begin == 0 || earlier != last);
+        const uint64_t b = __ballot(is_new), m = __ballot(further && first == next_last);
+        slots[tid] = last;
         if (tid == 0) {
             masks[0] = b;
             masks[1] = m;
@@ -737,12 +757,16 @@ template <typename E, bool VEC, bool ADD> __global__ __launch_bounds__(kJoinThre
     __syncthreads();
     const uint64_t begins = masks[0], middles = masks[1];
     auto add = [&](float (&acc)[N], uint32_t b, uint32_t from, uint32_t more, uint32_t stride) {
-#pragma unroll 8
-        for (uint32_t c = from; c < more; c += stride) {
-            float x[N];
-            load_columns<float, N, true>(p.first + (int64_t(b) + 1 + c) * columns, c0, p.hd, x);
+        for (uint32_t c = from; c < more; c += kFlight * stride) {
+            float x[kFlight][N];
 #pragma unroll
-            for (int j = 0; j < N; ++j) acc[j] += x[j];
+            for (int u = 0; u < kFlight; ++u)
+                load_columns<float, N, true>(p.first + (int64_t(b) + 1 + min(c + u * stride, more - 1)) * columns, c0, p.hd, x[u]);
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u)
+                if (c + u * stride < more)
+#pragma unroll
+                    for (int j = 0; j < N; ++j) acc[j] += x[u][j];
         }
     };
     auto finish = [&](uint32_t slot, const float (&acc)[N]) {
@@ -764,13 +788,13 @@ template <typename E, bool VEC, bool ADD> __global__ __launch_bounds__(kJoinThre
         float acc[N];
         load_columns<float, N, true>(p.last + b * columns, c0, p.hd, acc);
         add(acc, b, 0, more, 1);
-        finish(at(uint64_t(b) * p.block + p.block - 1), acc);
+        finish(slots[i], acc);
     }
     for (uint64_t left = begins; left != 0; left &= left - 1) {
         const int i = __ffsll(static_cast<unsigned long long>(left)) - 1;
         uint32_t more = known(i);
         if (more <= kShort && i + more <= 64) continue;  // of the whole workgroup
-        const uint32_t b = b0 + uint32_t(i), slot = at(uint64_t(b) * p.block + p.block - 1);
+        const uint32_t b = b0 + uint32_t(i), slot = slots[i];
         if (i + more > 64) {  // perhaps further than the masks
             uint32_t found;
             do {
@@ -806,6 +830,13 @@ int log2_of(int v) {
     return s;
 }
 
+// Whether a written bank's sums are made a row at a time. With few entries for its rows it is zeroed
+// beside the sort instead, which takes as long without it, and only the rows that entries name are
+// written again: 32768 tokens of 50000 x 1024 in PLACE1 us instead of 88, 8192 entries of 131072 x 128
+// in PLACE2 instead of 44; but c3's 3.1 M entries of 2^21 slots, most of which are named, would take
+// as long as now.
+bool by_rows(const BankGradParams& p) { return !p.add && p.entries > p.num_slots; }
+
 SumGrid sum_grid(const BankGradParams& p, int dout_size, int bank_size) {
     const int n = 16 / dout_size, vecs = (p.hd + n - 1) / n;
     SumGrid g{};
@@ -822,7 +853,7 @@ SumGrid sum_grid(const BankGradParams& p, int dout_size, int bank_size) {
     g.shift = log2_of(p.block);
     g.ranges = (p.blocks + groups - 1) / groups;
     g.sums = uint32_t((int64_t(g.ranges) * g.slices + 7) / 8);
-    if (!p.add) {
+    if (by_rows(p)) {
         // Rows of a lane group: 32 KB of the bank a workgroup. (1563 tiles of 64 KB are one and a half
         // rounds of the compute units: 32768 tokens of 50000 x 1024, 123 against 89 us for the call; with
         // 16 KB, 101 us.)
@@ -842,10 +873,11 @@ void run_sum(const BankGradParams& p, const SumGrid& g, hipStream_t stream) {
     const int groups = kThreads / g.lanes, most = groups * p.block + p.spill + 2;
     size_t lds = size_t(lds_place(most, g.shift) + 1) * (sizeof(Term) + 4);
     const size_t for_rows = kStaged * sizeof(Term) + size_t(groups * g.group_rows + 3) * 4;
-    if (!p.add && for_rows > lds) lds = for_rows;
+    if (by_rows(p) && for_rows > lds) lds = for_rows;
     const dim3 grid{8 * (g.sums + g.rows)}, block{kThreads};
-    if (p.add) hipLaunchKernelGGL((sum_kernel<D, E, VEC, WEIGHTS, DROP, true>), grid, block, lds, stream, p, g);
-    else hipLaunchKernelGGL((sum_kernel<D, E, VEC, WEIGHTS, DROP, false>), grid, block, lds, stream, p, g);
+    if (p.add) hipLaunchKernelGGL((sum_kernel<D, E, VEC, WEIGHTS, DROP, kAdd>), grid, block, lds, stream, p, g);
+    else if (by_rows(p)) hipLaunchKernelGGL((sum_kernel<D, E, VEC, WEIGHTS, DROP, kByRows>), grid, block, lds, stream, p, g);
+    else hipLaunchKernelGGL((sum_kernel<D, E, VEC, WEIGHTS, DROP, kStore>), grid, block, lds, stream, p, g);
 }
 
 template <typename D, typename E, bool VEC> void run_sums(const BankGradParams& p, hipStream_t stream) {
@@ -876,7 +908,7 @@ template <typename D, typename E> void run_types(const BankGradParams& p, hipStr
 // Up to this many entries one workgroup sorts them all.
 constexpr int64_t kOneEntries = 4 * kOneThreads;
 template <bool LOOKUP> void run_sort_one(const BankGradParams& p, hipStream_t stream) {
-    const dim3 grid{1}, block{kOneThreads};
+    const dim3 grid{unsigned(1 + zero_groups(p.zero_bytes, 1))}, block{kOneThreads};
     if (p.entries <= kOneThreads) hipLaunchKernelGGL((sort_one_kernel<LOOKUP, 1>), grid, block, 0, stream, p);
     else if (p.entries <= 2 * kOneThreads) hipLaunchKernelGGL((sort_one_kernel<LOOKUP, 2>), grid, block, 0, stream, p);
     else hipLaunchKernelGGL((sort_one_kernel<LOOKUP, 4>), grid, block, 0, stream, p);
@@ -886,7 +918,7 @@ template <bool LOOKUP> void run_sort_one(const BankGradParams& p, hipStream_t st
 constexpr uint32_t kSumTiles = 64;
 
 template <bool FIRST, bool LOOKUP, int ITEMS, bool SUMS> void run_pass(const BankGradParams& p, int pass, hipStream_t stream) {
-    const dim3 tiles{p.tiles}, block{kThreads};
+    const dim3 tiles{unsigned(p.tiles + zero_groups(p.zero_bytes, 2 * p.passes))}, block{kThreads};
     hipLaunchKernelGGL((sort_count_kernel<FIRST, LOOKUP, ITEMS, SUMS>), tiles, block, 0, stream, p, pass);
     if (!SUMS) hipLaunchKernelGGL(sort_scan_kernel, dim3(1u << p.bits), block, 0, stream, p, pass);
     hipLaunchKernelGGL((sort_place_kernel<FIRST, LOOKUP, ITEMS, SUMS>), tiles, block, 0, stream, p, pass);
@@ -940,7 +972,8 @@ int64_t bank_grad_layout(BankGradParams* p, void* workspace) {
 
 int64_t bank_grad_groups(const BankGradParams& p, int dout_size, int bank_size) {
     const SumGrid g = sum_grid(p, dout_size, bank_size);
-    return 8 * (int64_t(g.sums) + g.rows);
+    const int64_t zeros = p.add || by_rows(p) ? 0 : zero_groups(int64_t(p.num_slots) * p.hd * bank_size, 1);
+    return 8 * (int64_t(g.sums) + g.rows) + 4 * (p.tiles + zeros + 1);  // the sort's may have 1024 threads
 }
 
 hipError_t launch_bank_grad(const BankGradParams& call, bool dout_bf16, bool bank_bf16, hipStream_t stream) {
@@ -949,11 +982,9 @@ hipError_t launch_bank_grad(const BankGradParams& call, bool dout_bf16, bool ban
     p.by_width[0] = divisor(p.width[0]);
     p.by_width[1] = divisor(p.width[1]);
     p.by_chunk = divisor(p.chunk);
+    if (!by_rows(p) && !p.add) p.zero_bytes = int64_t(p.num_slots) * p.hd * (bank_bf16 ? 2 : 4);
     if (p.entries == 0) {
-        const int64_t bytes = int64_t(p.num_slots) * p.hd * (bank_bf16 ? 2 : 4);
-        if (!p.add)
-            hipLaunchKernelGGL(zero_kernel, dim3(unsigned((bytes + kZeroBytes - 1) / kZeroBytes)), dim3(kThreads), 0, stream,
-                               static_cast<char*>(p.dbank), bytes);
+        if (!p.add) hipLaunchKernelGGL(zero_kernel, dim3(unsigned(zero_groups(p.zero_bytes, 1))), dim3(kThreads), 0, stream, p);
         return hipGetLastError();
     }
     if (p.w[0] == nullptr) run_sort<true>(p, stream);

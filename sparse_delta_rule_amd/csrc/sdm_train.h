@@ -118,6 +118,7 @@ struct BankGradParams {
     uint32_t tiles;       // of 256 * items entries
     int block, spill;     // entries of a lane group; how far it may go past their end
     uint32_t blocks;
+    int64_t zero_bytes;   // of dbank, zeroed beside the sort
     // workspace
     uint32_t* n;          // [1] entries that count
     int64_t stride;       // of the counts of a digit

@@ -267,7 +267,9 @@ def test_bank_grad_workspace():
     assert f(-1, 1, 1) == f(1, 0, 1) == f(1, 1, 0) == f(1 << 31, 1, 1) == f(1, 1 << 31, 1) == f(1, 1, 1 << 29) == 0
     for n in (1, 1000, 1 << 20):
         for hd in (1, 8, 128, 1024):
-            assert 16 * n < f(n, 1 << 20, hd) < 16 * n + 100 * 256 * 4 + n * 1024 * 4 // 2048 + 2 * (n // 8 + 1) * 4 * (hd + 8) + n
+            # two arrays of 12 bytes an entry, sums of at most two runs for each 16 entries, counts of digits
+            least, rows = 24 * n, 2 * -(-n // 16) * 4 * (hd + 7) // 8 * 8
+            assert least < f(n, 1 << 20, hd) < least + rows + 64 * 1024 + n
 
 
 # ------------------------------------------------------------------ the binding's own checks
