@@ -31,7 +31,6 @@ struct Larger {
 };
 struct Plus {
     __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
-    __device__ __forceinline__ int32_t operator()(int32_t a, int32_t b) const { return int32_t(uint32_t(a) + uint32_t(b)); }
 };
 constexpr Larger larger{};
 constexpr Plus plus{};
@@ -163,7 +162,9 @@ constexpr int kSmallKeys = 1024;
 constexpr int kSmallThreads = 512;
 
 // Rows of at most 1024 keys: LANES lanes a row, VPT keys a lane, whose sums over the piece
-// stay in registers and are put together over the workgroup's rows at its end.
+// stay in registers and are put together over the workgroup's rows at its end. 32768 x 256 float32
+// keys, 30 MB of live rows, take 10.6 us and the second pass 7.6: both bound by the latency of
+// their steps (5 us are the bytes'), as 512 pieces are two workgroups a compute unit.
 template <typename E, int LANES, int VPT, bool VEC>
 __global__ __launch_bounds__(kSmallThreads) void balance_small_kernel(BalanceParams p) {
     using Row = RowKeys<E, LANES, VPT, VEC>;
@@ -219,12 +220,16 @@ __global__ __launch_bounds__(kSmallThreads) void balance_small_kernel(BalancePar
 constexpr int kCountKeys = 16384;  // keys counted in LDS at a time
 
 // Longer rows: the workgroup takes one row after another, its sums in registers. A wavefront's
-// terms have an offset of their own, so a row needs one barrier.
-template <typename E, int THREADS, int VPT, bool VEC>
+// terms have an offset of their own, so a row needs one barrier. Rows of more than 32768 keys are
+// taken in parts, which are read again for their shares: a lane's 64 keys and 64 sums do not fit its
+// registers (1024 rows of 65536 bfloat16 keys: 228 us with both there, 194 in parts). 4096 rows of
+// 16384 bfloat16 keys take 36 us, 3.7 TB/s: the instructions (200 for a wavefront's part of a row)
+// are 24 us of it, one barrier a row with 16 wavefronts a compute unit the rest.
+template <typename E, int THREADS, int VPT, int PARTS, bool VEC>
 __global__ __launch_bounds__(THREADS) void balance_big_kernel(BalanceParams p) {
     using Row = RowKeys<E, THREADS, VPT, VEC>;
-    constexpr int kWaves = THREADS / 64;
-    constexpr bool kAhead = VPT * sizeof(E) <= 64;  // the next row is loaded while one is taken
+    constexpr int kWaves = THREADS / 64, kPart = THREADS * VPT;
+    constexpr bool kAhead = PARTS == 1 && VPT * sizeof(E) <= 64;  // the next row is loaded while one is taken
     __shared__ float offset[2][kWaves], total[2][kWaves];
     __shared__ uint32_t words[kCountKeys / 2];
     ieee_mode_off();
@@ -246,69 +251,91 @@ __global__ __launch_bounds__(THREADS) void balance_big_kernel(BalanceParams p) {
         for (int i = tid; i < min(kCountKeys / 2, stride - base / 2); i += THREADS) to[i] = words[i];
         __syncthreads();
     }
-    float acc[VPT];
+    float acc[PARTS][VPT];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) acc[i] = 0.0f;
+    for (int h = 0; h < PARTS; ++h)
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) acc[h][i] = 0.0f;
     int buffer = 0;
     for (uint32_t t = r.first; t < r.end; ++t) {
+        const E* row = logits + int64_t(t) * p.keys;
         float c[VPT];
         if (kAhead) {
             next.values(p.keys, tid, c);
             next.load(logits + int64_t(min(t + 1, r.end - 1)) * p.keys, p.keys, tid);
         }
         if (!is_live(p, t)) continue;  // of the whole workgroup
-        if (!kAhead) {
-            next.load(logits + int64_t(t) * p.keys, p.keys, tid);
-            next.values(p.keys, tid, c);
+        // A part's terms, relative to an offset of its own.
+        float o, scale;
+        auto take = [&](int h) {
+            if (!kAhead) {
+                next.load(row + h * kPart, p.keys - h * kPart, tid);
+                next.values(p.keys - h * kPart, tid, c);
+            }
+            o = terms(p.score, reduce<64>(max_of(c, -INFINITY), larger), c, nullptr, scale);
+        };
+        float mine = -FLT_MAX, its = 0;
+#pragma unroll 1
+        for (int h = 0; h < PARTS; ++h) {
+            take(h);
+            const float sum = reduce<64>(sum_of(c), plus) * scale, most = max32(mine, o);
+            its = PARTS == 1 ? sum : its * exp32(mine - most) + sum * exp32(o - most);
+            mine = most;
         }
-        const float largest = reduce<64>(max_of(c, -INFINITY), larger);
-        float scale;
-        const float o = terms(p.score, largest, c, nullptr, scale);
-        const float sum = reduce<64>(sum_of(c), plus) * scale;
         if (lane == 0) {
-            offset[buffer][wave] = o;
-            total[buffer][wave] = sum;
+            offset[buffer][wave] = mine;
+            total[buffer][wave] = its;
         }
         __syncthreads();
         // A lane for each wavefront's part, in every 16 lanes.
         const int w = lane % 16 % kWaves;
         const float part = offset[buffer][w], most = lanes_reduce<16>(part, larger);
         const float z = lanes_reduce<16>(lane % 16 < kWaves ? total[buffer][w] * exp32(part - most) : 0.0f, plus);
-        const float f = z > 0 ? scale * exp32(o - most) / z : 0.0f;
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) acc[i] = fmaf(c[i], f, acc[i]);
+        for (int h = 0; h < PARTS; ++h) {
+            if (PARTS > 1) take(h);
+            const float f = z > 0 ? scale * exp32(o - most) / z : 0.0f;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) acc[h][i] = fmaf(c[i], f, acc[h][i]);
+        }
         buffer ^= 1;
     }
     float* out = p.part + int64_t(blockIdx.x) * p.keys;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
-        if (Row::key_of(i, tid) < p.keys) out[Row::key_of(i, tid)] = acc[i];
+    for (int h = 0; h < PARTS; ++h) {
+#pragma unroll
+        for (int i = 0; i < VPT; i += VEC ? 4 : 1) {
+            const int key = h * kPart + Row::key_of(i, tid);
+            if (key >= p.keys) continue;
+            if constexpr (VEC) *reinterpret_cast<float4*>(out + key) = make_float4(acc[h][i], acc[h][i + 1], acc[h][i + 2], acc[h][i + 3]);
+            else out[key] = acc[h][i];
+        }
+    }
 }
 
 // ------------------------------------------------------------------ second pass: sequences
 
-constexpr int kJoinThreads = 1024;
 constexpr int kJoinKeys = 64;  // keys of an item
 
 template <typename T> __device__ __forceinline__ T wave_sum(T v) {
     for (int n = 1; n < 64; n *= 2) v += __shfl_xor(v, n);
     return v;
 }
-template <typename T> __device__ __forceinline__ T join_sum(T v, T* lds) {
+template <int THREADS, typename T> __device__ __forceinline__ T join_sum(T v, T* lds) {
     v = wave_sum(v);
     __syncthreads();
     if (threadIdx.x % 64 == 0) lds[threadIdx.x / 64] = v;
     __syncthreads();
     v = lds[0];
-    for (int w = 1; w < kJoinThreads / 64; ++w) v += lds[w];
+    for (int w = 1; w < THREADS / 64; ++w) v += lds[w];
     return v;
 }
 
 // An item is 64 keys of a sequence: the pieces' sums and counts in order, in float64. 16 lanes take
-// a piece's keys, four each, so that a workgroup reads 64 pieces at a time. The workgroup that ends
-// last puts the items' parts of the loss together.
-__global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceParams p) {
-    constexpr int kRows = kJoinThreads / 16, kWaves = kJoinThreads / 64;
+// a piece's keys, four each, so that a workgroup reads THREADS / 16 pieces at a time. The workgroup
+// that ends last puts the items' parts of the loss together.
+template <int THREADS> __global__ __launch_bounds__(THREADS) void balance_join_kernel(BalanceParams p) {
+    constexpr int kRows = THREADS / 16, kWaves = THREADS / 64;
     __shared__ double sums[kWaves][kJoinKeys];
     __shared__ int32_t counts[kWaves][kJoinKeys];
     __shared__ double scratch[kWaves];
@@ -323,7 +350,7 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceParam
         const uint64_t first = uint64_t(g) * p.pieces;
         const int key = int(b) * kJoinKeys + k0;
         double n = 0;
-        for (uint32_t i = tid; i < p.pieces; i += kJoinThreads) n += p.live[first + i];
+        for (uint32_t i = tid; i < p.pieces; i += THREADS) n += p.live[first + i];
         double sum[4] = {};
         int32_t count[4] = {};
         if (key < p.keys) {
@@ -362,7 +389,7 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceParam
                 counts[wave][k0 + j] = count[j];
             }
         }
-        const uint32_t live = uint32_t(join_sum(n, scratch));  // and a barrier
+        const uint32_t live = uint32_t(join_sum<THREADS>(n, scratch));  // and a barrier
         if (wave == 0) {
             const int mine = int(b) * kJoinKeys + lane;
             double s = 0;
@@ -389,16 +416,16 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceParam
     __syncthreads();
     if (ticket != gridDim.x - 1) return;
     double with = 0;
-    for (uint32_t g = tid; g < p.sequences; g += kJoinThreads) with += p.live_all[g] > 0;
-    const double sequences = join_sum(with, scratch);
+    for (uint32_t g = tid; g < p.sequences; g += THREADS) with += p.live_all[g] > 0;
+    const double sequences = join_sum<THREADS>(with, scratch);
     auto coef = [&](uint32_t g) {
         const double n = p.live_all[g];
         return n > 0 ? p.scale * p.keys / (double(p.k) * n * n * sequences) : 0.0;
     };
     double loss = 0;
-    for (uint64_t item = tid; item < items; item += kJoinThreads) loss += coef(uint32_t(item / blocks)) * p.loss_part[item];
-    for (uint32_t g = tid; g < p.sequences; g += kJoinThreads) p.coef[g] = float(coef(g));
-    loss = join_sum(loss, scratch);
+    for (uint64_t item = tid; item < items; item += THREADS) loss += coef(uint32_t(item / blocks)) * p.loss_part[item];
+    for (uint32_t g = tid; g < p.sequences; g += THREADS) p.coef[g] = float(coef(g));
+    loss = join_sum<THREADS>(loss, scratch);
     if (tid == 0) *p.loss = float(loss);
 }
 
@@ -451,16 +478,28 @@ __device__ __forceinline__ float row_factor(const BalanceParams& p, uint32_t seq
     return p.coef[sequence] * (p.dloss != nullptr ? *p.dloss : 1.0f);
 }
 
-// A lane's counts; returns their sum.
+// A lane's counts; returns their sum. (In float64: counts that were added up over many devices may sum
+// to more than an integer of 32 bits holds.)
 template <typename Row, int VPT>
-__device__ __forceinline__ int32_t load_counts(const BalanceParams& p, uint32_t sequence, int tid, int32_t (&count)[VPT]) {
-    const int32_t* counts = p.counts + int64_t(sequence) * p.keys;
+__device__ __forceinline__ double load_counts(const int32_t* counts, int keys, int tid, int32_t (&count)[VPT]) {
+    if (Row::kN > 1 && reinterpret_cast<uintptr_t>(counts) % 16 == 0) {  // rows of whole vectors
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) count[i] = counts[min(Row::key_of(i, tid), p.keys - 1)];
-    uint32_t sum = 0;
+        for (int i = 0; i + 3 < VPT; i += 4) {
+            const int4 v = *reinterpret_cast<const int4*>(counts + min(Row::key_of(i, tid), keys - 4));
+            count[i] = v.x, count[i + 1] = v.y, count[i + 2] = v.z, count[i + 3] = v.w;
+        }
+    } else {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) sum += Row::key_of(i, tid) < p.keys ? uint32_t(count[i]) : 0;
-    return int32_t(sum);
+        for (int i = 0; i < VPT; ++i) count[i] = counts[min(Row::key_of(i, tid), keys - 1)];
+    }
+    double sum = 0;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) sum += Row::key_of(i, tid) < keys ? double(count[i]) : 0.0;
+    return sum;
+}
+template <int LANES> __device__ __forceinline__ double lanes_sum(double v) {
+    for (int n = 1; n < LANES; n *= 2) v += __shfl_xor(v, n);
+    return v;
 }
 // The differences to `from`, exact below 2^24.
 template <int N> __device__ __forceinline__ void apart(const int32_t (&count)[N], int32_t from, float (&c)[N]) {
@@ -521,6 +560,7 @@ __device__ __forceinline__ float count_of_largest(const float (&e)[VPT], const f
     return top;
 }
 
+// 32768 x 256 float32 keys: 14.6 us, 4.3 TB/s of live rows read and rows written.
 template <typename E, int LANES, int VPT, bool VEC>
 __global__ __launch_bounds__(kSmallThreads) void balance_backward_small_kernel(BalanceParams p) {
     using Row = RowKeys<E, LANES, VPT, VEC>;
@@ -539,8 +579,8 @@ __global__ __launch_bounds__(kSmallThreads) void balance_backward_small_kernel(B
     float c[VPT];
     {
         int32_t count[VPT];
-        const int32_t sum = reduce<LANES>(load_counts<Row>(p, r.sequence, lane, count), plus);
-        apart(count, sum / p.keys, c);
+        const double sum = lanes_sum<LANES>(load_counts<Row>(p.counts + int64_t(r.sequence) * p.keys, p.keys, lane, count));
+        apart(count, int32_t(sum / p.keys), c);
     }
     const float f = row_factor(p, r.sequence);
     for (uint32_t t0 = r.first; t0 < r.end; t0 += kRows) {  // the same rounds in every wavefront
@@ -566,6 +606,8 @@ __global__ __launch_bounds__(kSmallThreads) void balance_backward_small_kernel(B
     }
 }
 
+// A row at a time, the counts in registers. 4096 rows of 16384 bfloat16 keys: 61 us, 4.4 TB/s read
+// and written, with 41 us of instructions.
 template <typename E, int THREADS, int VPT, bool VEC>
 __global__ __launch_bounds__(THREADS) void balance_backward_big_kernel(BalanceParams p) {
     using Row = RowKeys<E, THREADS, VPT, VEC>;
@@ -573,7 +615,7 @@ __global__ __launch_bounds__(THREADS) void balance_backward_big_kernel(BalancePa
     constexpr bool kAhead = VPT * sizeof(E) <= 64;  // the next row is loaded while one is taken
     __shared__ float offset[2][kWaves], total[2][kWaves], dot[2][kWaves], term[2][kWaves];
     __shared__ float again[2][kWaves];
-    __shared__ int32_t sums[kWaves];
+    __shared__ double sums[kWaves];
     ieee_mode_off();
     const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
     const Piece r = this_piece(p, blockIdx.x);
@@ -584,12 +626,12 @@ __global__ __launch_bounds__(THREADS) void balance_backward_big_kernel(BalancePa
     float c[VPT];
     {
         int32_t count[VPT];
-        const int32_t mine = reduce<64>(load_counts<Row>(p, r.sequence, tid, count), plus);
+        const double mine = lanes_sum<64>(load_counts<Row>(p.counts + int64_t(r.sequence) * p.keys, p.keys, tid, count));
         if (lane == 0) sums[wave] = mine;
         __syncthreads();
-        uint32_t sum = 0;
-        for (int w = 0; w < kWaves; ++w) sum += uint32_t(sums[w]);
-        apart(count, int32_t(sum) / p.keys, c);
+        double sum = 0;
+        for (int w = 0; w < kWaves; ++w) sum += sums[w];
+        apart(count, int32_t(sum / p.keys), c);
     }
     const float f = row_factor(p, r.sequence);
     int buffer = 0;
@@ -631,10 +673,11 @@ __global__ __launch_bounds__(THREADS) void balance_backward_big_kernel(BalancePa
         const float biggest = lanes_reduce<16>(term[buffer][w] * part, larger);
         const float share = z > 0 ? 1.0f / z : 0.0f, own = scale * exp32(o - most);
         if (biggest * share > kMostShare) {  // of the whole workgroup
-            // The key's count, then the sum relative to it.
+            // The count of the key of the largest term (one that has more than kMostShare of the share is
+            // alone above half of it), then the sum relative to that.
             const float here = reduce<64>(max_of(e, 0.0f), larger);
             float its = reduce<64>(count_of_largest<Row>(e, c, here, p.keys, tid), larger);
-            if (!(term[buffer][wave] * exp32(o - most) == biggest)) its = -INFINITY;
+            if (!(here * own * share > 0.5f)) its = -INFINITY;
             if (lane == 0) again[0][wave] = its;
             __syncthreads();
             top = lanes_reduce<16>(again[0][w], larger);
@@ -649,9 +692,132 @@ __global__ __launch_bounds__(THREADS) void balance_backward_big_kernel(BalancePa
     }
 }
 
+// Rows of more than 32768 keys, in parts that are read, with their counts, for each of their uses: a
+// lane's 64 keys and counts do not fit its registers (1024 rows of 65536 keys, float32: 467 us with
+// both there, 205 in parts; bfloat16 and sigmoid: 625 and 142 us).
+template <typename E, int THREADS, int VPT, int PARTS, bool VEC>
+__global__ __launch_bounds__(THREADS) void balance_backward_long_kernel(BalanceParams p) {
+    using Row = RowKeys<E, THREADS, VPT, VEC>;
+    constexpr int kWaves = THREADS / 64, kPart = THREADS * VPT;
+    __shared__ float offset[2][kWaves], total[2][kWaves], dot[2][kWaves], term[2][kWaves];
+    __shared__ float again[2][kWaves];
+    __shared__ double sums[kWaves];
+    ieee_mode_off();
+    const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+    const Piece r = this_piece(p, blockIdx.x);
+    const E* logits = static_cast<const E*>(p.logits);
+    E* dlogits = static_cast<E*>(p.dlogits);
+    RawRow<E, THREADS, VPT, VEC> next;
+    const int32_t* counts = p.counts + int64_t(r.sequence) * p.keys;
+    int32_t mean = 0;
+    float c[VPT];
+    auto load_part = [&](int h) {
+        int32_t count[VPT];
+        const double sum = load_counts<Row>(counts + h * kPart, p.keys - h * kPart, tid, count);
+        apart(count, mean, c);
+        return sum;
+    };
+    {
+        double mine = 0;
+#pragma unroll 1
+        for (int h = 0; h < PARTS; ++h) mine += load_part(h);
+        mine = lanes_sum<64>(mine);
+        if (lane == 0) sums[wave] = mine;
+        __syncthreads();
+        double sum = 0;
+        for (int w = 0; w < kWaves; ++w) sum += sums[w];
+        mean = int32_t(sum / p.keys);
+    }
+    const float f = row_factor(p, r.sequence);
+    int buffer = 0;
+    for (uint32_t t = r.first; t < r.end; ++t) {
+        const E* row = logits + int64_t(t) * p.keys;
+        E* out = dlogits + int64_t(t) * p.keys;
+        float e[VPT], rest[VPT], o, scale, largest;
+        if (!is_live(p, t)) {  // of the whole workgroup
+            if (!p.accumulate) {
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) e[i] = 0.0f;
+#pragma unroll 1
+                for (int h = 0; h < PARTS; ++h)
+                    store_row<E, Row, VPT, VEC>(out + h * kPart, p.keys - h * kPart, tid, e, false);
+            }
+            continue;
+        }
+        // A part's terms, relative to an offset of its own, and its counts.
+        auto take = [&](int h) {
+            next.load(row + h * kPart, p.keys - h * kPart, tid);
+            next.values(p.keys - h * kPart, tid, e);
+            load_part(h);
+            largest = reduce<64>(max_of(e, -INFINITY), larger);
+            o = terms(p.score, largest, e, rest, scale);
+        };
+        float mine = -FLT_MAX, its_total = 0, its_dot = 0, its_term = 0;
+#pragma unroll 1
+        for (int h = 0; h < PARTS; ++h) {
+            take(h);
+            const float sum = reduce<64>(sum_of(e), plus) * scale, products = reduce<64>(dot_of(e, c, 0.0f), plus) * scale;
+            const float most = max32(mine, o), before = exp32(mine - most), now = exp32(o - most);
+            its_total = its_total * before + sum * now;
+            its_dot = its_dot * before + products * now;
+            its_term = max32(its_term * before, largest_term(p.score, largest, o) * now);
+            mine = most;
+        }
+        if (lane == 0) {
+            offset[buffer][wave] = mine;
+            total[buffer][wave] = its_total;
+            dot[buffer][wave] = its_dot;
+            term[buffer][wave] = its_term;
+        }
+        __syncthreads();
+        // A lane for each wavefront's part, in every 16 lanes.
+        const int w = lane % 16 % kWaves;
+        const float at = offset[buffer][w], most = lanes_reduce<16>(at, larger);
+        const float part = lane % 16 < kWaves ? exp32(at - most) : 0.0f;
+        const float z = lanes_reduce<16>(total[buffer][w] * part, plus);
+        float d = lanes_reduce<16>(dot[buffer][w] * part, plus), top = 0;
+        const float biggest = lanes_reduce<16>(term[buffer][w] * part, larger);
+        const float share = z > 0 ? 1.0f / z : 0.0f;
+        if (biggest * share > kMostShare) {  // of the whole workgroup
+            // The count of the key of the largest term (one that has more than kMostShare of the share is
+            // alone above half of it), then the sum relative to that.
+            float its = -INFINITY;
+#pragma unroll 1
+            for (int h = 0; h < PARTS; ++h) {
+                take(h);
+                const float own = scale * exp32(o - most), here = reduce<64>(max_of(e, 0.0f), larger);
+                if (here * own * share > 0.5f)
+                    its = max32(its, reduce<64>(count_of_largest<Row>(e, c, here, p.keys - h * kPart, tid), larger));
+            }
+            if (lane == 0) again[0][wave] = its;
+            __syncthreads();
+            top = lanes_reduce<16>(again[0][w], larger);
+            its = 0;
+#pragma unroll 1
+            for (int h = 0; h < PARTS; ++h) {
+                take(h);
+                its += reduce<64>(dot_of(e, c, top), plus) * scale * exp32(o - most);
+            }
+            if (lane == 0) again[1][wave] = its;
+            __syncthreads();
+            d = lanes_reduce<16>(lane % 16 < kWaves ? again[1][w] : 0.0f, plus);
+        }
+#pragma unroll 1
+        for (int h = 0; h < PARTS; ++h) {
+            take(h);
+            gradients(p.score, rest, c, top, share * scale * exp32(o - most), d * share, f, e);
+            store_row<E, Row, VPT, VEC>(out + h * kPart, p.keys - h * kPart, tid, e, p.accumulate);
+        }
+        buffer ^= 1;
+    }
+}
+
 // ------------------------------------------------------------------ launches
 
-constexpr int64_t kPieces = 512, kBigPieces = 256;  // pieces wanted of a call with many tokens
+// Pieces wanted of a call with many tokens. More read the rows no faster and leave the second pass
+// more to add (32768 x 256: 19.4 us with 512, 20.2 with 1024 and 256; 4096 x 16384: 64 with 256, 80
+// with 512).
+constexpr int64_t kPieces = 512, kBigPieces = 256;
 
 template <typename E, int LANES, int VPT> void run_small(const BalanceParams& p, bool vec, bool backward, hipStream_t s) {
     const dim3 grid{unsigned(p.sequences * p.pieces)}, block{kSmallThreads};
@@ -660,12 +826,24 @@ template <typename E, int LANES, int VPT> void run_small(const BalanceParams& p,
     else if (vec) hipLaunchKernelGGL((balance_small_kernel<E, LANES, VPT, true>), grid, block, 0, s, p);
     else hipLaunchKernelGGL((balance_small_kernel<E, LANES, VPT, false>), grid, block, 0, s, p);
 }
-template <typename E, int THREADS, int VPT> void run_big(const BalanceParams& p, bool vec, bool backward, hipStream_t s) {
-    const dim3 grid{unsigned(p.sequences * p.pieces)}, block{THREADS};
-    if (vec && backward) hipLaunchKernelGGL((balance_backward_big_kernel<E, THREADS, VPT, true>), grid, block, 0, s, p);
-    else if (backward) hipLaunchKernelGGL((balance_backward_big_kernel<E, THREADS, VPT, false>), grid, block, 0, s, p);
-    else if (vec) hipLaunchKernelGGL((balance_big_kernel<E, THREADS, VPT, true>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((balance_big_kernel<E, THREADS, VPT, false>), grid, block, 0, s, p);
+template <typename E, int VPT, int PARTS> void run_big(const BalanceParams& p, bool vec, bool backward, hipStream_t s) {
+    const dim3 grid{unsigned(p.sequences * p.pieces)}, block{1024};
+    if (backward) {
+        if constexpr (PARTS == 1) {
+            if (vec) hipLaunchKernelGGL((balance_backward_big_kernel<E, 1024, VPT, true>), grid, block, 0, s, p);
+            else hipLaunchKernelGGL((balance_backward_big_kernel<E, 1024, VPT, false>), grid, block, 0, s, p);
+        } else {
+            // Vectors of bfloat16 spill (65536 keys, sigmoid: 285 us; key by key 142); of float32 they pay
+            // (205 us; key by key 312).
+            constexpr bool kVec = sizeof(E) == 4;
+            if (kVec && vec) hipLaunchKernelGGL((balance_backward_long_kernel<E, 1024, VPT, PARTS, kVec>), grid, block, 0, s, p);
+            else hipLaunchKernelGGL((balance_backward_long_kernel<E, 1024, VPT, PARTS, false>), grid, block, 0, s, p);
+        }
+    } else if (vec) {
+        hipLaunchKernelGGL((balance_big_kernel<E, 1024, VPT, PARTS, true>), grid, block, 0, s, p);
+    } else {
+        hipLaunchKernelGGL((balance_big_kernel<E, 1024, VPT, PARTS, false>), grid, block, 0, s, p);
+    }
 }
 template <typename E> void run_rows(const BalanceParams& p, bool backward, hipStream_t s) {
     const uintptr_t at = reinterpret_cast<uintptr_t>(p.logits) | (backward ? reinterpret_cast<uintptr_t>(p.dlogits) : 0);
@@ -674,10 +852,10 @@ template <typename E> void run_rows(const BalanceParams& p, bool backward, hipSt
     else if (p.keys <= 256) run_small<E, 32, 8>(p, vec, backward, s);
     else if (p.keys <= 512) run_small<E, 64, 8>(p, vec, backward, s);
     else if (p.keys <= 1024) run_small<E, 64, 16>(p, vec, backward, s);
-    else if (p.keys <= 8192) run_big<E, 1024, 8>(p, vec, backward, s);
-    else if (p.keys <= 16384) run_big<E, 1024, 16>(p, vec, backward, s);
-    else if (p.keys <= 32768) run_big<E, 1024, 32>(p, vec, backward, s);
-    else run_big<E, 1024, 64>(p, vec, backward, s);
+    else if (p.keys <= 8192) run_big<E, 8, 1>(p, vec, backward, s);
+    else if (p.keys <= 16384) run_big<E, 16, 1>(p, vec, backward, s);
+    else if (p.keys <= 32768) run_big<E, 32, 1>(p, vec, backward, s);
+    else run_big<E, 16, 4>(p, vec, backward, s);
 }
 
 }  // namespace
@@ -720,8 +898,10 @@ hipError_t launch_balance(const BalanceParams& p, bool bf16, hipStream_t stream)
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     int64_t items = int64_t(p.sequences) * ((p.keys + kJoinKeys - 1) / kJoinKeys);
-    if (items > 65536) items = 65536;
-    hipLaunchKernelGGL(balance_join_kernel, dim3(unsigned(items)), dim3(kJoinThreads), 0, stream, p);
+    if (items > 1024) items = 1024;  // workgroups: each adds to one counter, some 20 ns after the other
+    // Many short sequences have few pieces each.
+    if (p.pieces <= 16) hipLaunchKernelGGL(balance_join_kernel<256>, dim3(unsigned(items)), dim3(256), 0, stream, p);
+    else hipLaunchKernelGGL(balance_join_kernel<1024>, dim3(unsigned(items)), dim3(1024), 0, stream, p);
     return hipGetLastError();
 }
 

@@ -135,7 +135,7 @@ def test_no_tokens(per_chunk):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
-@pytest.mark.parametrize("N", [50, 600, 3000])
+@pytest.mark.parametrize("N", [50, 200, 600, 3000, 20000, 40000])
 def test_masked_and_extreme_logits(N, score):
     x = logits_like(9, 24, N)
     g = torch.Generator().manual_seed(5)
@@ -159,7 +159,7 @@ def test_masked_and_extreme_logits(N, score):
     assert torch.isfinite(mean).all() and not d[2].any() and not d[3].any()
 
 
-@pytest.mark.parametrize("N", [64, 2048])
+@pytest.mark.parametrize("N", [64, 2048, 16384, 20001, 40000, 65535])
 @pytest.mark.parametrize("gap", [5.0, 20.0, 40.0, 80.0])
 def test_one_key_far_above_the_rest(N, gap):
     """Its gradient is of the others' size times their shares: differences to its own count cancel nothing."""
@@ -173,6 +173,37 @@ def test_one_key_far_above_the_rest(N, gap):
     # of at most 120 roundings, and (4 + 3 gap) u of the shares
     assert np.allclose(d[:, 3].cpu(), want[:, 3], rtol=(8 * 120 + 4 * gap) * 2.0 ** -24, atol=2.0 ** -126)
     assert want[0, 3] > 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("N", [40, 300, 900, 5000, 33000])
+def test_confident_rows(N, score, dtype):
+    """Rows one of whose keys has more, or nearly, 4/5 of the share, beside even ones."""
+    x = logits_like(3, 40, N, torch.float32, 0.5)
+    for t in range(40):
+        if t % 3:
+            level = np.log(max(N - 1, 1) * (3.5 + t / 20))  # shares about 0.78 to 0.85
+            x[t] = x[t] * 0.01 - (30 if score == "sigmoid" else 0)
+            x[t, (t * 7) % N] += float(level)
+    check(x.to(dtype), choices(4, 40, N, 4), score=score, chunk=10, chunk_valid=torch.tensor([10, 7, 0, 9], dtype=torch.int32),
+          per_chunk=True)
+
+
+def test_counts_that_are_all_alike_or_large():
+    """The gradient of equal counts is 0 up to the differences' own roundings; counts past 2^24 keep their differences."""
+    x = logits_like(5, 16, 64).to(DEV)
+    coef = torch.ones(1, device=DEV)
+    same = torch.full((1, 64), 123456, dtype=torch.int32, device=DEV)
+    assert not sdm.sdm_route_balance_backward(x, same, coef).any()
+    big = same + (1 << 28)
+    big[0, ::2] += 3
+    small = torch.zeros_like(same)
+    small[0, ::2] = 3
+    a, b = (sdm.sdm_route_balance_backward(x, c, coef) for c in (big, small))
+    want, size = ref.balance_backward(x.cpu().numpy(), small.cpu().numpy(), [1.0])
+    for d in (a, b):
+        assert (np.abs(d.double().cpu().numpy() - want) <= size + 2.0 ** -23 * np.abs(want)).all()
 
 
 def test_streams_and_index_types():

@@ -93,6 +93,56 @@ def test_slots(slots):
     lookup_case(5000, slots, 2, "skewed", add=True, index=torch.int32)
 
 
+@pytest.mark.parametrize("kind", ["even", "skewed", "one", "runs", "falling", "none"])
+@pytest.mark.parametrize("n", [15, 16, 17, 4096, 4097, 8192, 65536, 65537, 70001])
+def test_banks_of_more_rows_than_entries(n, kind):
+    """Zeroed beside the sort: of one workgroup, of up to 64 tiles, of more."""
+    lookup_case(n, n, 4, kind, out=torch.bfloat16)
+    lookup_case(n, n + 77777, 9 if n < 20000 else 2, kind, bank=torch.bfloat16, index=torch.int32)
+
+
+@pytest.mark.parametrize("kind", ["even", "skewed", "one"])
+@pytest.mark.parametrize("n", [65537, 131072, 140001, 300000])
+def test_more_entries_than_rows(n, kind):
+    lookup_case(n, 5000, 4, kind)
+    lookup_case(n, 300, 5, kind, add=True, exactly=kind != "one")
+
+
+@pytest.mark.parametrize("n", [16 * 64 - 1, 16 * 64, 16 * 64 + 1, 16 * 65, 16 * 130 + 5, 16 * 1100])
+@pytest.mark.parametrize("before", [0, 1, 15, 16, 17, 500])
+def test_runs_over_many_blocks(n, before):
+    """A run that begins anywhere in a block and goes on over windows of 64 of them, with other runs around it."""
+    idx = torch.cat([torch.zeros(before, dtype=torch.int64), torch.full((n,), 5), torch.arange(6, 40), torch.full((300,), 41)])
+    dout = whole((len(idx), 4), 3)
+    for slots in (42, 100000):
+        want = torch.zeros((slots, 4), dtype=torch.float64).index_add_(0, idx, dout.double())
+        for add in (False, True):
+            dbank = torch.full((slots, 4), 2.0, device=DEV)
+            got = sdm.sdm_lookup_grad(idx.to(DEV), dout.to(DEV), slots, dbank=dbank, accumulate=add)
+            assert torch.equal(got.double().cpu(), want + 2 if add else want)
+
+
+@pytest.mark.parametrize("add", [False, True], ids=["write", "add"])
+@pytest.mark.parametrize("hd,bank", [(64, torch.float32), (128, torch.float32), (256, torch.float32), (1000, torch.float32),
+                                     (129, torch.float32), (128, torch.bfloat16), (512, torch.bfloat16)])
+def test_columns_in_slices(hd, bank, add):
+    """dout larger than an L2 cache: a row's columns on two, four and eight XCDs."""
+    g = torch.Generator(device=DEV).manual_seed(1)
+    T, W, slots = (8 << 20) // hd // 2, 8, 3000
+    idx = torch.randint(0, slots, (2, T, W), generator=g, device=DEV)
+    idx[0, ::5] = 7
+    w = torch.randint(-1, 2, (2, T, W), generator=g, device=DEV).float()
+    dout = torch.randint(-1, 2, (2, T, hd), generator=g, device=DEV).float()
+    dbank = torch.ones((slots, hd), dtype=bank, device=DEV)
+    got = sdm.sdm_gather_bank_grad(idx[0], w[0], dout[0], slots, chunk=T, valid=T - 3, idx1=idx[1], w1=w[1], dout1=dout[1],
+                                   dbank=dbank, accumulate=add)
+    want = torch.full((slots, hd), float(add), dtype=torch.float64, device=DEV)
+    for o in range(2):
+        for c in range(W):
+            want.index_add_(0, idx[o, :T - 3, c], (w[o, :T - 3, c, None] * dout[o, :T - 3]).double())
+    assert torch.equal(got.double(), want.to(bank).double())
+
+
 @pytest.mark.parametrize("out", BOTH, ids=["dout-f32", "dout-bf16"])
 @pytest.mark.parametrize("hd", [5, 8, 64, 136])
 @pytest.mark.parametrize("p", [0.1, 0.5])
