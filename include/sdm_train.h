@@ -173,7 +173,7 @@ int sdm_lookup_grad(int64_t n, const void* idx, int idx_dtype, const void* dout,
  *
  *     dbank_s = sum_{(o, t, n) : idx_o[t,n] = s} w_o[t,n] dout_o[t]    (or dbank_s + that)
  * over the live tokens t of sdm_gather (or sdm_gather_packed's values) with the same slots
- * and weights; padding tokens' slots, weights and dout are not read. Sums are float32,
+ * and weights; padding tokens' slots and weights may hold anything, their dout is not read. Sums are float32,
  * fused multiply-adds over the entries of a slot in ascending order (o, t, n), in runs as
  * in sdm_lookup_grad; the result is rounded once to bank_dtype.
  *

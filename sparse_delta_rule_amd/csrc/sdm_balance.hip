@@ -223,7 +223,7 @@ constexpr int kCountKeys = 16384;  // keys counted in LDS at a time
 // terms have an offset of their own, so a row needs one barrier. Rows of more than 32768 keys are
 // taken in parts, which are read again for their shares: a lane's 64 keys and 64 sums do not fit its
 // registers (1024 rows of 65536 bfloat16 keys: 228 us with both there, 194 in parts). 4096 rows of
-// 16384 bfloat16 keys take 36 us, 3.7 TB/s: the instructions (200 for a wavefront's part of a row)
+// 16384 bfloat16 keys take 35 us, 3.9 TB/s: the instructions (200 for a wavefront's part of a row)
 // are 24 us of it, one barrier a row with 16 wavefronts a compute unit the rest.
 template <typename E, int THREADS, int VPT, int PARTS, bool VEC>
 __global__ __launch_bounds__(THREADS) void balance_big_kernel(BalanceParams p) {
@@ -560,7 +560,7 @@ __device__ __forceinline__ float count_of_largest(const float (&e)[VPT], const f
     return top;
 }
 
-// 32768 x 256 float32 keys: 14.6 us, 4.3 TB/s of live rows read and rows written.
+// 32768 x 256 float32 keys: 15 us, 4.4 TB/s of live rows read and rows written.
 template <typename E, int LANES, int VPT, bool VEC>
 __global__ __launch_bounds__(kSmallThreads) void balance_backward_small_kernel(BalanceParams p) {
     using Row = RowKeys<E, LANES, VPT, VEC>;
@@ -606,7 +606,7 @@ __global__ __launch_bounds__(kSmallThreads) void balance_backward_small_kernel(B
     }
 }
 
-// A row at a time, the counts in registers. 4096 rows of 16384 bfloat16 keys: 61 us, 4.4 TB/s read
+// A row at a time, the counts in registers. 4096 rows of 16384 bfloat16 keys: 59 us, 4.5 TB/s read
 // and written, with 41 us of instructions.
 template <typename E, int THREADS, int VPT, bool VEC>
 __global__ __launch_bounds__(THREADS) void balance_backward_big_kernel(BalanceParams p) {

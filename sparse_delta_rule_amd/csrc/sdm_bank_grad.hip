@@ -462,8 +462,8 @@ template <typename D, typename E, bool VEC, bool WEIGHTS, bool DROP> struct Sums
 };
 
 // The grid of the sums, workgroups in eights, one on each XCD: `sums` eights for the blocks of entries,
-// then `rows` eights for the bank's rows. (Taken in turn, the blocks' workgroups, most of which end
-// at once, left the rows' to half of the compute units.)
+// then `rows` eights for the bank's rows. (With the blocks' workgroups, most of which end at once, and
+// the rows' taken in turn, 2.35 M entries of 2^21 x 128 took 459 us instead of 332.)
 struct SumGrid {
     int lanes, slices, shift;  // lanes of a group; groups that share a row's columns; log2 of p.block
     uint32_t ranges;           // workgroups of a slice, for the blocks
@@ -494,9 +494,9 @@ __device__ __forceinline__ uint32_t lower_bound(const Record* records, uint32_t 
 // A workgroup takes neighbouring rows of the bank and writes each: the sum of its entries, or 0. So
 // the bank is written once and in order. Rows of long runs are left to the blocks' sums.
 // Bound by what leaves and enters the L2 caches: 3.1 M entries (2.35 M that count) of 2^21 x 128
-// float32 in 330 us, 1.07 GB written and 0.56 GB fetched (5.0 TB/s). Without slices of the columns
-// 375 us (dout comes from the Infinity Cache, 25 MB against an L2 of 4), with slices of 64 bytes, half
-// lines of the bank, 540; the sums of the entries' rows alone and the zeros in a pass of its own 342.
+// float32 in 332 us, 1.07 GB written and 0.59 GB or more fetched (reads are counted as 64 bytes
+// each), at least 5.0 TB/s. Without slices of the columns 376 us, 0.82 GB: 41% of the L2's accesses
+// hit, 54% with four slices. The entries' rows first and the zeros in a pass of its own 342.
 template <typename S>
 __device__ __forceinline__ void sum_rows(const S& s, const SumGrid& g, uint32_t range, uint32_t* lds) {
     constexpr int N = S::N;
@@ -830,8 +830,9 @@ bool by_rows(const BankGradParams& p) { return !p.add && p.entries > p.num_slots
 SumGrid sum_grid(const BankGradParams& p, int dout_size, int bank_size) {
     const int n = 16 / dout_size, vecs = (p.hd + n - 1) / n;
     SumGrid g{};
-    // A gather reads each token's dout once for every entry: slices of the columns, so that what the
-    // entries read of them nearly fits an XCD's 4 MB of L2, but of whole 128-byte lines of dbank.
+    // A gather reads each token's dout once for every entry: slices of the columns, so that an XCD's 4 MB
+    // of L2 hold more of what its entries read, but of whole 128-byte lines of dbank (c3's entries: the
+    // call 490 us with one slice, 471 with two, 440 with four, 609 with eight).
     g.slices = 1;
     const int64_t bytes = (p.width[1] != 0 ? 2 : 1) * int64_t(p.tokens) * p.hd * dout_size;
     if (p.width[0] + p.width[1] >= 8)

@@ -33,8 +33,8 @@ template <> struct OctetOf<SDM_MX8, 16> : PackedOctet<false> {};
 template <> struct OctetOf<SDM_MX4, 16> : PackedOctet<true> {};
 
 // A thread takes eight columns of ROWS rows, a row's threads are neighbours. Bound by its memory
-// traffic: 32768 rows of 1024 bfloat16 with dropout in 20 us, 5.8 TB/s of different rows read and of
-// rows written; the ten rounds of the generator, one run for eight columns, hide behind it. A launch
+// traffic: 32768 rows of 1024 bfloat16 with dropout in 20 us, 5.1 TB/s of rows fetched (each by
+// the XCDs that read it) and written; the ten rounds of the generator, one run for eight columns, hide behind it. A launch
 // of few rows is bound by two dependent loads (64 rows: 2.6 us).
 template <int KIND, int VB, typename E, int OVB, bool DROP, int ROWS>
 __global__ __launch_bounds__(kThreads) void lookup_kernel(LookupParams p) {
