@@ -34,6 +34,7 @@ extern "C" {
 
 #define SDM_MAX_GRAD_ENTRIES 0x7fffffffLL /* most entries, and most slots, of a gradient to a bank */
 #define SDM_MAX_LOOKUP_ROWS 0x7fffffffLL  /* most rows of a lookup */
+/* Lookups and gradients to a bank take rows of at most 65535 * 256 columns. */
 
 /* What a gradient to a bank does with dbank. */
 enum {

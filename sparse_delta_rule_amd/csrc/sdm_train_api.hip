@@ -15,7 +15,7 @@ using namespace sdm;
 
 using i64 = long long;
 
-constexpr int64_t kMaxColumns = 65535LL * 512;  // column slices of a grid, of 512 columns at the widest
+constexpr int64_t kMaxColumns = 65535LL * 256;  // slices along y of a grid: 256 columns where runs are joined
 constexpr int64_t kMaxGroups = 0xffffffffLL / 256;  // workgroups of 256 threads along one axis
 
 // The workspace is there, large enough and apart from the call's arrays (`read` and `written`

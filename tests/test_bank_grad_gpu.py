@@ -308,6 +308,21 @@ def test_a_bank_past_32_bit_offsets():
 
 
 @pytest.mark.slow
+def test_the_widest_rows():
+    """As many slices of the columns as the last pass's grid holds, and a run over several blocks of entries."""
+    hd, n = 65535 * 256, 40
+    idx = torch.ones(n, dtype=torch.int64, device=DEV)
+    idx[7] = 0
+    dout = (torch.arange(hd, device=DEV) % 5 - 2).to(torch.bfloat16).expand(n, hd).contiguous()
+    got = sdm.sdm_lookup_grad(idx, dout, 3)
+    assert torch.equal(got[0], dout[0].float()) and torch.equal(got[1], 39 * dout[0].float()) and not got[2].any()
+    add = sdm.sdm_lookup_grad(idx, dout, 3, dbank=got.clone(), accumulate=True)
+    assert torch.equal(add, 2 * got)
+    with pytest.raises(sdm.SdmError, match="head_dim must be at most"):
+        sdm.sdm_lookup_grad(idx[:1], torch.zeros((1, hd + 1), device=DEV), 1)
+
+
+@pytest.mark.slow
 def test_many_entries():
     """Several hundred tiles of the sort, both kinds of slots, and a run over thousands of blocks."""
     g = torch.Generator(device=DEV).manual_seed(1)

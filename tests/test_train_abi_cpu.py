@@ -150,6 +150,7 @@ LOOKUP = dict(bank=A, scales=A + 64 * MB, bank_dtype=MX8, num_slots=1000, head_d
     (dict(num_slots=0), E_SHAPE, "empty bank"),
     (dict(head_dim=0), E_SHAPE, "empty bank"),
     (dict(head_dim=1 << 29), E_RANGE, "head_dim must be"),
+    (dict(head_dim=65535 * 256 + 1), E_RANGE, "head_dim must be at most 16776960"),
     (dict(num_slots=1 << 60), E_SHAPE, "overflow"),
     (dict(n=-1), E_SHAPE, "n must be"),
     (dict(n=1 << 31), E_SHAPE, "n must be"),
@@ -191,6 +192,7 @@ GRAD = dict(n=300, idx=A, idx_dtype=I32, dout=A + 64 * MB, dout_dtype=BF16, scal
     (dict(num_slots=0), E_SHAPE, "empty bank"),
     (dict(num_slots=1 << 31), E_RANGE, "at most 2^31 - 1 slots"),
     (dict(head_dim=-1), E_SHAPE, "empty bank"),
+    (dict(head_dim=65535 * 256 + 1, num_slots=2), E_RANGE, "head_dim must be at most 16776960"),
     (dict(mode=2), E_RANGE, "mode must be"),
     (dict(n=-1), E_SHAPE, "n must be"),
     (dict(n=1 << 31), E_SHAPE, "n must be"),
