@@ -135,7 +135,7 @@ int sdm_route_balance_backward(const void* logits, int logit_dtype, int64_t toke
  *               scales (sdm_memory.h).
  *   n           0..SDM_MAX_LOOKUP_ROWS; 0 enqueues nothing.
  *   idx         [n] of idx_dtype SDM_I32 or SDM_I64: any values.
- *   scale       finite. dropout in [0, 1 - 2^-16].
+ *   scale       finite, and so that a is finite. dropout in [0, 1 - 2^-16].
  *   rng         [2] uint64 in device memory (so that a captured call can be replayed
  *               with others); may be NULL where T = 0.
  *   out         [n, head_dim] of out_dtype SDM_F32 or SDM_BF16, written.

@@ -459,6 +459,11 @@ template <typename D, typename E, bool VEC, bool WEIGHTS, bool DROP> struct Sums
         E* row = static_cast<E*>(p.dbank) + int64_t(slot) * p.hd;
         store_columns<E, N, VEC, ADD>(row, c, p.hd, WEIGHTS ? 1.0f : p.factor, acc);
     }
+    __device__ __forceinline__ void zero(uint32_t slot) const {  // no entry names it: +0, whatever the factor's sign
+        float none[N];
+        clear(none);
+        store_columns<E, N, VEC, false>(static_cast<E*>(p.dbank) + int64_t(slot) * p.hd, c, p.hd, 1.0f, none);
+    }
 };
 
 // The grid of the sums, workgroups in eights, one on each XCD: `sums` eights for the blocks of entries,
@@ -541,10 +546,10 @@ __device__ __forceinline__ void sum_rows(const S& s, const SumGrid& g, uint32_t 
         return b - a > uint32_t(p.spill) && (((a >> g.shift) + 1) << g.shift) + uint32_t(p.spill) < b;
     };
     const uint32_t r0 = min(group * g.group_rows, rows), r1 = min(r0 + g.group_rows, rows);
+    for (uint32_t r = r0; r < r1; ++r)
+        if (starts[r] == starts[r + 1]) s.zero(uint32_t(first) + r);
     float acc[N];
     s.clear(acc);
-    for (uint32_t r = r0; r < r1; ++r)
-        if (starts[r] == starts[r + 1]) s.template finish<false>(uint32_t(first) + r, acc);
     for (uint32_t r = r0; r < r1;) {
         if (is_long(r)) {
             ++r;

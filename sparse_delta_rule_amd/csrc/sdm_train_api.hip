@@ -72,6 +72,9 @@ int check_dropout(const char* fn, float scale, float dropout, const uint64_t* rn
         return fail(SDM_E_RANGE, "%s: dropout must be in [0, 1 - 2^-16], got %g", fn, double(dropout));
     *threshold = uint32_t(nearbyint(double(dropout) * 65536.0));
     *factor = float(double(scale) * 65536.0 / (65536.0 - double(*threshold)));
+    if (!std::isfinite(*factor))
+        return fail(SDM_E_RANGE, "%s: scale / (1 - dropout) must be finite in float32, got %g / (1 - %g)", fn, double(scale),
+                    double(dropout));
     if (*threshold != 0 && run && rng == nullptr) return fail(SDM_E_NULL, "%s: dropout needs rng", fn);
     if (!aligned(rng, 8)) return fail(SDM_E_ALIGN, "%s: rng must be 8-byte aligned", fn);
     return SDM_OK;

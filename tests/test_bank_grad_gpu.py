@@ -168,6 +168,18 @@ def test_dropped_columns_and_rows_outside_are_not_counted_whatever_they_hold():
     assert torch.isnan(got[1]).any() and torch.equal(got[[0, 2, 3, 4]], want[[0, 2, 3, 4]])
 
 
+@pytest.mark.parametrize("bank", BOTH, ids=["f32", "bf16"])
+@pytest.mark.parametrize("slots", [40, 4000])  # fewer rows than entries, and more
+def test_rows_that_no_entry_names_are_plus_zero(slots, bank):
+    """Also where the factor is negative, or the largest that float32 holds."""
+    idx = (torch.arange(300) % 20).to(DEV)
+    for scale in (-1.0, 3e38, -3e38):
+        for hd in (16, 33):
+            dout = torch.zeros((300, hd), device=DEV)
+            got = sdm.sdm_lookup_grad(idx, dout, slots, scale=scale, bank_dtype=bank)
+            assert not got.any() and not torch.signbit(got[20:]).any()
+
+
 @pytest.mark.parametrize("n", [0, 3])
 def test_nothing_to_add(n):
     idx, dout = torch.full((n,), -1, device=DEV), torch.ones((n, 9), device=DEV)

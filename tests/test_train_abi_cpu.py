@@ -217,6 +217,14 @@ def test_lookup_grad_rejects(kw, code, msg):
     rejects("sdm_lookup_grad", GRAD, kw, code, msg)
 
 
+@pytest.mark.parametrize("scale,dropout,ok", [(3e38, 0.5, False), (-3e38, 0.2, False), (6e33, 1 - 2.0 ** -16, False),
+                                              (3e38, 0.0, True), (1.5e38, 0.5, True), (5e33, 1 - 2.0 ** -16, True)])
+def test_a_factor_past_float32_is_refused(scale, dropout, ok):
+    """scale / (1 - dropout); a call that passes this check stops at the pointer that it lacks."""
+    for fn, args in (("sdm_lookup", with_changes(LOOKUP, dict(bank=None))), ("sdm_lookup_grad", with_changes(GRAD, dict(dout=None)))):
+        rejects(fn, args, dict(scale=scale, dropout=dropout), *((E_NULL, "required") if ok else (E_RANGE, "finite in float32")))
+
+
 def test_lookup_grad_of_nothing():
     assert call("sdm_lookup_grad", with_changes(GRAD, dict(n=0, mode=1, idx=None, dout=None, dbank=None, rng=None))) == (OK, "")
 
