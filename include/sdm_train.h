@@ -97,8 +97,10 @@ int64_t sdm_route_balance_workspace(int64_t tokens, int64_t keys, int64_t chunk,
  *     dlogits = d,  or dlogits + d (accumulate)
  * Counts are taken relative to their mean, or in a row where one key has more than 4/5 of
  * the share to that key's count (p sums to 1, so that a constant changes nothing): there
- * nothing cancels, however far that key is above the rest. Differences below 2^24 are
- * exact, the rest is float32; the sum is rounded once to the logits' type.
+ * nothing cancels, however far that key is above the rest. A row's gradient depends on no
+ * other row. A count's difference to the mean is rounded to float32, exact below 2^24, and a
+ * difference to a key's count is that of two of those; the rest is float32, and the sum is
+ * rounded once to the logits' type.
  *
  * Arguments: as sdm_route_balance, with
  *   counts, coef  [sequences, keys] and [sequences].

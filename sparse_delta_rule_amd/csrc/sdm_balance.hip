@@ -103,18 +103,24 @@ template <int LANES, typename T, typename F> __device__ __forceinline__ T reduce
     return v;
 }
 
+// What holds for all lanes of a row or for none: a branch of the wavefront where that is the row's. (Of
+// more rows it is not: a row's path, and so its bits, would be its neighbours'.)
+template <int LANES> __device__ __forceinline__ bool all_of(bool holds) {
+    return LANES == 64 ? __ballot(!holds) == 0 : holds;
+}
+
 // The terms of one lane's keys, c[i] -> e_i, given the largest of the part's logits; returns the
 // offset. scale: what every e_i is to be multiplied by to be relative to that offset: an exponential
 // by one fused operation, 2^(x L - q) with q = o L rounded, has what q's rounding puts into all of
 // them, 2^(o L - q), taken out there. rest (may be NULL): 1 - s_i of a sigmoid, for positive x the
 // exponential's own share, so that it is as precise as s_i is for negative x.
-template <int N>
+template <int LANES, int N>
 __device__ __forceinline__ float terms(int score, float largest, float (&c)[N], float* rest, float& scale) {
     constexpr float kL = 1.44269504f;
     scale = 1.0f;
     if (score == SDM_SOFTMAX) {
         const float o = max32(largest, -FLT_MAX);
-        if (__ballot(!(fabsf(o) < 65536.0f)) == 0) {
+        if (all_of<LANES>(fabsf(o) < 65536.0f)) {
             const float q = o * kL;
 #pragma unroll
             for (int i = 0; i < N; ++i) c[i] = __builtin_amdgcn_exp2f(fmaf(c[i], kL, -q));
@@ -199,7 +205,7 @@ __global__ __launch_bounds__(kSmallThreads) void balance_small_kernel(BalancePar
         load(t + 2 * kRows, next[1]);
         const float largest = reduce<LANES>(max_of(c, -INFINITY), larger);
         float scale;  // of all of the row's terms
-        terms(p.score, largest, c, nullptr, scale);
+        terms<LANES>(p.score, largest, c, nullptr, scale);
         const float sum = reduce<LANES>(sum_of(c), plus);
         const float f = sum > 0 && t < r.end && is_live(p, t) ? 1.0f / sum : 0.0f;
 #pragma unroll
@@ -272,7 +278,7 @@ __global__ __launch_bounds__(THREADS) void balance_big_kernel(BalanceParams p) {
                 next.load(row + h * kPart, p.keys - h * kPart, tid);
                 next.values(p.keys - h * kPart, tid, c);
             }
-            o = terms(p.score, reduce<64>(max_of(c, -INFINITY), larger), c, nullptr, scale);
+            o = terms<64>(p.score, reduce<64>(max_of(c, -INFINITY), larger), c, nullptr, scale);
         };
         float mine = -FLT_MAX, its = 0;
 #pragma unroll 1
@@ -521,11 +527,11 @@ template <int N> __device__ __forceinline__ float dot_of(const float (&e)[N], co
 }
 
 // A lane's gradients, e[i] -> e_i share ((c_i - top) - d) f, and for a sigmoid times 1 - s_i.
-template <int N>
+template <int LANES, int N>
 __device__ __forceinline__ void gradients(int score, const float (&rest)[N], const float (&c)[N], float top, float share, float d,
                                           float f, float (&e)[N]) {
     const float k = share * f;
-    if (__ballot(!(fabsf(k) < INFINITY && fabsf(d) < INFINITY)) != 0) {  // a key of score 0 has the gradient 0 all the same
+    if (!all_of<LANES>(fabsf(k) < INFINITY && fabsf(d) < INFINITY)) {  // a key of score 0 has the gradient 0 all the same
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const float s = e[i] * share, v = s * ((c[i] - top) - d) * f * (score == SDM_SIGMOID ? rest[i] : 1.0f);
@@ -591,16 +597,18 @@ __global__ __launch_bounds__(kSmallThreads) void balance_backward_small_kernel(B
         next[0] = next[1];
         load(t + 2 * kRows, next[1]);
         const float largest = reduce<LANES>(max_of(e, -INFINITY), larger);
-        const float o = terms(p.score, largest, e, rest, scale);
+        const float o = terms<LANES>(p.score, largest, e, rest, scale);
         const float z = reduce<LANES>(sum_of(e), plus);
         const float share = z > 0 && live ? 1.0f / z : 0.0f;
         float top = 0;
-        if (__ballot(share * largest_term(p.score, largest, o) > kMostShare) != 0) {
+        const bool confident = share * largest_term(p.score, largest, o) > kMostShare;
+        if (__ballot(confident) != 0) {  // of any row of the wavefront; the others keep the mean
             const float most = reduce<LANES>(max_of(e, 0.0f), larger);
-            top = reduce<LANES>(count_of_largest<Row>(e, c, most, p.keys, lane), larger);
+            const float its = reduce<LANES>(count_of_largest<Row>(e, c, most, p.keys, lane), larger);
+            top = confident ? its : 0.0f;
         }
         const float d = reduce<LANES>(dot_of(e, c, top), plus);
-        gradients(p.score, rest, c, top, share, d * share, f, e);
+        gradients<LANES>(p.score, rest, c, top, share, d * share, f, e);
         if (there && (live || !p.accumulate))
             store_row<E, Row, VPT, VEC>(dlogits + int64_t(t) * p.keys, p.keys, lane, e, p.accumulate);
     }
@@ -655,7 +663,7 @@ __global__ __launch_bounds__(THREADS) void balance_backward_big_kernel(BalancePa
             next.values(p.keys, tid, e);
         }
         const float largest = reduce<64>(max_of(e, -INFINITY), larger);
-        const float o = terms(p.score, largest, e, rest, scale);
+        const float o = terms<64>(p.score, largest, e, rest, scale);
         const float mine = reduce<64>(sum_of(e), plus) * scale, its_dot = reduce<64>(dot_of(e, c, 0.0f), plus) * scale;
         if (lane == 0) {
             offset[buffer][wave] = o;
@@ -686,7 +694,7 @@ __global__ __launch_bounds__(THREADS) void balance_backward_big_kernel(BalancePa
             __syncthreads();
             d = lanes_reduce<16>(lane % 16 < kWaves ? again[1][w] : 0.0f, plus);
         }
-        gradients(p.score, rest, c, top, share * own, d * share, f, e);
+        gradients<64>(p.score, rest, c, top, share * own, d * share, f, e);
         store_row<E, Row, VPT, VEC>(out, p.keys, tid, e, p.accumulate);
         buffer ^= 1;
     }
@@ -750,7 +758,7 @@ __global__ __launch_bounds__(THREADS) void balance_backward_long_kernel(BalanceP
             next.values(p.keys - h * kPart, tid, e);
             load_part(h);
             largest = reduce<64>(max_of(e, -INFINITY), larger);
-            o = terms(p.score, largest, e, rest, scale);
+            o = terms<64>(p.score, largest, e, rest, scale);
         };
         float mine = -FLT_MAX, its_total = 0, its_dot = 0, its_term = 0;
 #pragma unroll 1
@@ -805,7 +813,7 @@ __global__ __launch_bounds__(THREADS) void balance_backward_long_kernel(BalanceP
 #pragma unroll 1
         for (int h = 0; h < PARTS; ++h) {
             take(h);
-            gradients(p.score, rest, c, top, share * scale * exp32(o - most), d * share, f, e);
+            gradients<64>(p.score, rest, c, top, share * scale * exp32(o - most), d * share, f, e);
             store_row<E, Row, VPT, VEC>(out + h * kPart, p.keys - h * kPart, tid, e, p.accumulate);
         }
         buffer ^= 1;

@@ -259,6 +259,26 @@ def test_gradients_that_are_not_finite_stay_in_their_rows():
     assert torch.isfinite(sdm.sdm_route_balance_backward(x.to(DEV), counts, coef, chunk=5, per_chunk=True)).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("N", [8, 100, 200, 400, 1000, 3000])
+def test_a_rows_gradient_is_its_own(N, score, dtype):
+    """The same bits whatever the rows beside it hold: a key above the rest, none, very large ones, very small scores."""
+    T = 4096  # eight rows and more of a workgroup
+    x = logits_like(N, T, N, torch.float32, 0.5)
+    counts = torch.randint(0, 50, (1, N), generator=torch.Generator().manual_seed(1), dtype=torch.int32)
+    counts[0, N // 2] = 1 << 20
+    beside = x.clone()
+    beside[1::6], beside[3::6], beside[5::6] = 0.0, 3e30, -63.9  # every other row; e^63.9 times dloss passes float32
+    beside[1::6, N // 3] = 12.0 + np.log(N)
+    beside[51] = -INF
+    coef, dloss = torch.ones(1, device=DEV), torch.tensor(1e15, device=DEV)
+    for add in (False, True):
+        got = [sdm.sdm_route_balance_backward(v.to(dtype).to(DEV), counts.to(DEV), coef, dloss=dloss, score=score,
+                                              dlogits=torch.zeros((T, N), dtype=dtype, device=DEV), accumulate=add)[::2] for v in (x, beside)]
+        assert torch.isfinite(got[0]).all() and got[0].any() and torch.equal(*got)
+
+
 def test_given_outputs_and_workspace_and_repeats():
     x, idx = logits_like(1, 3000, 300).to(DEV), choices(2, 3000, 300, 8).to(DEV)
     first = sdm.sdm_route_balance(x, idx, scale=0.1)
