@@ -52,6 +52,8 @@ enum {
  * scores of token t (softmax, or sigmoid; NaN and -inf logits have score 0, +inf counts
  * as the largest float32) and
  *     p_ti = s_ti / sum_i s_ti         (0 in a row whose logits are all NaN or -inf)
+ * (a score below 2^-126 may count as 0; where a row's largest logit is at most -64, its
+ * sigmoid scores are taken relative to the largest, so that this goes by their quotient)
  * the results are
  *     counts_gi = number of (t, j), t live in g, with idx_tj key i of token t
  *     mean_gi   = sum_{t live in g} p_ti / n_g                       (0 where n_g = 0)

@@ -531,10 +531,13 @@ template <int LANES, int N>
 __device__ __forceinline__ void gradients(int score, const float (&rest)[N], const float (&c)[N], float top, float share, float d,
                                           float f, float (&e)[N]) {
     const float k = share * f;
-    if (!all_of<LANES>(fabsf(k) < INFINITY && fabsf(d) < INFINITY)) {  // a key of score 0 has the gradient 0 all the same
+    // Differences of counts are below 2^33, so that a product of k and one is finite. Otherwise a key's own
+    // share comes first, whose product is infinite only where the gradient is; one of score 0 has the
+    // gradient 0 all the same.
+    if (!all_of<LANES>(fabsf(k) < 0x1p90f && fabsf(d) < INFINITY)) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const float s = e[i] * share, v = s * ((c[i] - top) - d) * f * (score == SDM_SIGMOID ? rest[i] : 1.0f);
+            const float s = e[i] * share, v = s * (score == SDM_SIGMOID ? rest[i] : 1.0f) * ((c[i] - top) - d) * f;
             e[i] = s > 0 ? v : 0.0f;
         }
         return;

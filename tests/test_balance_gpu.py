@@ -259,6 +259,36 @@ def test_gradients_that_are_not_finite_stay_in_their_rows():
     assert torch.isfinite(sdm.sdm_route_balance_backward(x.to(DEV), counts, coef, chunk=5, per_chunk=True)).all()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("N", [40, 200, 600, 3000, 20000, 40000])
+def test_gradients_near_the_largest_float32(N, score):
+    """With a factor of 1e35 some gradients are past float32: those are infinite, the others as they are, and a key without a
+    score has none."""
+    x = logits_like(N, 6, N)
+    x[:, ::3] -= 60.0  # shares of 1e-26
+    x[:, 5], x[2], x[3, :] = -INF, -INF, -80.0
+    x[3, 7] = -INF
+    x[1] -= 30.0
+    x[1, 1] = x[1].max() + np.log(N)  # the key of the large count, with half of the share or more
+    counts = torch.randint(0, 50, (1, N), generator=torch.Generator().manual_seed(1), dtype=torch.int32)
+    counts[0, 1] = 1 << 24
+    coef, dloss = torch.tensor([1e5], device=DEV), np.float32(1e30)
+    d = sdm.sdm_route_balance_backward(x.to(DEV), counts.to(DEV), coef, dloss=torch.tensor(float(dloss), device=DEV), score=score)
+    got = d.double().cpu().numpy()
+    want, size = ref.balance_backward(x.numpy(), counts.numpy(), [1e5], dloss=float(dloss), score=score)
+    most = float(torch.finfo(torch.float32).max)
+    # f is rounded twice more here. A score below 2^-126 (a softmax's and a deep sigmoid's relative to the row's
+    # largest) may count as 0: a share of 2^-126 over the row's sum, which is at least its largest score, times a
+    # difference below 2^25.
+    top = x.double().numpy().max(1, keepdims=True)
+    least = 1 / (1 + np.exp(-top)) if score == "sigmoid" else np.ones_like(top)
+    least[top <= -64] = 1
+    bound = size + 4 * 2.0 ** -24 * (np.abs(want) + size) + 2.0 ** -126 / least * 2.0 ** 25 * 1e35
+    inside, past = np.abs(want) + bound < most, np.abs(want) - bound > most
+    assert inside.any() and past.any() and not d[torch.isneginf(x).to(DEV)].any()
+    assert (np.abs(got - want)[inside] <= bound[inside]).all() and (got[past] == np.sign(want[past]) * INF).all()
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("N", [8, 100, 200, 400, 1000, 3000])
