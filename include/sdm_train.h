@@ -137,7 +137,8 @@ int sdm_route_balance_backward(const void* logits, int logit_dtype, int64_t toke
  *   bank        [num_slots, head_dim] of bank_dtype SDM_F32 or SDM_BF16, scales NULL;
  *               or the codes of a packed bank of bank_dtype SDM_MX8 or SDM_MX4 and its
  *               scales (sdm_memory.h).
- *   n           0..SDM_MAX_LOOKUP_ROWS; 0 enqueues nothing.
+ *   n           0..SDM_MAX_LOOKUP_ROWS, and at most 2^28 * max(1, 256 / ceil(head_dim / 8)), the
+ *               quotient rounded down; 0 enqueues nothing.
  *   idx         [n] of idx_dtype SDM_I32 or SDM_I64: any values.
  *   scale       finite, and so that a is finite. dropout in [0, 1 - 2^-16].
  *   rng         [2] uint64 in device memory (so that a captured call can be replayed

@@ -42,7 +42,7 @@ __global__ __launch_bounds__(kThreads) void lookup_kernel(LookupParams p) {
     const int per_row = min(octets, kThreads), rows = kThreads / per_row;
     const int r = int(threadIdx.x) / per_row, o = int(blockIdx.y) * kThreads + int(threadIdx.x) % per_row;
     if (r >= rows || o >= octets) return;
-    const int64_t i0 = int64_t(blockIdx.x) * (rows * ROWS) + r;
+    const int64_t i0 = p.first + int64_t(blockIdx.x) * (rows * ROWS) + r;
     int64_t slot[ROWS];
     float x[ROWS][8];
 #pragma unroll
@@ -69,24 +69,32 @@ __global__ __launch_bounds__(kThreads) void lookup_kernel(LookupParams p) {
 struct LookupGrid {
     int64_t groups;
     int slices, rows;  // rows of a thread
+    int group_rows;
 };
 LookupGrid lookup_grid(const LookupParams& p) {
     const int octets = (p.hd + 7) / 8, rows = kThreads / (octets < kThreads ? octets : kThreads);
-    LookupGrid g{(p.n + rows - 1) / rows, (octets + kThreads - 1) / kThreads, 1};
+    LookupGrid g{(p.n + rows - 1) / rows, (octets + kThreads - 1) / kThreads, 1, rows};
     // Several rows a thread where that leaves 1024 workgroups (32768 x 1024: 20.7 us, with one row a
     // thread 23.4; 65521 rows of 100 4-bit columns: 10.4 us, with one 9.8).
     if (g.groups * g.slices >= 4096) {
         g.rows = 4;
         g.groups = (g.groups + 3) / 4;
+        g.group_rows = 4 * rows;
     }
     return g;
 }
 
-template <int KIND, int VB, typename E, int OVB, bool DROP> void run(const LookupParams& p, hipStream_t stream) {
-    const LookupGrid g = lookup_grid(p);
-    const dim3 grid{unsigned(g.groups), unsigned(g.slices)}, block{kThreads};
-    if (g.rows == 4) hipLaunchKernelGGL((lookup_kernel<KIND, VB, E, OVB, DROP, 4>), grid, block, 0, stream, p);
-    else hipLaunchKernelGGL((lookup_kernel<KIND, VB, E, OVB, DROP, 1>), grid, block, 0, stream, p);
+// Rows past what a grid holds along one axis, 2^32 threads, are a launch of their own.
+constexpr int64_t kMostGroups = 0xffffffffLL / kThreads;
+template <int KIND, int VB, typename E, int OVB, bool DROP> void run(const LookupParams& call, hipStream_t stream) {
+    const LookupGrid g = lookup_grid(call);
+    LookupParams p = call;
+    for (int64_t at = 0; at < g.groups; at += kMostGroups) {
+        const dim3 grid{unsigned(g.groups - at < kMostGroups ? g.groups - at : kMostGroups), unsigned(g.slices)}, block{kThreads};
+        p.first = at * g.group_rows;
+        if (g.rows == 4) hipLaunchKernelGGL((lookup_kernel<KIND, VB, E, OVB, DROP, 4>), grid, block, 0, stream, p);
+        else hipLaunchKernelGGL((lookup_kernel<KIND, VB, E, OVB, DROP, 1>), grid, block, 0, stream, p);
+    }
 }
 
 template <int KIND, int VB, typename E, int OVB> void run_drop(const LookupParams& p, hipStream_t stream) {

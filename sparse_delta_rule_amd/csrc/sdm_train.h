@@ -76,6 +76,7 @@ struct LookupParams {
     const void* bank;
     const uint8_t* scales;
     int64_t num_slots, n;
+    int64_t first;  // of the launch's rows
     int hd;
     int64_t row_bytes;
     int scale_bytes;
@@ -85,7 +86,7 @@ struct LookupParams {
     Dropout dropout;
     void* out;
 };
-int64_t lookup_groups(const LookupParams& p);  // workgroups of the launch along its first axis
+int64_t lookup_groups(const LookupParams& p);  // workgroups for a slice of the columns
 hipError_t launch_lookup(const LookupParams& p, int bank_dtype, bool out_bf16, hipStream_t stream);
 
 // ------------------------------------------------------------------ gradient to a bank

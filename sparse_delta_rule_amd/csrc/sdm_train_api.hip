@@ -17,6 +17,7 @@ using i64 = long long;
 
 constexpr int64_t kMaxColumns = 65535LL * 256;  // slices along y of a grid: 256 columns where runs are joined
 constexpr int64_t kMaxGroups = 0xffffffffLL / 256;  // workgroups of 256 threads along one axis
+constexpr int64_t kMaxLookupGroups = 1LL << 26;  // of a lookup's launches: 288 GiB of 2-byte outputs take 3.8e7 at most
 
 // The workspace is there, large enough and apart from the call's arrays (`read` and `written`
 // hold them; the workspace becomes the last of `written`).
@@ -222,6 +223,9 @@ int sdm_lookup(const void* bank, const void* scales, int bank_dtype, int64_t num
     rc = check_dropout(fn, scale, dropout, rng, n > 0, &p.dropout.threshold, &p.factor);
     if (rc != SDM_OK) return rc;
     if (n == 0) return ok();
+    p.n = n;
+    p.hd = int(head_dim);
+    if (lookup_groups(p) > kMaxLookupGroups) return fail(SDM_E_SHAPE, "%s: %lld rows exceed the grid", fn, (i64)n);
     if (bank == nullptr || (packed && scales == nullptr) || idx == nullptr || out == nullptr)
         return fail(SDM_E_NULL, "%s: the bank, idx and out are required", fn);
     const int is = elem_size(idx_dtype), os = elem_size(out_dtype);
@@ -244,15 +248,12 @@ int sdm_lookup(const void* bank, const void* scales, int bank_dtype, int64_t num
     p.bank = bank;
     p.scales = static_cast<const uint8_t*>(scales);
     p.num_slots = num_slots;
-    p.n = n;
-    p.hd = int(head_dim);
     p.row_bytes = row_bytes;
     p.scale_bytes = int(scale_bytes);
     p.idx = idx;
     p.idx64 = idx_dtype == SDM_I64;
     p.dropout.rng = rng;
     p.out = out;
-    if (lookup_groups(p) > kMaxGroups) return fail(SDM_E_SHAPE, "%s: %lld rows exceed the grid", fn, (i64)n);
     return launched(fn, launch_lookup(p, bank_dtype, out_dtype == SDM_BF16, static_cast<hipStream_t>(hip_stream)));
 }
 

@@ -138,6 +138,26 @@ def test_a_bank_past_32_bit_offsets():
     assert sdm.sdm_lookup(bank, at.to(DEV))[:, 135].tolist() == [1, 2, 3, 4]
 
 
+@pytest.mark.slow
+def test_more_rows_than_a_grid_holds():
+    """70 M rows of 1032 columns, 144 GB: the rows past 2^24 - 1 workgroups of four, too, and their own masks."""
+    n, hd = 70_000_000, 1032
+    bank = torch.arange(1, 4, device=DEV, dtype=torch.bfloat16)[:, None].expand(3, hd).contiguous()
+    idx = (torch.arange(n, device=DEV) % 4).to(torch.int32)  # a fourth of them none
+    out = sdm.sdm_lookup(bank, idx)
+    assert out.shape == (n, hd)
+    for a in range(0, n, 1 << 22):
+        rows, at = out[a:a + (1 << 22)], idx[a:a + (1 << 22)]
+        assert (rows == torch.where(at < 3, at + 1, 0).to(torch.bfloat16)[:, None]).all()
+    rng = rng_of(5, 6)
+    sdm.sdm_lookup(bank, idx, dropout=0.5, rng=rng.to(DEV), out=out)
+    edge = 4 * ((1 << 24) - 1)
+    for i in (0, edge - 1, edge, edge + 6, n - 3):
+        keep = torch.tensor([[w >> 16 * (j % 2) & 0xffff for j in range(8) for w in [ref.philox((o, i, 6, 0), (5, 0))[j // 2]]]
+                             for o in range(hd // 8)]).flatten() >= 1 << 15
+        assert torch.equal(out[i].cpu().float(), torch.where(keep, 2.0 * (i % 4 + 1), 0.0) * (i % 4 < 3)), i
+
+
 def test_refusals():
     bank, idx = torch.ones((4, 8), device=DEV), torch.zeros(3, dtype=torch.int64, device=DEV)
     with pytest.raises(sdm.SdmError, match="needs rng"):

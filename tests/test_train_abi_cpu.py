@@ -176,6 +176,15 @@ def test_lookup_rejects(kw, code, msg):
     rejects("sdm_lookup", LOOKUP, kw, code, msg)
 
 
+@pytest.mark.parametrize("head_dim", [513, 1024, 1025, 1032, 5000])
+def test_rows_of_a_lookup(head_dim):
+    """As many as the header says, and one more; the call stops at the shared memory that it finds, or at the grid."""
+    most = (1 << 28) * max(1, 256 // -(-head_dim // 8))
+    args = with_changes(LOOKUP, dict(bank_dtype=BF16, scales=None, head_dim=head_dim, idx=A + (1 << 50), out=A))
+    rejects("sdm_lookup", args, dict(n=most), E_OVERLAP, "out and bank")
+    rejects("sdm_lookup", args, dict(n=most + 1, out=A + (1 << 51)), E_SHAPE, "exceed the grid")
+
+
 def test_lookup_of_nothing():
     assert call("sdm_lookup", with_changes(LOOKUP, dict(n=0, bank=None, idx=None, out=None, rng=None))) == (OK, "")
 
