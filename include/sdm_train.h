@@ -167,6 +167,7 @@ int sdm_lookup(const void* bank, const void* scales, int bank_dtype, int64_t num
  *   dout        [n, head_dim] of dout_dtype SDM_F32 or SDM_BF16.
  *   dbank       [num_slots, head_dim] of bank_dtype SDM_F32 or SDM_BF16; mode one of
  *               SDM_GRAD_*. Must not overlap an input.
+ *               (SDM_GRAD_WRITE into more than 2^38 - 2^17 bytes may be refused.)
  *   workspace   of sdm_bank_grad_workspace(n, num_slots, head_dim) bytes.
  * Errors: as sdm_route_balance.
  */
@@ -197,7 +198,11 @@ int sdm_gather_bank_grad(int64_t tokens, int64_t chunk, int64_t valid, const int
                          int bank_dtype, int64_t num_slots, int64_t head_dim, int mode, void* workspace,
                          int64_t workspace_bytes, void* hip_stream);
 
-/* Bytes of the workspace of a gradient to a bank; 0 for sizes that the calls refuse. */
+/*
+ * Bytes of the workspace of a gradient to a bank: at most 27 an entry, and 1 GiB or 16 an
+ * entry, whichever is more, for sums of runs, and a MiB. 0 where one of the three is outside
+ * its range.
+ */
 int64_t sdm_bank_grad_workspace(int64_t entries, int64_t num_slots, int64_t head_dim);
 
 #ifdef __cplusplus

@@ -15,6 +15,14 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Columns are summed in turns, which use the same memory, where the sums of blocks would take more than
+// this: up to hd / 4 bytes an entry, far more than dout where its tokens have many entries (32768 tokens of
+// 512 x 8192: 1.5 GB of workspace, at once 34.8). A turn reads the entries again, 12 bytes for 256 or more
+// of dout, and finds more of its columns in the caches (8192 tokens of 256 x 8192 into 32768 slots, four
+// turns: 10.4 ms, at once 11.2).
+constexpr int64_t kTurnBytes = 1LL << 30;
+constexpr int kMinTurn = 64;  // columns: whole lines of dout and of dbank
+
 // ------------------------------------------------------------------ entries
 
 constexpr uint32_t kNone = 0xffffffffu;
@@ -429,7 +437,7 @@ template <typename D, typename E, bool VEC, bool WEIGHTS, bool DROP> struct Sums
         records = p.records[last];
         weights = p.weights[last];
         n = *p.n;
-        c = (int(slice) * lanes + lane) * N;
+        c = (p.line * (kMinTurn / N) + int(slice) * lanes + lane) * N;  // a multiple of N that the compiler sees
         key = {};
         if (DROP) key = philox_key(p.dropout);
     }
@@ -539,7 +547,7 @@ __device__ __forceinline__ void sum_rows(const S& s, const SumGrid& g, uint32_t 
         }
     }
     __syncthreads();
-    if (s.c >= p.hd) return;
+    if (s.c >= p.columns) return;
     const bool staged = count <= kStaged;
     auto is_long = [&](uint32_t r) {
         const uint32_t a = lo + starts[r], b = lo + starts[r + 1];
@@ -612,7 +620,6 @@ __device__ __forceinline__ void sum_blocks(const S& s, const SumGrid& g, uint32_
     constexpr bool ALL = MODE != kByRows;
     const BankGradParams& p = s.p;
     const int groups = kThreads / g.lanes, group = int(threadIdx.x) / g.lanes;
-    const int columns = (p.hd + 7) / 8 * 8;
     const uint64_t range = uint64_t(groups) * p.block, start = range_number * range;
     const uint32_t n = s.n;
     if (start >= n) return;
@@ -635,7 +642,7 @@ __device__ __forceinline__ void sum_blocks(const S& s, const SumGrid& g, uint32_
     __syncthreads();
     const uint32_t b = range_number * groups + group;
     const uint64_t begin = uint64_t(b) * p.block;
-    if (begin >= n || s.c >= p.hd) return;
+    if (begin >= n || s.c >= p.columns) return;
     auto slot_of_sorted = [&](uint64_t i) { return slots[place(int(i + 1 - start))]; };
     const bool from_before = cont(p, slot_of_sorted, n, begin), goes_on = cont(p, slot_of_sorted, n, begin + p.block);
     int at = int(begin + 1 - start), end = min(at + p.block, there);
@@ -664,10 +671,10 @@ __device__ __forceinline__ void sum_blocks(const S& s, const SumGrid& g, uint32_
                 const uint32_t next = is_last ? kNone : slots[place(at + u + 1)];
                 if (next != slot) {
                     if (open || (is_last && goes_on)) {
-                        float* to = (open ? p.first : p.last) + int64_t(b) * columns;
+                        float* to = (open ? p.first : p.last) + int64_t(b) * p.turn + (s.c - p.line * kMinTurn);
 #pragma unroll
                         for (int j = 0; j < N; j += 4)
-                            *reinterpret_cast<float4*>(to + s.c + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+                            *reinterpret_cast<float4*>(to + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
                     } else {
                         s.template finish<MODE == kAdd>(slot, acc);
                     }
@@ -725,8 +732,8 @@ template <typename E, bool VEC, bool ADD> __global__ __launch_bounds__(kJoinThre
     __shared__ uint32_t slots[64];  // of the blocks' last entries
     __shared__ float sums[kJoinThreads][N];
     const int tid = threadIdx.x, groups = kJoinThreads / lanes, lane = tid % lanes, group = tid / lanes;
-    const int c0 = (int(blockIdx.y) * lanes + lane) * N;
-    const int64_t columns = (p.hd + 7) / 8 * 8;
+    const int at0 = (int(blockIdx.y) * lanes + lane) * N, c0 = p.line * kMinTurn + at0;  // of the turn, and of the row
+    const int64_t columns = p.turn;
     const Record* records = p.records[(p.passes - 1) & 1];
     const uint32_t n = *p.n;
     const uint32_t b0 = blockIdx.x * uint32_t(kJoinBlocks);
@@ -756,7 +763,7 @@ template <typename E, bool VEC, bool ADD> __global__ __launch_bounds__(kJoinThre
             float x[kFlight][N];
 #pragma unroll
             for (int u = 0; u < kFlight; ++u)
-                load_columns<float, N, true>(p.first + (int64_t(b) + 1 + min(c + u * stride, more - 1)) * columns, c0, p.hd, x[u]);
+                load_columns<float, N, true>(p.first + (int64_t(b) + 1 + min(c + u * stride, more - 1)) * columns, at0, p.turn, x[u]);
 #pragma unroll
             for (int u = 0; u < kFlight; ++u)
                 if (c + u * stride < more)
@@ -779,9 +786,9 @@ template <typename E, bool VEC, bool ADD> __global__ __launch_bounds__(kJoinThre
         if (turn % groups != group) continue;
         const int i = __ffsll(static_cast<unsigned long long>(left)) - 1;
         const uint32_t b = b0 + uint32_t(i), more = known(i);
-        if (more > kShort || i + more > 64 || c0 >= p.hd) continue;
+        if (more > kShort || i + more > 64 || c0 >= p.columns) continue;
         float acc[N];
-        load_columns<float, N, true>(p.last + b * columns, c0, p.hd, acc);
+        load_columns<float, N, true>(p.last + b * columns, at0, p.turn, acc);
         add(acc, b, 0, more, 1);
         finish(slots[i], acc);
     }
@@ -800,13 +807,13 @@ template <typename E, bool VEC, bool ADD> __global__ __launch_bounds__(kJoinThre
             } while (found == kJoinThreads);
         }
         float acc[N] = {};
-        if (c0 < p.hd) {
-            if (group == 0) load_columns<float, N, true>(p.last + b * columns, c0, p.hd, acc);
+        if (c0 < p.columns) {
+            if (group == 0) load_columns<float, N, true>(p.last + b * columns, at0, p.turn, acc);
             add(acc, b, group, more, groups);
         }
         *reinterpret_cast<float4*>(sums[tid]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
         __syncthreads();
-        if (group == 0 && c0 < p.hd) {
+        if (group == 0 && c0 < p.columns) {
             for (int g = 1; g < min(groups, int(min(more, uint32_t(kJoinThreads)))); ++g) {
 #pragma unroll
                 for (int j = 0; j < N; ++j) acc[j] += sums[g * lanes + lane][j];
@@ -833,15 +840,15 @@ int log2_of(int v) {
 bool by_rows(const BankGradParams& p) { return !p.add && p.entries > p.num_slots; }
 
 SumGrid sum_grid(const BankGradParams& p, int dout_size, int bank_size) {
-    const int n = 16 / dout_size, vecs = (p.hd + n - 1) / n;
+    const int width = p.columns - p.line * kMinTurn, n = 16 / dout_size, vecs = (width + n - 1) / n;
     SumGrid g{};
     // A gather reads each token's dout once for every entry: slices of the columns, so that an XCD's 4 MB
     // of L2 hold more of what its entries read, but of whole 128-byte lines of dbank (c3's entries: the
     // call 490 us with one slice, 471 with two, 440 with four, 609 with eight).
     g.slices = 1;
-    const int64_t bytes = (p.width[1] != 0 ? 2 : 1) * int64_t(p.tokens) * p.hd * dout_size;
+    const int64_t bytes = (p.width[1] != 0 ? 2 : 1) * int64_t(p.tokens) * width * dout_size;
     if (p.width[0] + p.width[1] >= 8)
-        while (g.slices < 8 && bytes / g.slices > (3 << 20) && p.hd * bank_size / g.slices >= 256) g.slices *= 2;
+        while (g.slices < 8 && bytes / g.slices > (3 << 20) && width * bank_size / g.slices >= 256) g.slices *= 2;
     if (vecs > 64 * g.slices) g.slices = (vecs + 63) / 64;
     g.lanes = kMinLanes;
     while (g.lanes * g.slices < vecs) g.lanes *= 2;
@@ -876,7 +883,7 @@ void run_sum(const BankGradParams& p, const SumGrid& g, hipStream_t stream) {
     else hipLaunchKernelGGL((sum_kernel<D, E, VEC, WEIGHTS, DROP, kStore>), grid, block, lds, stream, p, g);
 }
 
-template <typename D, typename E, bool VEC> void run_sums(const BankGradParams& p, hipStream_t stream) {
+template <typename D, typename E, bool VEC> void run_turn(const BankGradParams& p, hipStream_t stream) {
     const SumGrid g = sum_grid(p, int(sizeof(D)), int(sizeof(E)));
     if (p.w[0] != nullptr) {
         if constexpr (sizeof(D) == 4) run_sum<D, E, VEC, true, false>(p, g, stream);
@@ -886,11 +893,21 @@ template <typename D, typename E, bool VEC> void run_sums(const BankGradParams& 
         run_sum<D, E, VEC, false, false>(p, g, stream);
     }
     if (p.blocks <= 1) return;
+    const int vecs = (p.columns - p.line * kMinTurn + 3) / 4;
     int lanes = kMinLanes;
-    while (lanes < 64 && lanes < (p.hd + 3) / 4) lanes *= 2;
-    const dim3 join{unsigned((p.blocks + kJoinBlocks - 1) / kJoinBlocks), unsigned(((p.hd + 3) / 4 + lanes - 1) / lanes)};
+    while (lanes < 64 && lanes < vecs) lanes *= 2;
+    const dim3 join{unsigned((p.blocks + kJoinBlocks - 1) / kJoinBlocks), unsigned((vecs + lanes - 1) / lanes)};
     if (p.add) hipLaunchKernelGGL((join_kernel<E, VEC, true>), join, dim3(kJoinThreads), 0, stream, p, lanes);
     else hipLaunchKernelGGL((join_kernel<E, VEC, false>), join, dim3(kJoinThreads), 0, stream, p, lanes);
+}
+
+template <typename D, typename E, bool VEC> void run_sums(const BankGradParams& call, hipStream_t stream) {
+    BankGradParams p = call;
+    for (int first = 0; first < p.hd; first += p.turn) {
+        p.line = first / kMinTurn;
+        p.columns = p.hd - first < p.turn ? p.hd : first + p.turn;
+        run_turn<D, E, VEC>(p, stream);
+    }
 }
 
 template <typename D, typename E> void run_types(const BankGradParams& p, hipStream_t stream) {
@@ -947,6 +964,15 @@ int64_t bank_grad_layout(BankGradParams* p, void* workspace) {
     p->block = block;
     p->spill = block / 2 < kMaxSpill ? block / 2 : kMaxSpill;
     p->blocks = uint32_t((entries + block - 1) / block);
+    p->turn = int(8 * octets);
+    const int64_t column_bytes = 8 * int64_t(p->blocks);  // of both arrays
+    if (column_bytes * p->turn > kTurnBytes) {
+        const int64_t most = kTurnBytes / column_bytes / kMinTurn * kMinTurn;
+        p->turn = int(most > kMinTurn ? most : kMinTurn);
+        if (p->turn > 8 * octets) p->turn = int(8 * octets);
+    }
+    p->line = 0;
+    p->columns = p->hd < p->turn ? p->hd : p->turn;
     char* base = static_cast<char*>(workspace);
     int64_t used = 0;
     auto place = [&](int64_t bytes) {
@@ -961,15 +987,18 @@ int64_t bank_grad_layout(BankGradParams* p, void* workspace) {
     p->hist = reinterpret_cast<uint32_t*>(place(4 * p->passes * p->stride * digits));
     for (int i = 0; i < 2; ++i) p->records[i] = reinterpret_cast<Record*>(place(8 * entries));
     for (int i = 0; i < 2; ++i) p->weights[i] = reinterpret_cast<float*>(place(4 * entries));
-    p->first = reinterpret_cast<float*>(place(32 * octets * p->blocks));
-    p->last = reinterpret_cast<float*>(place(32 * octets * p->blocks));
+    p->first = reinterpret_cast<float*>(place(4 * int64_t(p->turn) * p->blocks));
+    p->last = reinterpret_cast<float*>(place(4 * int64_t(p->turn) * p->blocks));
     return used;
 }
 
 int64_t bank_grad_groups(const BankGradParams& p, int dout_size, int bank_size) {
     const SumGrid g = sum_grid(p, dout_size, bank_size);
-    const int64_t zeros = p.add || by_rows(p) ? 0 : zero_groups(int64_t(p.num_slots) * p.hd * bank_size, 1);
-    return 8 * (int64_t(g.sums) + g.rows) + 4 * (p.tiles + zeros + 1);  // the sort's may have 1024 threads
+    const int64_t zeroed = p.add || by_rows(p) ? 0 : int64_t(p.num_slots) * p.hd * bank_size;
+    // In workgroups of 256 threads: one workgroup's sort has 1024, the bank's part beside it too.
+    const int64_t sort = p.items == 0 ? 4 * (1 + zero_groups(zeroed, 1)) : p.tiles + zero_groups(zeroed, 2 * p.passes);
+    const int64_t sums = 8 * (int64_t(g.sums) + g.rows);
+    return sort > sums ? sort : sums;
 }
 
 hipError_t launch_bank_grad(const BankGradParams& call, bool dout_bf16, bool bank_bf16, hipStream_t stream) {

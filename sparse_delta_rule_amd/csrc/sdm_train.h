@@ -120,6 +120,8 @@ struct BankGradParams {
     int block, spill;     // entries of a lane group; how far it may go past their end
     uint32_t blocks;
     int64_t zero_bytes;   // of dbank, zeroed beside the sort
+    int turn;             // columns that are summed at a time: all, or a multiple of 64
+    int line, columns;    // the first of this turn's, in 64s, and the end of them
     // workspace
     uint32_t* n;          // [1] entries that count
     int64_t stride;       // of the counts of a digit
@@ -127,8 +129,8 @@ struct BankGradParams {
     uint32_t* total;      // [passes, 2^bits]
     Record* records[2];   // [entries]
     float* weights[2];    // [entries] (a gather)
-    float* first;         // [blocks, columns rounded up to 8] sums of a run that began in an earlier block
-    float* last;          // [blocks, columns rounded up to 8] of one that goes on in the next
+    float* first;         // [blocks, turn] sums of a run that began in an earlier block
+    float* last;          // [blocks, turn] of one that goes on in the next
 };
 // From entries, num_slots and hd: the other sizes and, where `workspace` is given, the places of
 // its arrays; returns the workspace's bytes.

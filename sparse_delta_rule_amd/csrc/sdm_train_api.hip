@@ -287,10 +287,14 @@ int sdm_lookup_grad(int64_t n, const void* idx, int idx_dtype, const void* dout,
     const int is = elem_size(idx_dtype), ds = elem_size(dout_dtype), bs = elem_size(bank_dtype);
     if (!aligned(idx, is) || !aligned(dout, ds) || !aligned(dbank, bs))
         return fail(SDM_E_ALIGN, "%s: a pointer is not aligned to its element size", fn);
-    p.entries = uint32_t(n);
+    p.entries = p.tokens = p.chunk = p.valid = uint32_t(n);
+    p.width[0] = 1;
     p.num_slots = uint32_t(num_slots);
     p.hd = int(head_dim);
+    p.add = mode == SDM_GRAD_ADD;
     const int64_t needed = bank_grad_layout(&p, workspace);
+    if (bank_grad_groups(p, ds, bs) > kMaxGroups)
+        return fail(SDM_E_SHAPE, "%s: the bank or the entries exceed the grid", fn);
     const Named read[] = {{idx, "idx", n * is},
                           {dout, "dout", n * head_dim * ds},
                           {p.dropout.threshold != 0 ? rng : nullptr, "rng", 16}};
@@ -304,14 +308,9 @@ int sdm_lookup_grad(int64_t n, const void* idx, int idx_dtype, const void* dout,
     }
     p.idx[0] = idx;
     p.dout[0] = dout;
-    p.width[0] = 1;
-    p.tokens = p.chunk = p.valid = uint32_t(n);
     p.idx64 = idx_dtype == SDM_I64;
     p.dropout.rng = rng;
     p.dbank = dbank;
-    p.add = mode == SDM_GRAD_ADD;
-    if (bank_grad_groups(p, ds, bs) > kMaxGroups)
-        return fail(SDM_E_SHAPE, "%s: the bank or the entries exceed the grid", fn);
     return launched(fn, launch_bank_grad(p, dout_dtype == SDM_BF16, bank_dtype == SDM_BF16,
                                          static_cast<hipStream_t>(hip_stream)));
 }
@@ -360,9 +359,14 @@ int sdm_gather_bank_grad(int64_t tokens, int64_t chunk, int64_t valid, const int
     if (!fine) return fail(SDM_E_ALIGN, "%s: a pointer is not aligned to its element size", fn);
     BankGradParams p{};
     p.entries = uint32_t(tokens * all);
+    p.tokens = uint32_t(tokens);
+    for (int o = 0; o < operands; ++o) p.width[o] = uint32_t(width[o]);
     p.num_slots = uint32_t(num_slots);
     p.hd = int(head_dim);
+    p.add = mode == SDM_GRAD_ADD;
     const int64_t needed = bank_grad_layout(&p, workspace);
+    if (bank_grad_groups(p, 4, bs) > kMaxGroups)
+        return fail(SDM_E_SHAPE, "%s: the bank or the entries exceed the grid", fn);
     Named written[2] = {{dbank, "dbank", num_slots * head_dim * bs}};
     rc = check_workspace(fn, workspace, workspace_bytes, needed, written, 1, read, size_t(1 + 3 * operands));
     if (rc != SDM_OK) return rc;
@@ -375,9 +379,7 @@ int sdm_gather_bank_grad(int64_t tokens, int64_t chunk, int64_t valid, const int
         p.idx[o] = idx[o];
         p.w[o] = w[o];
         p.dout[o] = dout[o];
-        p.width[o] = uint32_t(width[o]);
     }
-    p.tokens = uint32_t(tokens);
     p.chunk = uint32_t(chunk < UINT32_MAX ? chunk : UINT32_MAX);  // past the tokens only where there are none
     p.valid = uint32_t(valid < INT32_MAX ? valid : INT32_MAX);
     p.chunk_valid = chunk_valid;
@@ -385,9 +387,6 @@ int sdm_gather_bank_grad(int64_t tokens, int64_t chunk, int64_t valid, const int
     p.w_bf16 = w_dtype == SDM_BF16;
     p.factor = 1.0f;
     p.dbank = dbank;
-    p.add = mode == SDM_GRAD_ADD;
-    if (bank_grad_groups(p, 4, bs) > kMaxGroups)
-        return fail(SDM_E_SHAPE, "%s: the bank or the entries exceed the grid", fn);
     return launched(fn, launch_bank_grad(p, false, bank_dtype == SDM_BF16, static_cast<hipStream_t>(hip_stream)));
 }
 

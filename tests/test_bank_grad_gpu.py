@@ -349,6 +349,44 @@ def test_many_entries():
     assert torch.equal(got.double(), want)
 
 
+@pytest.mark.slow
+@pytest.mark.parametrize("hd", [4160, 4163])
+@pytest.mark.parametrize("kind", ["even", "skewed", "one"])
+def test_columns_in_turns(hd, kind):
+    """2^20 entries of so many columns that the sums of blocks are made for 4096 of them at a time."""
+    T, W, slots = 4096, 256, 64
+    idx = slots_like(kind, T * W, slots, 1).view(T, W).to(DEV)
+    w = whole((T, W), 2, 1).to(DEV)
+    dout = whole((T, hd), 3, 1).to(DEV)
+    assert sdm.library().sdm_bank_grad_workspace(T * W, slots, hd) < 27 * T * W + (1 << 30) + (1 << 20) < 24 * T * W + T * W // 4 * hd
+    matrix = torch.zeros((slots, T), dtype=torch.float64, device=DEV)
+    matrix.index_put_((idx.flatten(), torch.arange(T, device=DEV).repeat_interleave(W)), w.flatten().double(), accumulate=True)
+    want = matrix @ dout.double()  # whole numbers below 2^21
+    got = sdm.sdm_gather_bank_grad(idx, w, dout, slots, chunk=T)
+    assert torch.equal(got.double(), want)
+    got = sdm.sdm_gather_bank_grad(idx, w, dout, slots, chunk=T, dbank=got, accumulate=True)
+    assert torch.equal(got.double(), 2 * want)
+    large = sdm.sdm_gather_bank_grad(idx + 7, w, dout, T * W + 9, chunk=T, bank_dtype=torch.bfloat16)  # zeroed beside the sort
+    assert torch.equal(large[7:71], want.to(torch.bfloat16)) and not large[:7].any() and not large[71:].any()
+
+
+@pytest.mark.slow
+def test_dropout_in_turns():
+    n, slots, hd = 1 << 20, 33, 4160
+    idx = slots_like("skewed", n, slots, 1).to(DEV)
+    rng = torch.tensor([11, 12], device=DEV)
+    dout = torch.randint(-1, 2, (n, hd), device=DEV, dtype=torch.int8, generator=torch.Generator(device=DEV).manual_seed(1)).to(torch.bfloat16)
+    got = sdm.sdm_lookup_grad(idx, dout, slots, dropout=0.5, rng=rng)
+    mask = sdm.sdm_lookup(torch.ones((slots, hd), device=DEV, dtype=torch.bfloat16), idx, dropout=0.5, rng=rng)  # 0 or 2
+    want = torch.zeros((slots, hd), device=DEV, dtype=torch.float64)
+    for a in range(0, n, 1 << 17):
+        at = slice(a, a + (1 << 17))
+        one_hot = torch.zeros((slots, 1 << 17), dtype=torch.float32, device=DEV)
+        one_hot[idx[at], torch.arange(1 << 17, device=DEV)] = 1
+        want += (one_hot @ (mask[at] * dout[at]).float()).double()  # whole numbers, of less than 2^18
+    assert torch.equal(got.double(), want)
+
+
 def test_refusals():
     idx, dout = torch.zeros(3, dtype=torch.int64, device=DEV), torch.ones((3, 8), device=DEV)
     with pytest.raises(ValueError, match="dbank to add to"):

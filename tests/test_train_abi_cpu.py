@@ -291,6 +291,25 @@ def test_bank_grad_workspace():
             assert least < f(n, 1 << 20, hd) < least + rows + 64 * 1024 + n
 
 
+@pytest.mark.parametrize("entries,slots,head_dim", [
+    (32768 * 512, 32768, 8192), ((1 << 20) * 512, 1 << 20, 1024), (1 << 20, 64, 4160), (33024, 3, 65535 * 256), (40, 3, 65535 * 256),
+    ((1 << 31) - 1, 1 << 21, 128), ((1 << 31) - 1, (1 << 31) - 1, 1), ((1 << 31) - 1, 1 << 27, 40), (5000, 1 << 27, 20000)])
+def test_bank_grad_workspace_of_many_entries(entries, slots, head_dim):
+    """The header's bound: sums of runs do not grow with entries times columns."""
+    size = sdm.library().sdm_bank_grad_workspace(entries, slots, head_dim)
+    assert 24 * entries < size <= 27 * entries + max(1 << 30, 16 * entries) + MB
+
+
+@pytest.mark.parametrize("entries,over", [(300, True), (4096, True), (5000, False)])
+def test_the_largest_written_bank(entries, over):
+    """Sizes alone: a call within them stops at the memory that dbank and dout share."""
+    args = with_changes(GRAD, dict(n=entries, num_slots=1 << 22, head_dim=16384, dout=A + (1 << 45), dbank=A + (1 << 46), workspace=A + (1 << 44),
+                                   workspace_bytes=1 << 40))
+    if over:
+        rejects("sdm_lookup_grad", args, {}, E_SHAPE, "exceed the grid")
+    rejects("sdm_lookup_grad", args, dict(num_slots=(1 << 22) - 2, dout=A + (1 << 46)), E_OVERLAP, "dbank and dout")
+
+
 # ------------------------------------------------------------------ the binding's own checks
 def test_the_binding_checks_its_tensors():
     """Host tensors: every call stops before the library."""
