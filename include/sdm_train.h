@@ -157,9 +157,10 @@ int sdm_lookup(const void* bank, const void* scales, int bank_dtype, int64_t num
  * with a, and m the mask of columns that stay, as in sdm_lookup of the same idx, scale,
  * dropout and rng. Rows whose idx lies outside the bank add nothing, and their dout is not
  * read; neither is a dropped column's dout ever counted, whatever it holds. Sums are
- * float32, over the rows of a slot in ascending order in runs whose lengths are fixed by
- * the call's sizes and idx: the same inputs give the same bits. The result is rounded once
- * to bank_dtype.
+ * float32, over at most 48 rows of a slot in ascending order. Where a slot has more, up to 17
+ * such sums are added in their order in float32, and more of them in float64 and rounded to
+ * float32. All of this is fixed by the call's sizes and idx: the same inputs give the same
+ * bits. The result is rounded once to bank_dtype.
  *
  * Arguments: as sdm_lookup, with
  *   n           0..SDM_MAX_GRAD_ENTRIES (0: dbank is zeroed, or left).
@@ -181,8 +182,8 @@ int sdm_lookup_grad(int64_t n, const void* idx, int idx_dtype, const void* dout,
  *     dbank_s = sum_{(o, t, n) : idx_o[t,n] = s} w_o[t,n] dout_o[t]    (or dbank_s + that)
  * over the live tokens t of sdm_gather (or sdm_gather_packed's values) with the same slots
  * and weights; padding tokens' slots and weights may hold anything, their dout is not read. Sums are float32,
- * fused multiply-adds over the entries of a slot in ascending order (o, t, n), in runs as
- * in sdm_lookup_grad; the result is rounded once to bank_dtype.
+ * fused multiply-adds over the entries of a slot in ascending order (o, t, n), put together
+ * as in sdm_lookup_grad; the result is rounded once to bank_dtype.
  *
  * Arguments: tokens, chunk, valid, chunk_valid, idx and w as sdm_gather's (a slot outside
  * the bank adds nothing), with tokens * (width0 + width1) <= SDM_MAX_GRAD_ENTRIES and

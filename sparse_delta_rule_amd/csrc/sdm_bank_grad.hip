@@ -718,9 +718,10 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(BankGradParams p, SumGrid
 // ------------------------------------------------------------------ sums of blocks' sums
 
 // Runs over several blocks, 14 us for a most frequent token of 2100 in 32768: a chain of loads. A
-// workgroup looks at 64 blocks. Of the runs that begin there each lane
-// group adds up some of the short ones; a long one's blocks are shared by all lane groups, whose
-// sums are added in order.
+// workgroup looks at 64 blocks. Of the runs that begin there each lane group adds up some of the short
+// ones, in order; a long one's blocks are dealt out to all lane groups, each of which adds its own, and
+// then the groups' sums are added. As many as a batch has rows may come together there, so that these
+// additions are float64.
 constexpr int kJoinThreads = 1024;
 constexpr int kJoinBlocks = 64;
 
@@ -730,7 +731,7 @@ template <typename E, bool VEC, bool ADD> __global__ __launch_bounds__(kJoinThre
     constexpr int N = 4;
     __shared__ uint64_t masks[2];
     __shared__ uint32_t slots[64];  // of the blocks' last entries
-    __shared__ float sums[kJoinThreads][N];
+    __shared__ double sums[kJoinThreads][N];
     const int tid = threadIdx.x, groups = kJoinThreads / lanes, lane = tid % lanes, group = tid / lanes;
     const int at0 = (int(blockIdx.y) * lanes + lane) * N, c0 = p.line * kMinTurn + at0;  // of the turn, and of the row
     const int64_t columns = p.turn;
@@ -758,7 +759,7 @@ template <typename E, bool VEC, bool ADD> __global__ __launch_bounds__(kJoinThre
     }
     __syncthreads();
     const uint64_t begins = masks[0], middles = masks[1];
-    auto add = [&](float (&acc)[N], uint32_t b, uint32_t from, uint32_t more, uint32_t stride) {
+    auto add = [&](auto (&acc)[N], uint32_t b, uint32_t from, uint32_t more, uint32_t stride) {
         for (uint32_t c = from; c < more; c += kFlight * stride) {
             float x[kFlight][N];
 #pragma unroll
@@ -806,19 +807,28 @@ template <typename E, bool VEC, bool ADD> __global__ __launch_bounds__(kJoinThre
                 more += found;
             } while (found == kJoinThreads);
         }
-        float acc[N] = {};
+        double acc[N] = {};
         if (c0 < p.columns) {
-            if (group == 0) load_columns<float, N, true>(p.last + b * columns, at0, p.turn, acc);
+            if (group == 0) {
+                float begun[N];
+                load_columns<float, N, true>(p.last + b * columns, at0, p.turn, begun);
+#pragma unroll
+                for (int j = 0; j < N; ++j) acc[j] = begun[j];
+            }
             add(acc, b, group, more, groups);
         }
-        *reinterpret_cast<float4*>(sums[tid]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+#pragma unroll
+        for (int j = 0; j < N; ++j) sums[tid][j] = acc[j];
         __syncthreads();
         if (group == 0 && c0 < p.columns) {
             for (int g = 1; g < min(groups, int(min(more, uint32_t(kJoinThreads)))); ++g) {
 #pragma unroll
                 for (int j = 0; j < N; ++j) acc[j] += sums[g * lanes + lane][j];
             }
-            finish(slot, acc);
+            float total[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) total[j] = float(acc[j]);
+            finish(slot, total);
         }
         __syncthreads();
     }

@@ -309,6 +309,28 @@ def test_the_same_inputs_give_the_same_bits(kind):
         sdm.sdm_lookup_grad(idx, dout, slots, workspace=ws[:1024])
 
 
+@pytest.mark.parametrize("add", [False, True], ids=["write", "add"])
+@pytest.mark.parametrize("hd", [40, 128, 129])
+@pytest.mark.parametrize("terms", ["alike", "any"])
+def test_long_sums_lose_no_more_than_short_ones(terms, hd, add):
+    """2^20 terms of one slot, and some of others. Alike: each term's lowest bits are less than half a step of a sum of 512
+    blocks of 32, so that a float32 sum of those would lose them every time."""
+    T, W, slots = 4096, 256, 50
+    g = torch.Generator(device=DEV).manual_seed(1)
+    idx = torch.where(torch.rand((T, W), generator=g, device=DEV) < 0.01, torch.randint(0, slots, (T, W), generator=g, device=DEV), 7)
+    w = torch.full((T, W), 1 + 1.5 * 2.0 ** -16, device=DEV) if terms == "alike" else torch.rand((T, W), generator=g, device=DEV)
+    dout = torch.ones((T, hd), device=DEV) if terms == "alike" else torch.rand((T, hd), generator=g, device=DEV)
+    got = sdm.sdm_gather_bank_grad(idx, w, dout, slots, chunk=T, dbank=torch.zeros((slots, hd), device=DEV), accumulate=add)
+    matrix = torch.zeros((slots, T), dtype=torch.float64, device=DEV)
+    matrix.index_put_((idx.flatten(), torch.arange(T, device=DEV).repeat_interleave(W)), w.flatten().double(), accumulate=True)
+    want = matrix @ dout.double()
+    # at most 48 roundings of a block's terms and 16 of up to 17 blocks, or one of more of them; one of the sum with what
+    # was there; terms are positive
+    assert ((got.double() - want).abs() <= (48 + 16 + 1) * 2.0 ** -24 * want).all()
+    long = (got.double() - want)[7].abs() / want[7]
+    assert (long <= (48 + 1 + 1) * 2.0 ** -24).all()
+
+
 @pytest.mark.slow
 def test_a_bank_past_32_bit_offsets():
     slots, hd = (1 << 25) + 5, 136  # 4.56e9 values
