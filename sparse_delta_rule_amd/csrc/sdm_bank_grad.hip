@@ -671,7 +671,7 @@ __device__ __forceinline__ void sum_blocks(const S& s, const SumGrid& g, uint32_
                 const uint32_t next = is_last ? kNone : slots[place(at + u + 1)];
                 if (next != slot) {
                     if (open || (is_last && goes_on)) {
-                        float* to = (open ? p.first : p.last) + int64_t(b) * p.turn + (s.c - p.line * kMinTurn);
+                        float* to = (open ? p.first : p.last) + int64_t(b) * p.turn + s.c;
 #pragma unroll
                         for (int j = 0; j < N; j += 4)
                             *reinterpret_cast<float4*>(to + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
@@ -727,13 +727,14 @@ constexpr int kJoinBlocks = 64;
 
 constexpr uint32_t kShort = 16;  // blocks of a run that one lane group adds up
 
-template <typename E, bool VEC, bool ADD> __global__ __launch_bounds__(kJoinThreads) void join_kernel(BankGradParams p, int lanes) {
+template <typename E, bool VEC, bool ADD>
+__global__ __launch_bounds__(kJoinThreads, 8) void join_kernel(BankGradParams p, int lanes) {  // 64 registers: two workgroups a compute unit
     constexpr int N = 4;
     __shared__ uint64_t masks[2];
     __shared__ uint32_t slots[64];  // of the blocks' last entries
     __shared__ double sums[kJoinThreads][N];
     const int tid = threadIdx.x, groups = kJoinThreads / lanes, lane = tid % lanes, group = tid / lanes;
-    const int at0 = (int(blockIdx.y) * lanes + lane) * N, c0 = p.line * kMinTurn + at0;  // of the turn, and of the row
+    const int c0 = p.line * kMinTurn + (int(blockIdx.y) * lanes + lane) * N;
     const int64_t columns = p.turn;
     const Record* records = p.records[(p.passes - 1) & 1];
     const uint32_t n = *p.n;
@@ -764,7 +765,7 @@ template <typename E, bool VEC, bool ADD> __global__ __launch_bounds__(kJoinThre
             float x[kFlight][N];
 #pragma unroll
             for (int u = 0; u < kFlight; ++u)
-                load_columns<float, N, true>(p.first + (int64_t(b) + 1 + min(c + u * stride, more - 1)) * columns, at0, p.turn, x[u]);
+                load_columns<float, N, true>(p.first + (int64_t(b) + 1 + min(c + u * stride, more - 1)) * columns, c0, p.hd, x[u]);
 #pragma unroll
             for (int u = 0; u < kFlight; ++u)
                 if (c + u * stride < more)
@@ -789,7 +790,7 @@ template <typename E, bool VEC, bool ADD> __global__ __launch_bounds__(kJoinThre
         const uint32_t b = b0 + uint32_t(i), more = known(i);
         if (more > kShort || i + more > 64 || c0 >= p.columns) continue;
         float acc[N];
-        load_columns<float, N, true>(p.last + b * columns, at0, p.turn, acc);
+        load_columns<float, N, true>(p.last + b * columns, c0, p.hd, acc);
         add(acc, b, 0, more, 1);
         finish(slots[i], acc);
     }
@@ -811,7 +812,7 @@ template <typename E, bool VEC, bool ADD> __global__ __launch_bounds__(kJoinThre
         if (c0 < p.columns) {
             if (group == 0) {
                 float begun[N];
-                load_columns<float, N, true>(p.last + b * columns, at0, p.turn, begun);
+                load_columns<float, N, true>(p.last + b * columns, c0, p.hd, begun);
 #pragma unroll
                 for (int j = 0; j < N; ++j) acc[j] = begun[j];
             }
@@ -915,6 +916,8 @@ template <typename D, typename E, bool VEC> void run_sums(const BankGradParams& 
     BankGradParams p = call;
     for (int first = 0; first < p.hd; first += p.turn) {
         p.line = first / kMinTurn;
+        p.first = call.first - first;  // where column 0 would be
+        p.last = call.last - first;
         p.columns = p.hd - first < p.turn ? p.hd : first + p.turn;
         run_turn<D, E, VEC>(p, stream);
     }
