@@ -127,13 +127,16 @@ def sdm_lookup(bank: Union[PackedBank, torch.Tensor], idx: torch.Tensor, *, scal
                rng: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
                out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Scaled rows of a bank, with dropout (``sdm_lookup`` of include/sdm_train.h):
-    [*idx.shape, head_dim] of out_dtype (default: the bank's, float32 of a packed bank).
+    [*idx.shape, head_dim] of out_dtype (default: that of a given ``out``, else the bank's,
+    float32 of a packed bank).
 
     bank [num_slots, head_dim] float32 or bfloat16, or a PackedBank; idx int32 or int64 of
     any shape, a row outside the bank (-1, say) is 0. ``dropout`` (taken to the nearest
     2^-16) needs rng, int64 [2] on the device: a seed and an offset, from which the mask is
     computed here and again in ``sdm_lookup_grad``.
     """
+    if out is not None and out_dtype not in (None, out.dtype):
+        raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
     if isinstance(bank, PackedBank):
         dev, hd, head, default = bank._device, bank.head_dim, bank._head, torch.float32
     else:
@@ -175,7 +178,8 @@ def sdm_lookup_grad(idx: torch.Tensor, dout: torch.Tensor, num_slots: int, *, sc
                     workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient of a lookup with respect to its bank (``sdm_lookup_grad`` of
     include/sdm_train.h): dbank [num_slots, head_dim] of bank_dtype, written whole, or with
-    ``accumulate`` given and added to (rows that idx does not name are not touched).
+    ``accumulate`` given and added to (rows that idx does not name are not touched). A given
+    dbank is float32 or bfloat16, whatever bank_dtype says.
 
     dout [*idx.shape, head_dim] float32 or bfloat16; idx, scale, dropout and rng as in the
     lookup.
@@ -204,7 +208,8 @@ def sdm_gather_bank_grad(idx0: torch.Tensor, w0: torch.Tensor, dout0: torch.Tens
                          workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient of a gather's outputs with respect to its bank (``sdm_gather_bank_grad`` of
     include/sdm_train.h): dbank [num_slots, head_dim] of bank_dtype, written whole, or with
-    ``accumulate`` given and added to (rows that no live token names are not touched).
+    ``accumulate`` given and added to (rows that no live token names are not touched). A given
+    dbank is float32 or bfloat16, whatever bank_dtype says.
 
     idx0, w0 [tokens, width0], idx1, w1 and the padding as in the gather; dout0, dout1
     float32 [tokens, head_dim].

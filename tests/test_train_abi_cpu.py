@@ -323,3 +323,11 @@ def test_the_binding_checks_its_tensors():
         sdm.sdm_lookup(x.half(), i)
     with pytest.raises(ValueError, match="none of them"):
         sdm.sdm_gather_bank_grad(i, x[:, :2].contiguous(), x, 9, chunk=4, idx1=i)
+
+
+def test_a_lookups_out_and_its_type_agree():
+    x, i = torch.zeros((4, 8)), torch.zeros(4, dtype=torch.int64)
+    with pytest.raises(TypeError, match="out is torch.bfloat16, out_dtype torch.float32"):
+        sdm.sdm_lookup(x, i, out=x.bfloat16(), out_dtype=torch.float32)
+    with pytest.raises(ValueError, match="device -1"):  # which they do here
+        sdm.sdm_lookup(x, i, out=x.bfloat16(), out_dtype=torch.bfloat16)
