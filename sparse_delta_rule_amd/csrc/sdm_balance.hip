@@ -569,7 +569,8 @@ __device__ __forceinline__ float count_of_largest(const float (&e)[VPT], const f
     return top;
 }
 
-// 32768 x 256 float32 keys: 15 us, 4.4 TB/s of live rows read and rows written.
+// 32768 x 256 float32 keys: 15 us. A copy of as many bytes takes 9 (the caches hold a part), the 5.1 M
+// vector instructions some 9; neither fills the other's gaps, with two workgroups a compute unit.
 template <typename E, int LANES, int VPT, bool VEC>
 __global__ __launch_bounds__(kSmallThreads) void balance_backward_small_kernel(BalanceParams p) {
     using Row = RowKeys<E, LANES, VPT, VEC>;
@@ -617,8 +618,10 @@ __global__ __launch_bounds__(kSmallThreads) void balance_backward_small_kernel(B
     }
 }
 
-// A row at a time, the counts in registers. 4096 rows of 16384 bfloat16 keys: 59 us, 4.5 TB/s read
-// and written, with 41 us of instructions.
+// A row at a time, the counts in registers. 4096 rows of 16384 bfloat16 keys: 59 to 63 us, 4.3 to 4.5
+// TB/s read and written, with 41 us of instructions. Rows of more than
+// 16384 keys, and of more than 8192 that are not whole vectors, do not fit the registers (32768 float32
+// keys spill 32, or 118).
 template <typename E, int THREADS, int VPT, bool VEC>
 __global__ __launch_bounds__(THREADS) void balance_backward_big_kernel(BalanceParams p) {
     using Row = RowKeys<E, THREADS, VPT, VEC>;
@@ -825,9 +828,11 @@ __global__ __launch_bounds__(THREADS) void balance_backward_long_kernel(BalanceP
 
 // ------------------------------------------------------------------ launches
 
-// Pieces wanted of a call with many tokens. More read the rows no faster and leave the second pass
-// more to add (32768 x 256: 19.4 us with 512, 20.2 with 1024 and 256; 4096 x 16384: 64 with 256, 80
-// with 512).
+// Pieces wanted of a call with many tokens. More leave the second pass more to add, fewer leave compute
+// units idle. Up to 1024 keys 512: the gradient of 32768 x 256 in 14.4 us, with 256 in 16.9, with 1024 in
+// 15.8; of 32768 x 1024 in 47.1, 45.8 and 53.8, its first pass 36.4, 32.2 and 40.6. Beyond 256: 4096 x
+// 16384 in 50.1 us, with 128 in 67.5, with 512 in 58.7; 1024 x 65536 float32 in 234, 278 and 293; only
+// 8192 x 4096 would take 512 (52.2, 87.0 and 46.8).
 constexpr int64_t kPieces = 512, kBigPieces = 256;
 
 template <typename E, int LANES, int VPT> void run_small(const BalanceParams& p, bool vec, bool backward, hipStream_t s) {

@@ -137,8 +137,9 @@ template <int THREADS> __device__ __forceinline__ uint32_t sum_below(uint32_t v,
     return below;
 }
 
-// Few entries: one workgroup sorts them in LDS, all passes in one launch (500 entries: 5 us; 8192, two
-// passes: 25 us, as long as the four launches of many workgroups, which zero the bank beside it).
+// Few entries, up to 4096: one workgroup sorts them in LDS, all passes in one launch (500 entries: 5 us).
+// With 8 entries a thread it took 25 us for 8192 in two passes, as long as the four launches of many
+// workgroups, which zero the bank beside it.
 constexpr int kOneThreads = 1024;
 constexpr int kOneWaves = kOneThreads / 64;
 
@@ -271,8 +272,8 @@ __global__ __launch_bounds__(kThreads) void sort_scan_kernel(BankGradParams p, i
 // 64 neighbours at a time; the lanes of the same digit find one another by ballots. The tile's
 // entries are put in order in LDS first, so that those of a digit leave as one run of memory.
 // SUMS: the tiles are few, and a workgroup adds up the lower ones' counts by itself.
-// Bound by a tile's chain of steps, with five tiles on a compute unit at a time: 2.35 M entries of
-// 12 bytes in 23 us, 2.5 TB/s; directly to their places, without LDS, 37 us.
+// Bound by a tile's chain of steps, with five tiles on a compute unit at a time: 3.14 M entries of
+// 12 bytes read and written in 23 us, 3.2 TB/s; directly to their places, without LDS, 37 us.
 template <bool FIRST, bool LOOKUP, int ITEMS, bool SUMS>
 __global__ __launch_bounds__(kThreads) void sort_place_kernel(BankGradParams p, int pass) {
     constexpr uint32_t kTile = kThreads * ITEMS;
@@ -476,7 +477,7 @@ template <typename D, typename E, bool VEC, bool WEIGHTS, bool DROP> struct Sums
 
 // The grid of the sums, workgroups in eights, one on each XCD: `sums` eights for the blocks of entries,
 // then `rows` eights for the bank's rows. (With the blocks' workgroups, most of which end at once, and
-// the rows' taken in turn, 2.35 M entries of 2^21 x 128 took 459 us instead of 332.)
+// the rows' taken in turn, 3.14 M entries of 2^21 x 128 took 459 us instead of 332.)
 struct SumGrid {
     int lanes, slices, shift;  // lanes of a group; groups that share a row's columns; log2 of p.block
     uint32_t ranges;           // workgroups of a slice, for the blocks
@@ -506,10 +507,10 @@ __device__ __forceinline__ uint32_t lower_bound(const Record* records, uint32_t 
 
 // A workgroup takes neighbouring rows of the bank and writes each: the sum of its entries, or 0. So
 // the bank is written once and in order. Rows of long runs are left to the blocks' sums.
-// Bound by what leaves and enters the L2 caches: 3.1 M entries (2.35 M that count) of 2^21 x 128
-// float32 in 332 us, 1.07 GB written and 0.59 GB or more fetched (reads are counted as 64 bytes
-// each), at least 5.0 TB/s. Without slices of the columns 376 us, 0.82 GB: 41% of the L2's accesses
-// hit, 54% with four slices. The entries' rows first and the zeros in a pass of its own 342.
+// Bound by what leaves and enters the L2 caches: 4.19 M entries (3.14 M that count) of 2^21 x 128
+// float32 in 332 us, 1.07 GB written and 1.19 GB fetched (9.27 M misses of 128 bytes), 6.8 TB/s, of which
+// dout, 34 MB, comes from the cache behind the L2s. 56% of the L2s' reads hit. Without slices of the
+// columns 376 us, 1.64 GB fetched. The entries' rows first and the zeros in a pass of its own 342.
 template <typename S>
 __device__ __forceinline__ void sum_rows(const S& s, const SumGrid& g, uint32_t range, uint32_t* lds) {
     constexpr int N = S::N;

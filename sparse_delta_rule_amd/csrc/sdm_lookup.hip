@@ -32,10 +32,11 @@ template <bool MX4> struct PackedOctet {
 template <> struct OctetOf<SDM_MX8, 16> : PackedOctet<false> {};
 template <> struct OctetOf<SDM_MX4, 16> : PackedOctet<true> {};
 
-// A thread takes eight columns of ROWS rows, a row's threads are neighbours. Bound by its memory
-// traffic: 32768 rows of 1024 bfloat16 with dropout in 20 us, 5.1 TB/s of rows fetched (each by
-// the XCDs that read it) and written; the ten rounds of the generator, one run for eight columns, hide behind it. A launch
-// of few rows is bound by two dependent loads (64 rows: 2.6 us).
+// A thread takes eight columns of ROWS rows, a row's threads are neighbours. 32768 rows of 1024
+// bfloat16 take 15.5 us, 6.5 TB/s of rows fetched (each by the XCDs that read it) and written; with
+// dropout 20, as the ten rounds of the generator, though one run serves eight columns, are 10.4 M vector
+// instructions, some 17 us, that the loads only in part hide. A launch of few rows is bound by two
+// dependent loads (64 rows: 2.6 us).
 template <int KIND, int VB, typename E, int OVB, bool DROP, int ROWS>
 __global__ __launch_bounds__(kThreads) void lookup_kernel(LookupParams p) {
     const int octets = (p.hd + 7) / 8;
@@ -74,8 +75,10 @@ struct LookupGrid {
 LookupGrid lookup_grid(const LookupParams& p) {
     const int octets = (p.hd + 7) / 8, rows = kThreads / (octets < kThreads ? octets : kThreads);
     LookupGrid g{(p.n + rows - 1) / rows, (octets + kThreads - 1) / kThreads, 1, rows};
-    // Several rows a thread where that leaves 1024 workgroups (32768 x 1024: 20.7 us, with one row a
-    // thread 23.4; 65521 rows of 100 4-bit columns: 10.4 us, with one 9.8).
+    // Several rows a thread where that leaves 1024 workgroups: with dropout 32768 x 1024 in 19.4 us, with
+    // one row a thread 21.9; 131072 x 8192 in 613, with one 775. Fewer workgroups have one (65521 rows of
+    // 100 4-bit columns: 8.8 us, with four 9.3). Rows that are not whole vectors would take one too
+    // (32768 x 1001: 38.1 us, with one 22.5), and 8-bit ones (50.7, with one 41.4).
     if (g.groups * g.slices >= 4096) {
         g.rows = 4;
         g.groups = (g.groups + 3) / 4;
