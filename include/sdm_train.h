@@ -157,10 +157,10 @@ int sdm_lookup(const void* bank, const void* scales, int bank_dtype, int64_t num
  * with a, and m the mask of columns that stay, as in sdm_lookup of the same idx, scale,
  * dropout and rng. Rows whose idx lies outside the bank add nothing, and their dout is not
  * read; neither is a dropped column's dout ever counted, whatever it holds. Sums are
- * float32, over at most 48 rows of a slot in ascending order. Where a slot has more, up to 17
- * such sums are added in their order in float32, and more of them in float64 and rounded to
- * float32. All of this is fixed by the call's sizes and idx: the same inputs give the same
- * bits. The result is rounded once to bank_dtype.
+ * float32, over at most 48 rows of a slot in ascending order. Where a slot has more, such sums
+ * are added in float32 in their order, of which there are at most 17 then, or, always where
+ * there are more, in float64 and rounded to float32. All of this is fixed by the call's sizes
+ * and idx: the same inputs give the same bits. The result is rounded once to bank_dtype.
  *
  * Arguments: as sdm_lookup, with
  *   n           0..SDM_MAX_GRAD_ENTRIES (0: dbank is zeroed, or left).

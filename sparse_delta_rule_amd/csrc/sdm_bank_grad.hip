@@ -720,7 +720,7 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(BankGradParams p, SumGrid
 
 // Runs over several blocks, 14 us for a most frequent token of 2100 in 32768: a chain of loads. A
 // workgroup looks at 64 blocks. Of the runs that begin there each lane group adds up some of the short
-// ones, in order; a long one's blocks are dealt out to all lane groups, each of which adds its own, and
+// ones that end there, in order; another's blocks are dealt out to all lane groups, each of which adds its own, and
 // then the groups' sums are added. As many as a batch has rows may come together there, so that these
 // additions are float64.
 constexpr int kJoinThreads = 1024;

@@ -390,6 +390,8 @@ def test_columns_in_turns(hd, kind):
     assert torch.equal(got.double(), 2 * want)
     large = sdm.sdm_gather_bank_grad(idx + 7, w, dout, T * W + 9, chunk=T, bank_dtype=torch.bfloat16)  # zeroed beside the sort
     assert torch.equal(large[7:71], want.to(torch.bfloat16)) and not large[:7].any() and not large[71:].any()
+    del large
+    torch.cuda.empty_cache()
 
 
 @pytest.mark.slow
@@ -407,6 +409,8 @@ def test_dropout_in_turns():
         one_hot[idx[at], torch.arange(1 << 17, device=DEV)] = 1
         want += (one_hot @ (mask[at] * dout[at]).float()).double()  # whole numbers, of less than 2^18
     assert torch.equal(got.double(), want)
+    del dout, mask
+    torch.cuda.empty_cache()
 
 
 def test_refusals():

@@ -156,6 +156,8 @@ def test_more_rows_than_a_grid_holds():
         keep = torch.tensor([[w >> 16 * (j % 2) & 0xffff for j in range(8) for w in [ref.philox((o, i, 6, 0), (5, 0))[j // 2]]]
                              for o in range(hd // 8)]).flatten() >= 1 << 15
         assert torch.equal(out[i].cpu().float(), torch.where(keep, 2.0 * (i % 4 + 1), 0.0) * (i % 4 < 3)), i
+    del out, rows
+    torch.cuda.empty_cache()
 
 
 def test_refusals():
